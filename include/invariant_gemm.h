@@ -309,6 +309,104 @@ int lora_apply(const ig_shape* shape, const void* x, void* y,
 int lora_shrink_noalloc(const ig_shape* shape, const void* x, const void* A_stack,
                         const int32_t* adapter_idx, float scale, float* z, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The block around the adapters: MX4 weights and activations, and the norms.
+ *
+ * A served layer is  y = x W^T + s (x A^T) B^T  between two norms. lora_apply
+ * adds the adapter term to a y that is already there; these calls make x, the
+ * quantised W and that y, and take y up into the residual stream. As with the
+ * LoRA calls, the bits of a row depend on that row, the weights and the sizes
+ * (K, N; H) only: never on M, the other rows, the row's place or the run.
+ *
+ * MX4: a matrix [rows][K] with the product's reduction along K, K a multiple
+ * of 32. Each 32 values of a row share one scale, held as an E8M0 byte b: the
+ * value 2^(b - 127), 255 = NaN. A value is a 4-bit E2M1 float: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 (codes 0-7) and their negatives (codes 8-15).
+ *   codes   uint8 [rows][K/2], the even k in bits 0-3, the odd k in bits 4-7
+ *   scales  uint8, ig_mx4_scale_bytes(rows, K) bytes: tiles of 512 bytes, one
+ *           per 128 rows x 128 k, tile (row / 128) * ceil(K / 128) + k / 128;
+ *           in a tile the byte of a block is at
+ *           (row % 32) * 16 + (row / 32 % 4) * 4 + k / 32 % 4.
+ *           Scale bytes of blocks past K are written as 127 by the calls
+ *           below and must be finite; those of rows past the last are
+ *           neither written nor of any effect.
+ * These calls keep the conventions above (device pointers, 16-byte alignment,
+ * enqueue only, argument errors before anything is enqueued); row strides
+ * (ld_*) are in elements and multiples of 8. An operator with no rows is a
+ * no-op.
+ * ------------------------------------------------------------------------ */
+typedef enum ig_type { IG_TYPE_BF16 = 0, IG_TYPE_F32 = 1 } ig_type;
+
+/* Bytes of the scales of a [rows][K] MX4 matrix; 0 for an invalid size. */
+size_t ig_mx4_scale_bytes(int64_t rows, int64_t K);
+
+/* x [rows][K] (bf16 or FP32) -> MX4. For a block with largest magnitude a the
+ * scale is 2^e, e = max(floor(log2 a) - 2, -127); each value is divided by it
+ * (exactly), rounded to the nearest E2M1 value, ties to the even code, and
+ * held at +-6 (magnitudes between 6 and 8 times the scale, at most a quarter
+ * off). A block that holds an infinity or a NaN gets the scale 255: all of it
+ * reads as NaN. */
+int ig_mx4_quantize(int64_t rows, int64_t K, const void* x, int64_t ld_x, int x_type,
+                    void* codes, void* scales, void* stream);
+
+/* The values an MX4 matrix stands for, rounded to the type of out
+ * [rows][K]. Every value ig_mx4_quantize can produce is exact in bf16. */
+int ig_mx4_dequantize(int64_t rows, int64_t K, const void* codes, const void* scales, void* out,
+                      int64_t ld_out, int out_type, void* stream);
+
+typedef struct ig_mx4_shape {
+  int64_t M;      /* tokens: rows of x and y */
+  int64_t N;      /* output features: rows of w (a multiple of 8) */
+  int64_t K;      /* reduction length (a multiple of 32) */
+  int64_t ld_y;   /* row stride of y */
+  int32_t y_type; /* ig_type */
+  int32_t flags;  /* 0 or IG_FLAG_STATIC_WEIGHTS (of w_codes and w_scales) */
+} ig_mx4_shape;
+
+/* Bytes of the workspace of ig_mx4_gemm: the status word and counters that a
+ * workspace begins with (see ig_workspace_init, ig_check_status). Any
+ * initialised workspace of the LoRA calls serves as it is; one of its own is
+ * these bytes, zeroed once. */
+size_t ig_mx4_workspace_bytes(void);
+
+/* y[m][n] = sum_k x[m][k] w[n][k], x [M][K] and w [N][K] in MX4: exact
+ * products, FP32 sums, one rounding to the type of y. A NaN scale makes the
+ * rows (of x) or columns (of w) that it touches NaN. */
+int ig_mx4_gemm(const ig_mx4_shape* shape, const void* x_codes, const void* x_scales,
+                const void* w_codes, const void* w_scales, void* y, void* ws, size_t ws_bytes,
+                void* stream);
+
+#define IG_NORM_WEIGHT_PLUS_ONE 1 /* norm weights are stored as w - 1 */
+
+typedef struct ig_norm_shape {
+  int64_t M;               /* rows */
+  int64_t H;               /* features: a multiple of 8, at most 32768 */
+  int64_t ld_h, ld_y, ld_h_out, ld_n; /* row strides of what is given */
+  int64_t gate_row_stride; /* 0: the same gate for every row */
+  int32_t gate_col_stride; /* 1, or 0: one gate value per row (then
+                              gate_row_stride may be any) */
+  int32_t h_type;          /* ig_type of h and h_out */
+  int32_t flags;           /* 0 or IG_NORM_WEIGHT_PLUS_ONE */
+  float eps;               /* >= 0 */
+  float scale;             /* residual scale */
+} ig_norm_shape;
+
+/* The norm after a block, its gate and residual scale, and the norm before
+ * the next block, in one pass over the row:
+ *   t  = y * rsqrt(mean(y^2) + eps) * w_post       (w_post NULL: t = y)
+ *   h' = h + scale * gate * t                      (gate NULL: 1; h NULL: 0;
+ *                                                   y NULL: h' = h)
+ *   n  = h' * rsqrt(mean(h'^2) + eps) * w_pre
+ * in FP32; h' goes to h_out (h_type; NULL: not wanted) and n, which is
+ * computed from the FP32 h', to n_out (bf16; NULL: not wanted). codes and
+ * scales (both or neither; H a multiple of 32) receive the bf16 n in MX4, the
+ * same bits as ig_mx4_quantize of n_out. w_pre is given if and only if one of
+ * n_out and codes is. y, gate, w_post and w_pre are bf16. h_out may be h, and
+ * n_out may be y (same strides). */
+int ig_block_norm(const ig_norm_shape* shape, const void* h, const void* y, const void* gate,
+                  const void* w_post, const void* w_pre, void* h_out, void* n_out, void* codes,
+                  void* scales, void* stream);
+
 /* Synchronise `stream`, read and clear the workspace status word, and return
  * the most severe device-side error recorded since the last check
  * (IG_ERR_TIMEOUT, IG_ERR_WS_CORRUPT, IG_ERR_ADAPTER_RANGE) or IG_OK. After

@@ -12,6 +12,8 @@ their data pointers are handed to the library unchanged. Layouts:
   z        f32   [slices][M][r]
   y        bf16  [M][slices*N]   (updated in place)
   idx      int32 [M]             (-1 = no adapter)
+The calls around the adapters (mx4_quantize, mx4_dequantize, mx4_gemm,
+block_norm) take their sizes and strides from the tensors and check them.
 """
 from __future__ import annotations
 
@@ -26,6 +28,8 @@ __all__ = [
     "plan_query", "workspace", "workspace_init", "map_tokens", "lora_shrink",
     "lora_expand", "lora_apply", "lora_shrink_noalloc", "check_status", "status_string",
     "EXPORTS",
+    "NORM_WEIGHT_PLUS_ONE", "Mx4Shape", "NormShape", "mx4_scale_bytes", "mx4_quantize",
+    "mx4_dequantize", "mx4_workspace", "mx4_gemm", "block_norm",
 ]
 
 MODE_DET, MODE_ATOMIC, MODE_UNSPLIT, MODE_DET_TREE = 0, 1, 2, 3
@@ -35,6 +39,7 @@ FLAG_Z_FP32 = 4
 FLAG_TEST_COPY_TIMEOUT = 8   # testing only: the first A-copy wait of each block expires
 FLAG_INPUT_READY = 16        # x not written by work still running on the stream
 PATH_AUTO, PATH_WARP, PATH_MMA, PATH_FMA = 0, 1, 2, 3
+NORM_WEIGHT_PLUS_ONE = 1     # block_norm: norm weights are stored as w - 1
 
 STATUS = {
     0: "IG_OK", -1: "IG_ERR_ARG", -2: "IG_ERR_SHAPE", -3: "IG_ERR_ALIGN",
@@ -46,7 +51,8 @@ STATUS = {
 EXPORTS = [
     "ig_version", "ig_status_string", "ig_workspace_bytes", "ig_plan_query",
     "ig_workspace_init", "ig_map_tokens", "lora_shrink", "lora_expand", "lora_apply",
-    "ig_check_status", "lora_shrink_noalloc",
+    "ig_check_status", "lora_shrink_noalloc", "ig_mx4_scale_bytes", "ig_mx4_workspace_bytes",
+    "ig_mx4_quantize", "ig_mx4_dequantize", "ig_mx4_gemm", "ig_block_norm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +85,23 @@ class PlanInfo(ctypes.Structure):
         ("shrink_tiles_max", ctypes.c_int64), ("shrink_ctas_max", ctypes.c_int64),
         ("workspace_bytes", ctypes.c_int64), ("determinism_key", ctypes.c_uint64),
         ("apply_kernels", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class Mx4Shape(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64), ("y_type", ctypes.c_int32), ("flags", ctypes.c_int32),
+    ]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("H", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64), ("ld_h_out", ctypes.c_int64), ("ld_n", ctypes.c_int64),
+        ("gate_row_stride", ctypes.c_int64), ("gate_col_stride", ctypes.c_int32),
+        ("h_type", ctypes.c_int32), ("flags", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -119,6 +142,20 @@ def lib() -> ctypes.CDLL:
         L.lora_shrink_noalloc.argtypes = [_SP, _P, _P, _P, ctypes.c_float, _P, _P]
         L.ig_check_status.restype = ctypes.c_int
         L.ig_check_status.argtypes = [_P, ctypes.c_size_t, _P]
+        i64 = ctypes.c_int64
+        L.ig_mx4_scale_bytes.restype = ctypes.c_size_t
+        L.ig_mx4_scale_bytes.argtypes = [i64, i64]
+        L.ig_mx4_workspace_bytes.restype = ctypes.c_size_t
+        L.ig_mx4_workspace_bytes.argtypes = []
+        L.ig_mx4_quantize.restype = ctypes.c_int
+        L.ig_mx4_quantize.argtypes = [i64, i64, _P, i64, ctypes.c_int, _P, _P, _P]
+        L.ig_mx4_dequantize.restype = ctypes.c_int
+        L.ig_mx4_dequantize.argtypes = [i64, i64, _P, _P, _P, i64, ctypes.c_int, _P]
+        L.ig_mx4_gemm.restype = ctypes.c_int
+        L.ig_mx4_gemm.argtypes = [ctypes.POINTER(Mx4Shape), _P, _P, _P, _P, _P, _P,
+                                  ctypes.c_size_t, _P]
+        L.ig_block_norm.restype = ctypes.c_int
+        L.ig_block_norm.argtypes = [ctypes.POINTER(NormShape)] + [_P] * 10
         _LIB = L
     return _LIB
 
@@ -222,3 +259,161 @@ def lora_shrink_noalloc(shape: Shape, x, A_stack, adapter_idx, scale, z, stream=
 def check_status(ws, stream=None) -> int:
     """Synchronise and return the device status (0 or a negative code)."""
     return int(lib().ig_check_status(_ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+# --- the block around the adapters: MX4 and the norms -------------------------
+#
+# Sizes and strides come from the tensors. A tensor of another type, size,
+# device or inner stride than its place asks for raises IGError (IG_ERR_ARG or
+# IG_ERR_SHAPE) before the library is called; the library checks the rest.
+
+def _rows(what, name, t, dev, dtypes, rows, cols):
+    """Checks a [rows][cols] operand with contiguous rows; its row stride."""
+    if t.dtype not in dtypes or t.device != dev:
+        raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise IGError(-2, f"{what}: {name} is {tuple(t.shape)}, ({rows}, {cols}) wanted")
+    ld, inner = t.stride()
+    if inner != 1 and cols != 1:
+        raise IGError(-2, f"{what}: {name} has strides ({ld}, {inner}), contiguous rows wanted")
+    return ld if rows > 1 else cols       # a single row's stride means nothing
+
+
+def _flat(what, name, t, dev, dtype, count):
+    """Checks a contiguous operand of at least `count` elements."""
+    if t.dtype != dtype or t.device != dev:
+        raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
+    if t.numel() < count or not t.is_contiguous():
+        raise IGError(-2, f"{what}: {name} has {t.numel()} elements, {count} contiguous wanted")
+
+
+def _packed(what, name, codes, scales, dev, rows, K):
+    """Checks the two tensors of a [rows][K] MX4 matrix."""
+    import torch
+    if codes.dtype != torch.uint8 or codes.device != dev:
+        raise IGError(-1, f"{what}: {name} codes are {codes.dtype} on {codes.device}")
+    if codes.dim() != 2 or codes.shape[0] != rows or codes.shape[1] * 2 != K or \
+            not codes.is_contiguous():
+        raise IGError(-2, f"{what}: {name} codes are {tuple(codes.shape)}, "
+                          f"({rows}, {K // 2}) contiguous wanted")
+    _flat(what, name + " scales", scales, dev, torch.uint8,
+          -(-rows // 128) * -(-K // 128) * 512)
+
+
+def _on(dev, stream):
+    """The stream of a call whose operands live on `dev`."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    if dev.type != "cuda":
+        raise IGError(-1, f"operands on {dev}")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def mx4_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the scales of a [rows][K] MX4 matrix."""
+    n = int(lib().ig_mx4_scale_bytes(rows, K))
+    if n == 0 and rows != 0:
+        raise IGError(-2, "ig_mx4_scale_bytes")
+    return n
+
+
+def mx4_quantize(x, codes, scales, stream=None):
+    """x [rows][K] (bf16 or FP32, rows may be strided) -> MX4: codes uint8
+    [rows][K/2] and scales, uint8 of mx4_scale_bytes(rows, K) elements."""
+    import torch
+    rows, K = x.shape
+    dev = x.device
+    ld = _rows("mx4_quantize", "x", x, dev, (torch.bfloat16, torch.float32), rows, K)
+    _packed("mx4_quantize", "x", codes, scales, dev, rows, K)
+    _check(lib().ig_mx4_quantize(rows, K, x.data_ptr(), ld, x.dtype == torch.float32,
+                                 codes.data_ptr(), scales.data_ptr(), _on(dev, stream)),
+           "mx4_quantize")
+
+
+def mx4_dequantize(codes, scales, out, stream=None):
+    """The values of an MX4 matrix into out [rows][K] (bf16 or FP32)."""
+    import torch
+    rows, K = out.shape
+    dev = out.device
+    ld = _rows("mx4_dequantize", "out", out, dev, (torch.bfloat16, torch.float32), rows, K)
+    _packed("mx4_dequantize", "input", codes, scales, dev, rows, K)
+    _check(lib().ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+                                   ld, out.dtype == torch.float32, _on(dev, stream)),
+           "mx4_dequantize")
+
+
+def mx4_workspace(device="cuda"):
+    """Allocate (with torch) a workspace for mx4_gemm. An initialised workspace
+    of the LoRA calls serves as well."""
+    import torch
+    return torch.zeros(int(lib().ig_mx4_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
+    """y [M][N] (bf16 or FP32) = x w^T, x [M][K] and w [N][K] in MX4. flags: 0 or
+    FLAG_STATIC_WEIGHTS."""
+    import torch
+    M, N = y.shape
+    K = 2 * x_codes.shape[-1]
+    dev = y.device
+    ld = _rows("mx4_gemm", "y", y, dev, (torch.bfloat16, torch.float32), M, N)
+    _packed("mx4_gemm", "x", x_codes, x_scales, dev, M, K)
+    _packed("mx4_gemm", "w", w_codes, w_scales, dev, N, K)
+    shape = Mx4Shape(M, N, K, ld, y.dtype == torch.float32, flags)
+    _check(lib().ig_mx4_gemm(ctypes.byref(shape), x_codes.data_ptr(), x_scales.data_ptr(),
+                             w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(),
+                             ws.data_ptr(), _nbytes(ws), _on(dev, stream)), "mx4_gemm")
+
+
+def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=1e-6,
+               h_out=None, n_out=None, codes=None, scales=None, flags=0, stream=None):
+    """t = rms_norm(y) w_post; h' = h + scale gate t; n = rms_norm(h') w_pre.
+
+    h [M][H] bf16 or FP32 (None: 0), y [M][H] bf16 (None: h' = h), gate bf16
+    that broadcasts to [M][H] from (H,), (1, H), (M, 1) or (M, H) (None: 1),
+    w_post and w_pre bf16 [H] (None: no such norm). h_out (may be h) receives
+    h', n_out n in bf16, codes and scales n in MX4; what is None is not
+    written. flags: 0 or NORM_WEIGHT_PLUS_ONE."""
+    import torch
+    what = "block_norm"
+    lead = h if h is not None else y
+    if lead is None:
+        raise IGError(-1, what + ": neither h nor y")
+    M, H = lead.shape
+    dev = lead.device
+    b16 = (torch.bfloat16,)
+    stream_type = h if h is not None else h_out
+    f32 = stream_type is not None and stream_type.dtype == torch.float32
+    h_types = (torch.float32,) if f32 else b16
+    s = NormShape(M, H, H, H, H, H, 0, 0, f32, flags, eps, scale)
+    if h is not None:
+        s.ld_h = _rows(what, "h", h, dev, h_types, M, H)
+    if y is not None:
+        s.ld_y = _rows(what, "y", y, dev, b16, M, H)
+    if h_out is not None:
+        s.ld_h_out = _rows(what, "h_out", h_out, dev, h_types, M, H)
+    if n_out is not None:
+        s.ld_n = _rows(what, "n_out", n_out, dev, b16, M, H)
+    if w_post is not None:
+        _flat(what, "w_post", w_post, dev, torch.bfloat16, H)
+    if w_pre is not None:
+        _flat(what, "w_pre", w_pre, dev, torch.bfloat16, H)
+    if gate is not None:
+        if gate.dtype != torch.bfloat16 or gate.device != dev:
+            raise IGError(-1, f"{what}: gate is {gate.dtype} on {gate.device}")
+        g = gate if gate.dim() == 2 else gate[None] if gate.dim() == 1 else None
+        if g is None or g.shape[0] not in (1, M) or g.shape[1] not in (1, H):
+            raise IGError(-2, f"{what}: gate is {tuple(gate.shape)}, which does not broadcast "
+                              f"to ({M}, {H})")
+        s.gate_row_stride = g.stride(0) if g.shape[0] > 1 else 0
+        s.gate_col_stride = int(g.shape[1] > 1 and g.stride(1) != 0)
+        if s.gate_col_stride and g.stride(1) != 1:
+            raise IGError(-2, f"{what}: gate has strides {g.stride()}, contiguous rows wanted")
+    if (codes is None) != (scales is None):
+        raise IGError(-1, what + ": codes and scales go together")
+    if codes is not None:
+        _packed(what, "n", codes, scales, dev, M, H)
+    _check(lib().ig_block_norm(ctypes.byref(s), _ptr(h), _ptr(y), _ptr(gate), _ptr(w_post),
+                               _ptr(w_pre), _ptr(h_out), _ptr(n_out), _ptr(codes), _ptr(scales),
+                               _on(dev, stream)), what)

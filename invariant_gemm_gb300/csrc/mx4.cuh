@@ -1,0 +1,145 @@
+// MX4 (blocks of 32 values along K, one E8M0 scale byte each, E2M1 codes):
+// what the quantiser, the block norm and the product share, and the launch
+// parameter blocks of the quantised-block operators.
+//
+// Codes: [rows][K/2] bytes, the even k in the low four bits. Scales: tiles of
+// 512 bytes, one per 128 rows x 4 blocks, [row % 32][row / 32 % 4][block % 4],
+// the tiles of a row group following each other along K. That is the order in
+// which tensor memory holds the scale factors of 128 rows x 128 k (32 lanes
+// of 16 bytes), so the product copies a tile as it stands.
+#pragma once
+
+#include "ig_common.cuh"
+
+namespace ig {
+
+constexpr int kMx4Block = 32;           // values per scale
+constexpr int kMx4TileBytes = 512;      // scale bytes of 128 rows x 128 k
+
+constexpr int64_t kNormMaxH = 32768;    // a row of the block norm stays in registers
+
+__host__ __device__ inline int64_t mx4_ktiles(int64_t K) { return (K + 127) / 128; }
+
+// Byte offset of the scale of (row, block kb); kt = mx4_ktiles(K).
+__host__ __device__ inline int64_t mx4_scale_at(int64_t row, int64_t kb, int64_t kt) {
+  return ((row >> 7) * kt + (kb >> 2)) * kMx4TileBytes + (row & 31) * 16 +
+         ((row >> 5) & 3) * 4 + (kb & 3);
+}
+
+struct Mx4QuantParams {
+  const void* x;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows, K, ldx, kt;
+};
+
+struct Mx4DequantParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* out;
+  int64_t rows, K, ldo, kt;
+};
+
+struct Mx4GemmParams {
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const uint8_t* wc;
+  const uint8_t* ws;
+  void* y;
+  int64_t M, N, K, ldy, kt;
+  int32_t y_f32;
+};
+
+struct NormParams {
+  const void* h;
+  const __nv_bfloat16* y;
+  const __nv_bfloat16* gate;
+  const __nv_bfloat16* w_post;
+  const __nv_bfloat16* w_pre;
+  void* h_out;
+  __nv_bfloat16* n_out;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows, H, ld_h, ld_y, ld_ho, ld_n, gate_rs, kt;
+  int32_t gate_cs, plus_one;
+  float eps, scale;
+};
+
+cudaError_t launch_mx4_quantize(const Mx4QuantParams& p, bool f32, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(const Mx4DequantParams& p, bool f32, cudaStream_t st);
+cudaError_t launch_mx4_gemm(const Mx4GemmParams& p, cudaStream_t st);
+cudaError_t launch_block_norm(const NormParams& p, bool h_f32, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// Eight FP32 values -> eight E2M1 codes, value i in bits 4i..4i+3 (nearest,
+// ties to even, held at +-6). Each conversion takes the high nibble first.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Eight codes -> the E2M1 values they stand for, without the scale. A code
+// seeem read as the bits s00000 00eem0.. of a bf16 is the value times 2^-126
+// (the code's exponent 0 is a subnormal there too), so one exact product by
+// 2^126 gives it.
+__device__ __forceinline__ void e2m1_values(uint32_t c, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t n = c >> (4 * i);
+    v[i] = __uint_as_float(((n & 8u) << 28) | ((n & 7u) << 22)) * 0x1p126f;
+  }
+}
+
+// 2^(byte - 127) as FP32; NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  const uint32_t bits = byte == 0 ? 0x00400000u : byte << 23;
+  return __uint_as_float(byte == 255 ? 0x7fc00000u : bits);
+}
+
+// Scale byte of a block whose largest magnitude has FP32 bits `top`
+// (non-negative; not below the bits of infinity for infinity and NaN):
+// exponent floor(log2 top) - 2, at least -127; 255 where the block has a
+// value that is not finite. A subnormal top has an exponent field of 0 and
+// falls under the lower limit like every top below 2^-124.
+__device__ __forceinline__ uint32_t e8m0_of(uint32_t top) {
+  if (top >= 0x7f800000u) return 255u;
+  const uint32_t e = top >> 23;      // floor(log2 top) + 127
+  return e > 2u ? e - 2u : 0u;
+}
+
+// The factor 2^-(byte - 127) that takes a block's values to code range; 0 for
+// a block of NaN (its codes are then 0).
+__device__ __forceinline__ float e8m0_inverse(uint32_t byte) {
+  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+
+// One thread's 8 values of a row (k = 8 t .. 8 t + 7 for lane t of an aligned
+// group of 4 lanes that hold one block): returns its codes, and the scale
+// byte of the block in all four lanes. Every lane of `mask` calls it.
+__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t& byte,
+                                                unsigned mask = 0xffffffffu) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(mask, top, 1));
+  top = max(top, __shfl_xor_sync(mask, top, 2));
+  byte = e8m0_of(top);
+  const float inv = e8m0_inverse(byte);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = byte == 255u ? 0.0f : v[i] * inv;
+  return e2m1x8(q);
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ig
