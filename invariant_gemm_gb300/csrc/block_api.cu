@@ -109,6 +109,8 @@ int ig_mx4_gemm(const ig_mx4_shape* shape, const void* x_codes, const void* x_sc
   p.ldy = shape->ld_y;
   p.kt = mx4_ktiles(shape->K);
   p.y_f32 = shape->y_type == IG_TYPE_F32;
+  p.flags = shape->flags;
+  p.status = static_cast<uint32_t*>(ws);
   return cuda_status(launch_mx4_gemm(p, static_cast<cudaStream_t>(stream)));
 }
 

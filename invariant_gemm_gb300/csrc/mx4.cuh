@@ -41,13 +41,18 @@ struct Mx4DequantParams {
 };
 
 struct Mx4GemmParams {
+  CUtensorMap tm_w;    // codes as [N][K / 4] 2-byte words, box 64 x 128, 128-byte swizzle
+  CUtensorMap tm_x;    // codes as [M][K / 4] 2-byte words, box 64 x BN, 128-byte swizzle
   const uint8_t* xc;
   const uint8_t* xs;
   const uint8_t* wc;
   const uint8_t* ws;
   void* y;
+  uint32_t* status;
   int64_t M, N, K, ldy, kt;
-  int32_t y_f32;
+  int64_t k_part;      // k per part: whole 256-k stages
+  int32_t S, ntiles;   // parts of K; 128-column tiles of N
+  int32_t y_f32, flags;
 };
 
 struct NormParams {
@@ -67,7 +72,7 @@ struct NormParams {
 
 cudaError_t launch_mx4_quantize(const Mx4QuantParams& p, bool f32, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams& p, bool f32, cudaStream_t st);
-cudaError_t launch_mx4_gemm(const Mx4GemmParams& p, cudaStream_t st);
+cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st);
 cudaError_t launch_block_norm(const NormParams& p, bool h_f32, cudaStream_t st);
 
 #ifdef __CUDACC__
