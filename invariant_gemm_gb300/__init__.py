@@ -267,47 +267,53 @@ def check_status(ws, stream=None) -> int:
 # device or inner stride than its place asks for raises IGError (IG_ERR_ARG or
 # IG_ERR_SHAPE) before the library is called; the library checks the rest.
 
-def _rows(what, name, t, dev, dtypes, rows, cols):
-    """Checks a [rows][cols] operand with contiguous rows; its row stride."""
-    if t.dtype not in dtypes or t.device != dev:
+def _rows(what, name, t, dev, dtype, rows, cols):
+    """Checks a [rows][cols] operand with contiguous rows on GPU `dev` (an
+    index); returns its row stride. A single row's stride means nothing."""
+    if t.dtype is not dtype or t.get_device() != dev:
         raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise IGError(-2, f"{what}: {name} is {tuple(t.shape)}, ({rows}, {cols}) wanted")
     ld, inner = t.stride()
     if inner != 1 and cols != 1:
         raise IGError(-2, f"{what}: {name} has strides ({ld}, {inner}), contiguous rows wanted")
-    return ld if rows > 1 else cols       # a single row's stride means nothing
+    return ld if rows > 1 else cols
 
 
 def _flat(what, name, t, dev, dtype, count):
     """Checks a contiguous operand of at least `count` elements."""
-    if t.dtype != dtype or t.device != dev:
+    if t.dtype is not dtype or t.get_device() != dev:
         raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
     if t.numel() < count or not t.is_contiguous():
         raise IGError(-2, f"{what}: {name} has {t.numel()} elements, {count} contiguous wanted")
 
 
-def _packed(what, name, codes, scales, dev, rows, K):
+def _packed(what, name, codes, scales, dev, u8, rows, K):
     """Checks the two tensors of a [rows][K] MX4 matrix."""
-    import torch
-    if codes.dtype != torch.uint8 or codes.device != dev:
+    if codes.dtype is not u8 or codes.get_device() != dev:
         raise IGError(-1, f"{what}: {name} codes are {codes.dtype} on {codes.device}")
-    if codes.dim() != 2 or codes.shape[0] != rows or codes.shape[1] * 2 != K or \
-            not codes.is_contiguous():
+    if K & 1 or codes.shape != (rows, K >> 1) or not codes.is_contiguous():
         raise IGError(-2, f"{what}: {name} codes are {tuple(codes.shape)}, "
                           f"({rows}, {K // 2}) contiguous wanted")
-    _flat(what, name + " scales", scales, dev, torch.uint8,
-          -(-rows // 128) * -(-K // 128) * 512)
+    _flat(what, name + " scales", scales, dev, u8, ((rows + 127) >> 7) * ((K + 127) >> 7) * 512)
 
 
-def _on(dev, stream):
-    """The stream of a call whose operands live on `dev`."""
-    if stream is not None:
-        return _stream(stream)
-    import torch
-    if dev.type != "cuda":
-        raise IGError(-1, f"operands on {dev}")
-    return torch.cuda.current_stream(dev).cuda_stream
+def _value_type(what, name, t, torch):
+    """ig_type of a bf16 or FP32 tensor."""
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    raise IGError(-1, f"{what}: {name} is {t.dtype}")
+
+
+def _on(dev, stream, torch):
+    """The stream of a call whose operands live on GPU `dev`."""
+    if dev < 0:
+        raise IGError(-1, "operands are not on a GPU")
+    # the current stream's handle without the Stream object around it, whose
+    # construction costs 2 us a call
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def mx4_scale_bytes(rows: int, K: int) -> int:
@@ -323,24 +329,28 @@ def mx4_quantize(x, codes, scales, stream=None):
     [rows][K/2] and scales, uint8 of mx4_scale_bytes(rows, K) elements."""
     import torch
     rows, K = x.shape
-    dev = x.device
-    ld = _rows("mx4_quantize", "x", x, dev, (torch.bfloat16, torch.float32), rows, K)
-    _packed("mx4_quantize", "x", codes, scales, dev, rows, K)
-    _check(lib().ig_mx4_quantize(rows, K, x.data_ptr(), ld, x.dtype == torch.float32,
-                                 codes.data_ptr(), scales.data_ptr(), _on(dev, stream)),
-           "mx4_quantize")
+    dev = x.get_device()
+    t = _value_type("mx4_quantize", "x", x, torch)
+    ld = _rows("mx4_quantize", "x", x, dev, x.dtype, rows, K)
+    _packed("mx4_quantize", "x", codes, scales, dev, torch.uint8, rows, K)
+    rc = (_LIB or lib()).ig_mx4_quantize(rows, K, x.data_ptr(), ld, t, codes.data_ptr(),
+                                         scales.data_ptr(), _on(dev, stream, torch))
+    if rc:
+        raise IGError(rc, "mx4_quantize")
 
 
 def mx4_dequantize(codes, scales, out, stream=None):
     """The values of an MX4 matrix into out [rows][K] (bf16 or FP32)."""
     import torch
     rows, K = out.shape
-    dev = out.device
-    ld = _rows("mx4_dequantize", "out", out, dev, (torch.bfloat16, torch.float32), rows, K)
-    _packed("mx4_dequantize", "input", codes, scales, dev, rows, K)
-    _check(lib().ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
-                                   ld, out.dtype == torch.float32, _on(dev, stream)),
-           "mx4_dequantize")
+    dev = out.get_device()
+    t = _value_type("mx4_dequantize", "out", out, torch)
+    ld = _rows("mx4_dequantize", "out", out, dev, out.dtype, rows, K)
+    _packed("mx4_dequantize", "input", codes, scales, dev, torch.uint8, rows, K)
+    rc = (_LIB or lib()).ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(),
+                                           out.data_ptr(), ld, t, _on(dev, stream, torch))
+    if rc:
+        raise IGError(rc, "mx4_dequantize")
 
 
 def mx4_workspace(device="cuda"):
@@ -356,14 +366,35 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
     import torch
     M, N = y.shape
     K = 2 * x_codes.shape[-1]
-    dev = y.device
-    ld = _rows("mx4_gemm", "y", y, dev, (torch.bfloat16, torch.float32), M, N)
-    _packed("mx4_gemm", "x", x_codes, x_scales, dev, M, K)
-    _packed("mx4_gemm", "w", w_codes, w_scales, dev, N, K)
-    shape = Mx4Shape(M, N, K, ld, y.dtype == torch.float32, flags)
-    _check(lib().ig_mx4_gemm(ctypes.byref(shape), x_codes.data_ptr(), x_scales.data_ptr(),
-                             w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(),
-                             ws.data_ptr(), _nbytes(ws), _on(dev, stream)), "mx4_gemm")
+    dev = y.get_device()
+    t = _value_type("mx4_gemm", "y", y, torch)
+    ld = _rows("mx4_gemm", "y", y, dev, y.dtype, M, N)
+    u8 = torch.uint8
+    _packed("mx4_gemm", "x", x_codes, x_scales, dev, u8, M, K)
+    _packed("mx4_gemm", "w", w_codes, w_scales, dev, u8, N, K)
+    _flat("mx4_gemm", "ws", ws, dev, u8, 0)
+    rc = (_LIB or lib()).ig_mx4_gemm(Mx4Shape(M, N, K, ld, t, flags), x_codes.data_ptr(),
+                                     x_scales.data_ptr(), w_codes.data_ptr(),
+                                     w_scales.data_ptr(), y.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), _on(dev, stream, torch))
+    if rc:
+        raise IGError(rc, "mx4_gemm")
+
+
+def _gate(what, gate, dev, torch, M, H):
+    """(row stride, column stride) of a gate that broadcasts to [M][H]."""
+    if gate.dtype is not torch.bfloat16 or gate.get_device() != dev:
+        raise IGError(-1, f"{what}: gate is {gate.dtype} on {gate.device}")
+    g = gate if gate.dim() == 2 else gate[None] if gate.dim() == 1 else None
+    if g is None or g.shape[0] not in (1, M) or g.shape[1] not in (1, H):
+        raise IGError(-2, f"{what}: gate is {tuple(gate.shape)}, which does not broadcast "
+                          f"to ({M}, {H})")
+    (rows, cols), (rs, cs) = g.shape, g.stride()
+    if cols == 1:
+        cs = 0
+    if cs not in (0, 1):
+        raise IGError(-2, f"{what}: gate has strides {g.stride()}, contiguous rows wanted")
+    return rs if rows > 1 else 0, cs
 
 
 def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=1e-6,
@@ -376,44 +407,45 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
     h', n_out n in bf16, codes and scales n in MX4; what is None is not
     written. flags: 0 or NORM_WEIGHT_PLUS_ONE."""
     import torch
-    what = "block_norm"
+    what, b16 = "block_norm", torch.bfloat16
     lead = h if h is not None else y
     if lead is None:
-        raise IGError(-1, what + ": neither h nor y")
+        raise IGError(-1, "block_norm: neither h nor y")
     M, H = lead.shape
-    dev = lead.device
-    b16 = (torch.bfloat16,)
-    stream_type = h if h is not None else h_out
-    f32 = stream_type is not None and stream_type.dtype == torch.float32
-    h_types = (torch.float32,) if f32 else b16
-    s = NormShape(M, H, H, H, H, H, 0, 0, f32, flags, eps, scale)
+    dev = lead.get_device()
+    res = h if h is not None else h_out
+    t = 0 if res is None else _value_type(what, "h", res, torch)
+    ld_h = ld_y = ld_ho = ld_n = H
+    ph = py = pg = p_post = p_pre = pho = pn = pc = ps = None
+    grs = gcs = 0
     if h is not None:
-        s.ld_h = _rows(what, "h", h, dev, h_types, M, H)
+        ld_h = _rows(what, "h", h, dev, h.dtype, M, H)
+        ph = h.data_ptr()
     if y is not None:
-        s.ld_y = _rows(what, "y", y, dev, b16, M, H)
+        ld_y = _rows(what, "y", y, dev, b16, M, H)
+        py = y.data_ptr()
     if h_out is not None:
-        s.ld_h_out = _rows(what, "h_out", h_out, dev, h_types, M, H)
+        ld_ho = _rows(what, "h_out", h_out, dev, res.dtype, M, H)
+        pho = h_out.data_ptr()
     if n_out is not None:
-        s.ld_n = _rows(what, "n_out", n_out, dev, b16, M, H)
+        ld_n = _rows(what, "n_out", n_out, dev, b16, M, H)
+        pn = n_out.data_ptr()
     if w_post is not None:
-        _flat(what, "w_post", w_post, dev, torch.bfloat16, H)
+        _flat(what, "w_post", w_post, dev, b16, H)
+        p_post = w_post.data_ptr()
     if w_pre is not None:
-        _flat(what, "w_pre", w_pre, dev, torch.bfloat16, H)
+        _flat(what, "w_pre", w_pre, dev, b16, H)
+        p_pre = w_pre.data_ptr()
     if gate is not None:
-        if gate.dtype != torch.bfloat16 or gate.device != dev:
-            raise IGError(-1, f"{what}: gate is {gate.dtype} on {gate.device}")
-        g = gate if gate.dim() == 2 else gate[None] if gate.dim() == 1 else None
-        if g is None or g.shape[0] not in (1, M) or g.shape[1] not in (1, H):
-            raise IGError(-2, f"{what}: gate is {tuple(gate.shape)}, which does not broadcast "
-                              f"to ({M}, {H})")
-        s.gate_row_stride = g.stride(0) if g.shape[0] > 1 else 0
-        s.gate_col_stride = int(g.shape[1] > 1 and g.stride(1) != 0)
-        if s.gate_col_stride and g.stride(1) != 1:
-            raise IGError(-2, f"{what}: gate has strides {g.stride()}, contiguous rows wanted")
-    if (codes is None) != (scales is None):
-        raise IGError(-1, what + ": codes and scales go together")
-    if codes is not None:
-        _packed(what, "n", codes, scales, dev, M, H)
-    _check(lib().ig_block_norm(ctypes.byref(s), _ptr(h), _ptr(y), _ptr(gate), _ptr(w_post),
-                               _ptr(w_pre), _ptr(h_out), _ptr(n_out), _ptr(codes), _ptr(scales),
-                               _on(dev, stream)), what)
+        grs, gcs = _gate(what, gate, dev, torch, M, H)
+        pg = gate.data_ptr()
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise IGError(-1, "block_norm: codes and scales go together")
+        _packed(what, "n", codes, scales, dev, torch.uint8, M, H)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
+    s = NormShape(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale)
+    rc = (_LIB or lib()).ig_block_norm(s, ph, py, pg, p_post, p_pre, pho, pn, pc, ps,
+                                       _on(dev, stream, torch))
+    if rc:
+        raise IGError(rc, what)

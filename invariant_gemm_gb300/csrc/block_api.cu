@@ -17,7 +17,7 @@ bool known_type(int t) { return t == IG_TYPE_BF16 || t == IG_TYPE_F32; }
 int check_mx4(int64_t rows, int64_t K) {
   if (rows < 0 || K < kMx4Block || K % kMx4Block) return IG_ERR_SHAPE;
   if (rows > (1ll << 31) - 1 || K > (1ll << 31) - 128) return IG_ERR_UNSUPPORTED;
-  if (rows > 0 && K > ((int64_t)1 << 46) / rows) return IG_ERR_UNSUPPORTED;
+  if (rows > 0 && K > ((int64_t)1 << 44) / rows) return IG_ERR_UNSUPPORTED;
   return IG_OK;
 }
 

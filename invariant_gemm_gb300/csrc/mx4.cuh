@@ -43,6 +43,7 @@ struct Mx4DequantParams {
 struct Mx4GemmParams {
   CUtensorMap tm_w;    // codes as [N][K / 4] 2-byte words, box 64 x 128, 128-byte swizzle
   CUtensorMap tm_x;    // codes as [M][K / 4] 2-byte words, box 64 x BN, 128-byte swizzle
+  CUtensorMap tm_ws, tm_xs;   // scale tiles as rows of 256 2-byte words, box 256 x 2 (pairs)
   const uint8_t* xc;
   const uint8_t* xs;
   const uint8_t* wc;
@@ -73,6 +74,7 @@ struct NormParams {
 cudaError_t launch_mx4_quantize(const Mx4QuantParams& p, bool f32, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(const Mx4DequantParams& p, bool f32, cudaStream_t st);
 cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st);
+cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st);
 cudaError_t launch_block_norm(const NormParams& p, bool h_f32, cudaStream_t st);
 
 #ifdef __CUDACC__

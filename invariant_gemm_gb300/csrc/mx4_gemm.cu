@@ -7,7 +7,7 @@
 //
 // K is cut into S parts of whole 256-k stages; S depends on (N, K) only. Each
 // part is one FP32 sum in tensor memory in increasing k, and the S sums are
-// added in increasing order, so that a row's bits do not depend on M.
+// added to 0 in increasing order, so that a row's bits do not depend on M.
 #include <algorithm>
 
 #include "mx4.cuh"
@@ -205,15 +205,11 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   if (n0 + n < p.N && ok) {
     for (int t = part * share + warp; t < min((part + 1) * share, tok); t += kThreads / 32) {
       const float* own = sums + t * kBM + n;
-      float4 v;
-      if (S == 1) {
-        v = *reinterpret_cast<const float4*>(own);
-      } else {
-        v = ld_cluster_v4(map_rank(own, 0));
-        for (int s = 1; s < S; ++s) {
-          const float4 u = ld_cluster_v4(map_rank(own, s));
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int s = 0; s < S; ++s) {
+        const float4 u = S == 1 ? *reinterpret_cast<const float4*>(own)
+                                : ld_cluster_v4(map_rank(own, s));
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
       }
       const int64_t at = (m0 + t) * p.ldy + n0 + n;
       if (p.y_f32)
@@ -265,6 +261,7 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   const int64_t per = (stages + S - 1) / S;
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
+  if (p.M > 512) return launch_mx4_gemm_pair(p, sm_count(), st);
   if (encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, kBM,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
     return cudaErrorInvalidValue;

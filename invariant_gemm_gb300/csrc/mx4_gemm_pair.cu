@@ -1,0 +1,374 @@
+// MX4 product for many tokens: the sums of mx4_gemm.cu, computed by pairs of
+// blocks that share each MMA (cta_group::2).
+//
+// A pair takes tiles of 256 output columns x 256 tokens, one after the other:
+// each of its two blocks holds 128 of the weight rows and 128 of the token
+// rows, so that shared memory is filled and read at 16 KB + 16 KB per 256 k
+// and block, where a block alone would need 16 KB + 32 KB for the same
+// products. Both blocks keep 128 x 256 sums in tensor memory.
+//
+// Warps: 0-15 take the sums out of tensor memory (32 lanes and a quarter of
+// the columns each), 16-19 put the scale factors there, 20 copies, 21 (of the
+// first block) issues the MMAs. The sums of a part of K go to registers at
+// once (64 a thread) and tensor memory is free again: the stores of a tile run
+// beside the products of the next.
+//
+// Scale factors go through registers (shared memory -> tcgen05.st) and not by
+// tcgen05.cp: a copy waits for the MMAs before it and holds up those after
+// it, which cost 40% of the products' time (646 against 1056 us at M = N =
+// 8192, K = 28672).
+#include "mx4.cuh"
+#include "umma_mx4.cuh"
+
+namespace ig {
+
+namespace {
+
+constexpr int kBN = 256;                 // output columns per tile (128 per block)
+constexpr int kBT = 256;                 // tokens per tile (128 rows of codes per block)
+constexpr int kBK = 256;                 // k per stage
+constexpr int kHalf = 128 * kBK / 2;     // codes of 128 rows
+constexpr int kStage = 2 * kHalf + 6 * kMx4TileBytes;   // w, x, w scales (2 tiles), x scales (4)
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 16;
+constexpr int kCols = kBT / (kEpiWarps / 4);   // token columns per warp
+constexpr int kSfWarp = kEpiWarps, kCopyWarp = kEpiWarps + 4, kMmaWarp = kEpiWarps + 5;
+constexpr int kThreads = 32 * (kEpiWarps + 6);
+constexpr uint32_t kSfCol = 256;         // tensor memory: sums 0-255, then scales
+constexpr uint32_t kSfCols = 8 + 16;     // per stage: w 2 x 4, x 2 x 8
+constexpr uint32_t kTmemCols = 512;
+constexpr int kGroup = 8;                // token tiles that run through the columns together
+
+struct Ctl {
+  uint64_t full[kStages];       // of the first block: the codes of both blocks
+  uint64_t sf_full[kStages];    // own: the scale tiles
+  uint64_t sf_ready[kStages];   // of the first block: scales of both in tensor memory
+  uint64_t empty[kStages];      // own: the MMAs that read the stage are done
+  uint64_t sums_full;           // own: a part's sums are complete
+  uint64_t sums_empty;          // of the first block: all warps have taken them out
+  uint32_t tmem;
+  int32_t fail;
+};
+
+constexpr size_t kSmem = 2048 + (size_t)kStages * kStage;
+
+// A stage of the ring and the parity of its barriers' current phase.
+struct Slot {
+  uint32_t s = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_mx4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb),
+        "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// One arrival on the barrier of both blocks of the pair once all earlier
+// tcgen05 operations of this thread have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+
+// Arrival on a barrier of either block. It orders tensor memory (with the
+// fences around it), not shared or global memory: nothing but tensor memory is
+// handed over, and the cluster-wide release would make the warp wait for its
+// stores.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// 8 consecutive FP32 columns of this thread's lane (see tmem_ld32).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 8 columns of this thread's lane <- two 16-byte vectors.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                 "r"(b.z), "r"(b.w) : "memory");
+}
+
+struct Tile {
+  int n0, m0;
+};
+
+// Tile i: token tiles in groups of kGroup; within a group all column tiles,
+// each with the group's token tiles, so that the pairs at work at a time share
+// both operands in L2.
+__device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t nt, uint32_t mt) {
+  const uint32_t per = kGroup * nt;
+  const uint32_t g = i / per, r = i - g * per;
+  const uint32_t gm = min((uint32_t)kGroup, mt - g * kGroup);
+  const uint32_t n = r / gm;
+  return {(int)(n * kBN), (int)((g * kGroup + (r - n * gm)) * kBT)};
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ Mx4GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem);
+  uint8_t* ring = smem + 1024;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t nt = (uint32_t)((p.N + kBN - 1) / kBN), mt = (uint32_t)((p.M + kBT - 1) / kBT);
+  const uint32_t tiles = nt * mt, pairs = gridDim.x / 2;
+  const int64_t stages_all = (p.K + kBK - 1) / kBK, per_part = p.k_part / kBK;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->sf_full[i], 1);
+      mbar_init(&ctl->sf_ready[i], 2 * 4);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    mbar_init(&ctl->sums_full, 1);
+    mbar_init(&ctl->sums_empty, 2 * kEpiWarps);
+    ctl->fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&ctl->tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();        // barriers of both blocks are ready, both have their tensor memory
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  griddep_wait();
+  griddep_launch();
+
+  // this pair's tiles, and their stages one after the other
+  const uint32_t first = blockIdx.x / 2;
+  const int64_t total = first < tiles ? (int64_t)((tiles - first - 1) / pairs + 1) * stages_all : 0;
+
+  if (warp == kCopyWarp) {
+    if (lane == 0) {
+      prefetch_tensormap(&p.tm_w);
+      prefetch_tensormap(&p.tm_x);
+      prefetch_tensormap(&p.tm_ws);
+      prefetch_tensormap(&p.tm_xs);
+      Slot at;
+      bool ok = true;
+      for (uint32_t i = first; i < tiles && ok; i += pairs) {
+        const Tile t = tile_at(i, nt, mt);
+        const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
+        // scale tiles, as rows of the maps; rows past the last one (of rows of
+        // the operands that do not exist) are filled with zeros
+        const int ws_row = (wr >> 7) * (int)p.kt, xs_row = (t.m0 >> 7) * (int)p.kt;
+        for (int64_t kb = 0; kb < stages_all; ++kb, at.next()) {
+          // a stage's first use finds its barrier in the phase before: parity 1 passes
+          if (!mbar_wait_bounded(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 4 * kHalf);
+          const uint32_t bar = map_rank(&ctl->full[at.s], 0);
+          uint8_t* st = ring + at.s * kStage;
+          tma_load_pair(st, &p.tm_w, (int)kb * 64, wr, bar);
+          tma_load_pair(st + kHalf, &p.tm_x, (int)kb * 64, xr, bar);
+          uint8_t* sf = st + 2 * kHalf;
+          const int k2 = 2 * (int)kb;
+          mbar_arrive_expect_tx(&ctl->sf_full[at.s], 6 * kMx4TileBytes);
+          tma_load_2d(sf, &p.tm_ws, 0, ws_row + k2, &ctl->sf_full[at.s]);
+          tma_load_2d(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xs_row + k2, &ctl->sf_full[at.s]);
+          tma_load_2d(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xs_row + (int)p.kt + k2,
+                      &ctl->sf_full[at.s]);
+        }
+      }
+      if (!ok) ctl->fail = 1;
+    }
+  } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
+    // a lane holds row `lane` of a tile (16 bytes: 4 rows of the operand x 4
+    // blocks) and stores it to its lane of this warp's partition
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    Slot at;
+    bool ok = true;
+    for (int64_t it = 0; it < total; ++it, at.next()) {
+      if (!mbar_wait_bounded(&ctl->sf_full[at.s], at.parity, p.status)) {
+        ok = false;
+        break;
+      }
+      const uint4* sf =
+          reinterpret_cast<const uint4*>(ring + at.s * kStage + 2 * kHalf) + lane;
+      constexpr int kT = kMx4TileBytes / 16;
+      const uint32_t dst = tmem + kSfCol + at.s * kSfCols + lanes;
+      tmem_st8(dst, sf[0], sf[kT]);
+      tmem_st8(dst + 8, sf[2 * kT], sf[4 * kT]);     // k 0-127: tokens 0-127, 128-255
+      tmem_st8(dst + 16, sf[3 * kT], sf[5 * kT]);    // k 128-255
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(&ctl->sf_ready[at.s], 0));
+    }
+    if (!ok && lane == 0) ctl->fail = 1;
+  } else if (warp == kMmaWarp) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc0 = umma_idesc_mx4(256, kBT);
+      constexpr uint32_t idesc1 = umma_idesc_sf(idesc0, 2);
+      const uint64_t wd = umma_desc_sw128(smem_u32(ring)), xd = umma_desc_sw128(smem_u32(ring) + kHalf);
+      Slot at;
+      int64_t kb = 0, part_end = 0;
+      uint32_t part = 0;
+      bool ok = true;
+      for (int64_t it = 0; it < total; ++it, at.next()) {
+        const bool begin = kb == part_end || kb == 0;
+        if (begin) {
+          part_end = min(stages_all, kb + per_part);
+          ok = part == 0 || mbar_wait_bounded(&ctl->sums_empty, (part - 1) & 1, p.status);
+        }
+        ok = ok && mbar_wait_bounded(&ctl->sf_ready[at.s], at.parity, p.status) &&
+             mbar_wait_bounded(&ctl->full[at.s], at.parity, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);
+        const uint32_t sfa = tmem + kSfCol + at.s * kSfCols, sfb = sfa + 8;
+        const int64_t rem = p.K - kb * kBK;
+        umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
+        if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
+        if (rem > 128) umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
+        if (rem > 192) umma_mx4_pair(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 8, true);
+        umma_commit_pair(&ctl->empty[at.s]);
+        if (++kb == part_end) {
+          umma_commit_pair(&ctl->sums_full);
+          ++part;
+          if (kb == stages_all) kb = 0;
+        }
+      }
+      if (!ok) ctl->fail = 1;
+    }
+  } else {
+    const uint32_t empty = map_rank(&ctl->sums_empty, 0);
+    const int c0 = (warp >> 2) * kCols;                 // this warp's token columns
+    const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+    uint32_t part = 0;
+    bool ok = true;
+    for (uint32_t i = first; i < tiles && ok; i += pairs) {
+      const Tile t = tile_at(i, nt, mt);
+      float acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+      for (int64_t kb0 = 0; kb0 < stages_all; kb0 += per_part, ++part) {
+        if (!mbar_wait_bounded(&ctl->sums_full, part & 1, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c) {
+          float v[8];
+          tmem_ld8(src + 8 * c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[8 * c + j] += v[j];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty);
+      }
+      if (!ok) break;
+      const int64_t n = t.n0 + 128 * (int)rank + (warp & 3) * 32;
+      const int64_t m = t.m0 + c0;
+      // the row stride, opaque to the compiler: multiples of it that are kept
+      // over tiles would cost the registers that hold the sums
+      int64_t ld = p.ldy;
+      asm volatile("" : "+l"(ld));
+      const int left = (int)min((int64_t)kCols, p.M - m);    // tokens of these columns
+      if (p.y_f32) {
+        float* y = static_cast<float*>(p.y) + m * ld + n + lane;
+        if (n + lane < p.N) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j < left) y[j * ld] = acc[j];
+        }
+      } else {
+        // lanes 2 l, 2 l + 1 trade values, so that each stores two columns of
+        // one token: the even lane of token j, the odd lane of token j + 1
+        const bool odd = lane & 1;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (m + odd) * ld + n + (lane & ~1);
+        const bool in = n + lane < p.N;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 2) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? acc[j] : acc[j + 1], 1);
+          const uint32_t v = odd ? f32x2_to_bf16x2_bits(got, acc[j + 1])
+                                 : f32x2_to_bf16x2_bits(acc[j], got);
+          if (in && j + odd < left) *reinterpret_cast<uint32_t*>(y + j * ld) = v;
+        }
+      }
+    }
+    if (!ok && lane == 0) ctl->fail = 1;
+  }
+  __syncthreads();
+  if (ctl->fail && tid == 0)
+    // a wait ran out: give copies in flight time to land before leaving
+    for (int s = 0; s < kStages; ++s)
+      for (int ph = 0; ph < 2; ++ph) {
+        if (rank == 0) mbar_wait_bounded(&ctl->full[s], ph, p.status, 1ll << 28);
+        mbar_wait_bounded(&ctl->sf_full[s], ph, p.status, 1ll << 28);
+      }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                 ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st) {
+  const uint64_t words = (uint64_t)p.K / 4, row = (uint64_t)p.K / 2;
+  const uint64_t wt = (uint64_t)((p.N + 127) / 128 * p.kt), xt = (uint64_t)((p.M + 127) / 128 * p.kt);
+  if (encode_map_2d(&p.tm_x, p.xc, (uint64_t)p.M, words, row, 64, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK ||
+      encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, words, row, 64, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK ||
+      encode_map_2d(&p.tm_ws, p.ws, wt, 256, kMx4TileBytes, 256, 2,
+                    CU_TENSOR_MAP_SWIZZLE_NONE) != IG_OK ||
+      encode_map_2d(&p.tm_xs, p.xs, xt, 256, kMx4TileBytes, 256, 2,
+                    CU_TENSOR_MAP_SWIZZLE_NONE) != IG_OK)
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (p.N + kBN - 1) / kBN * ((p.M + kBT - 1) / kBT);
+  if (tiles > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_pdl(gemm_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, st, p);
+}
+
+}  // namespace ig

@@ -25,7 +25,7 @@ __host__ __device__ constexpr uint32_t umma_idesc_mx4(int m, int n) {
          | (1u << 23)                    // scale format: E8M0
          | ((uint32_t)(m >> 7) << 27);   // M / 128
 }
-__device__ __forceinline__ uint32_t umma_idesc_sf(uint32_t idesc, uint32_t sf) {
+__host__ __device__ constexpr uint32_t umma_idesc_sf(uint32_t idesc, uint32_t sf) {
   return idesc | (sf << 4) | (sf << 29);
 }
 
