@@ -94,22 +94,32 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// Eight codes -> the E2M1 values they stand for, without the scale. A code
-// seeem read as the bits s00000 00eem0.. of a bf16 is the value times 2^-126
-// (the code's exponent 0 is a subnormal there too), so one exact product by
-// 2^126 gives it.
-__device__ __forceinline__ void e2m1_values(uint32_t c, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t n = c >> (4 * i);
-    v[i] = __uint_as_float(((n & 8u) << 28) | ((n & 7u) << 22)) * 0x1p126f;
-  }
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(f32x2_to_bf16x2_bits(f[0], f[1]), f32x2_to_bf16x2_bits(f[2], f[3]),
+                    f32x2_to_bf16x2_bits(f[4], f[5]), f32x2_to_bf16x2_bits(f[6], f[7]));
 }
 
-// 2^(byte - 127) as FP32; NaN for 255.
-__device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  const uint32_t bits = byte == 0 ? 0x00400000u : byte << 23;
-  return __uint_as_float(byte == 255 ? 0x7fc00000u : bits);
+// Eight codes -> the E2M1 values they stand for times 2^(byte - 127), two
+// bf16 to a word, all exact. A code seem read as the bf16 bits s0000000 eem0..
+// is its value times 2^-126 (the code's exponent 0 is a subnormal there too);
+// a product by 2^126, then one by the scale (2^-127 is a subnormal bf16).
+__device__ __forceinline__ uint4 mx4_decode8(uint32_t c, uint32_t byte) {
+  const uint32_t bits = byte == 0 ? 0x0040u : byte == 255 ? 0x7fc0u : byte << 7;
+  const uint32_t one = 0x7e807e80u, scale = bits | bits << 16;
+  const uint32_t odd = c >> 4;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // byte i of c in the low half, byte i of c >> 4 in the high one
+    const uint32_t u = __byte_perm(c, odd, i | i << 4 | (4 + i) << 8 | (4 + i) << 12);
+    const uint32_t w = (u << 12 & 0x80008000u) | (u << 6 & 0x01c001c0u);
+    __nv_bfloat162 v;
+    *reinterpret_cast<uint32_t*>(&v) = w;
+    v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&one));
+    v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&scale));
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Scale byte of a block whose largest magnitude has FP32 bits `top`
@@ -123,28 +133,52 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t top) {
   return e > 2u ? e - 2u : 0u;
 }
 
-// The factor 2^-(byte - 127) that takes a block's values to code range; 0 for
-// a block of NaN (its codes are then 0).
+// The factor 2^-(byte - 127) that takes a block's values to code range (of no
+// use for 255).
 __device__ __forceinline__ float e8m0_inverse(uint32_t byte) {
-  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+  return __uint_as_float((254u - byte) << 23);
 }
 
-// One thread's 8 values of a row (k = 8 t .. 8 t + 7 for lane t of an aligned
-// group of 4 lanes that hold one block): returns its codes, and the scale
-// byte of the block in all four lanes. Every lane of `mask` calls it.
-__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t& byte,
-                                                unsigned mask = 0xffffffffu) {
-  uint32_t top = 0;
+// Largest magnitude of one thread's 8 values as FP32 bits, the bits of
+// infinity or more where one is not finite.
+__device__ __forceinline__ uint32_t top_of(const uint4& b16) {
+  const uint32_t m = 0x7fff7fffu;     // bf16 magnitudes compare as integers
+  const uint32_t t = __vmaxu2(__vmaxu2(b16.x & m, b16.y & m), __vmaxu2(b16.z & m, b16.w & m));
+  return max(t << 16, t & 0xffff0000u);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
+  float t = fabsf(v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(mask, top, 1));
-  top = max(top, __shfl_xor_sync(mask, top, 2));
+  for (int i = 1; i < 8; ++i) t = max_nan(t, fabsf(v[i]));
+  return __float_as_uint(t);
+}
+
+// One thread's 8 values v of a row (k = 8 t .. 8 t + 7 for lane t of an aligned
+// group of 4 lanes that hold one block) and their top_of: returns the codes,
+// and the scale byte of the block in all four lanes. Whole warps call it.
+__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t top,
+                                                uint32_t& byte) {
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   byte = e8m0_of(top);
   const float inv = e8m0_inverse(byte);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = byte == 255u ? 0.0f : v[i] * inv;
-  return e2m1x8(q);
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+  const uint32_t codes = e2m1x8(q);
+  return byte == 255u ? 0u : codes;
+}
+
+// The 4 scale bytes of 16 lanes (one block to 4 of them), in the first of the
+// 16. Whole warps call it.
+__device__ __forceinline__ uint32_t mx4_scale_word(uint32_t byte) {
+  byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 8;
+  return byte | __shfl_down_sync(0xffffffffu, byte, 8) << 16;
 }
 
 #endif  // __CUDACC__

@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  // The next kernel may start once every block is here: each has its tensor
+  // memory by then, so no early block can hold what one of these still needs.
+  griddep_launch();
 
   if (warp == 0 && lane == 0) {
     auto atoms = [&](int b) { return (int)min((int64_t)2, (k1 - k0 - (int64_t)b * kBK + 127) / 128); };
@@ -182,7 +185,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         mbar_wait_bounded(&ctl->full[b % NST], (uint32_t)((b / NST) & 1), p.status);
     __syncthreads();
   }
-  griddep_launch();
   tc_fence_after();
 
   // the part's sums -> shared memory [token][n], where the stages were
