@@ -53,6 +53,8 @@ struct Mx4GemmParams {
   int64_t M, N, K, ldy, kt;
   int64_t k_part;      // k per part: whole 256-k stages
   int32_t S, ntiles;   // parts of K; 128-column tiles of N
+  int32_t stages;      // of the ring (few tokens)
+  uint32_t tmem_cols;
   int32_t y_f32, flags;
 };
 

@@ -1,5 +1,5 @@
 // MX4 product: y[m][n] = sum_k x[m][k] w[n][k], both operands MX4 (mx4.cuh),
-// on the tcgen05 tensor cores.
+// on the tcgen05 tensor cores. This file: few tokens; mx4_gemm_pair.cu: many.
 //
 // The weights are the MMA's A operand (128 output columns n are its 128
 // rows), the tokens its B operand (BN of them), so that a decode batch of up
@@ -7,7 +7,20 @@
 //
 // K is cut into S parts of whole 256-k stages; S depends on (N, K) only. Each
 // part is one FP32 sum in tensor memory in increasing k, and the S sums are
-// added to 0 in increasing order, so that a row's bits do not depend on M.
+// added to 0 in increasing order, so that a row's bits do not depend on M. A
+// part is a block here, the S blocks of a tile a cluster: each sends its sums,
+// four tokens at a time, to the block that owns those tokens (the groups of
+// four go round the blocks) through distributed shared memory, and the owner
+// adds and stores them.
+//
+// With few tokens the weights' bytes bound it: nearly all of shared memory is
+// a ring of copies (17 KB of weights to a stage), and with
+// IG_FLAG_STATIC_WEIGHTS the ring is filled while the kernel before ends.
+//
+// Warps: 0-3 put scale factors into tensor memory and take the sums out, 4
+// copies the weights, 6 the tokens, 5 issues the MMAs. Two warps copy because a
+// thread takes about 60 cycles to issue a copy or an expected count: one alone
+// took 640 over a stage, which held a block at 46 GB/s.
 #include <algorithm>
 
 #include "mx4.cuh"
@@ -19,16 +32,19 @@ namespace {
 
 constexpr int kBM = 128;            // output columns (weight rows) per tile
 constexpr int kBK = 256;            // k per stage: 128-byte rows of codes
-constexpr int kThreads = 128;
+constexpr int kCopyWarp = 4, kMmaWarp = 5, kCopyXWarp = 6;
+constexpr int kThreads = 224;
 constexpr int kWBytes = kBM * kBK / 2;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 10;
 
 struct Ctl {
   uint64_t full[kMaxStages];
+  uint64_t sf_ready[kMaxStages];   // scales in tensor memory
   uint64_t empty[kMaxStages];
   uint64_t done;
+  uint64_t parts;      // the other blocks' sums (and the own ones) have come
   uint32_t tmem;
-  int32_t issued;      // stages filled by the producer
+  int32_t issued[2];   // stages filled: weights, tokens
   int32_t consumed;    // stages whose copies the MMA thread saw arrive
 };
 
@@ -38,42 +54,33 @@ __host__ __device__ constexpr int x_bytes(int bn) { return bn * kBK / 2; }
 __host__ __device__ constexpr int stage_bytes(int bn) {
   return kWBytes + x_bytes(bn) + 2 * kMx4TileBytes * (1 + sf_groups(bn));
 }
-__host__ __device__ constexpr int stage_pitch(int bn) { return (stage_bytes(bn) + 1023) / 1024 * 1024; }
-__host__ __device__ constexpr int stages_of(int bn) { return bn >= 256 ? 4 : bn >= 128 ? 5 : 4; }
-// tensor memory: the accumulator, then the scale factors of each stage
+// tensor memory: the sums, then the scale factors of each stage
 __host__ __device__ constexpr int sf_col(int bn) { return bn < 32 ? 32 : bn; }
 __host__ __device__ constexpr int sf_cols(int bn) { return 8 * (1 + sf_groups(bn)); }
-__host__ __device__ constexpr int tmem_cols(int bn) {
-  const int need = sf_col(bn) + stages_of(bn) * sf_cols(bn);
-  return need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
-}
-// the part's sums [BN tokens][128] FP32 take the place of the stages
-__host__ __device__ constexpr size_t smem_bytes(int bn) {
-  const size_t ring = (size_t)stages_of(bn) * stage_pitch(bn);
-  const size_t sums = (size_t)bn * kBM * 4;
-  return 2048 + (ring > sums ? ring : sums);
-}
-
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
+// The parts' sums [S][groups of four tokens of this owner][128][4] FP32: BN *
+// 512 bytes, a little more where S does not divide the groups. Beside the ring
+// for up to 64 tokens; else in its place once every block of the cluster is
+// through with it.
+__host__ __device__ constexpr bool own_sums(int bn) { return bn <= 64; }
+__host__ __device__ inline int share_of(int bn, int S) { return (bn / 4 + S - 1) / S; }
+__host__ __device__ inline int sums_bytes(int bn, int S) { return share_of(bn, S) * S * kBM * 16; }
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ Mx4GemmParams p) {
-  constexpr int NST = stages_of(BN), SG = sf_groups(BN);
+  constexpr int SG = sf_groups(BN);
+  constexpr int kStage = stage_bytes(BN);
+  static_assert(kStage % 1024 == 0, "swizzled tiles start at multiples of 1024 bytes");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem);
-  uint8_t* ring = smem + 1024;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int S = p.S;
+  const int S = p.S, NST = p.stages;
+  uint8_t* ring = smem + 1024;
+  float4* sums = reinterpret_cast<float4*>(own_sums(BN) ? ring + NST * kStage : ring);
 
   uint32_t bid = blockIdx.x;
-  const int part = (int)next_digit(bid, (uint32_t)S);
+  const int part = (int)next_digit(bid, (uint32_t)S);      // the block's rank in its cluster
   const int64_t n0 = (int64_t)next_digit(bid, (uint32_t)p.ntiles) * kBM;
   const int64_t m0 = (int64_t)bid * BN;
   const int64_t k0 = (int64_t)part * p.k_part;
@@ -81,164 +88,222 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   const int nk = (int)((k1 - k0 + kBK - 1) / kBK);
   const int tok = (int)min((int64_t)BN, p.M - m0);         // tokens of the tile
   const int groups = (tok + 127) / 128;                    // their scale row groups
+  const int share = share_of(BN, S);
+  const int quads = (tok + 3) / 4;                         // groups of four tokens
+  const int owned = quads > part ? (quads - part - 1) / S + 1 : 0;
 
   if (tid == 0) {
-    prefetch_tensormap(&p.tm_w);
-    prefetch_tensormap(&p.tm_x);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->full[i], 2);
+      mbar_init(&ctl->sf_ready[i], 4);
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->done, 1);
-    ctl->issued = ctl->consumed = 0;
+    mbar_init(&ctl->parts, 1);
+    ctl->issued[0] = ctl->issued[1] = ctl->consumed = 0;
     fence_mbar_init();
+    if (S > 1) mbar_arrive_expect_tx(&ctl->parts, (uint32_t)(S * owned * kBM * 16));
   }
-  if (warp == 1) {
-    tmem_alloc(&ctl->tmem, tmem_cols(BN));
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem, p.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  if (S > 1 && own_sums(BN)) cluster_arrive_relaxed();
   // The next kernel may start once every block is here: each has its tensor
   // memory by then, so no early block can hold what one of these still needs.
   griddep_launch();
 
-  if (warp == 0 && lane == 0) {
-    auto atoms = [&](int b) { return (int)min((int64_t)2, (k1 - k0 - (int64_t)b * kBK + 127) / 128); };
-    auto arm = [&](int b) {
-      mbar_arrive_expect_tx(&ctl->full[b % NST], (uint32_t)(kWBytes + x_bytes(BN) +
-                                                            atoms(b) * kMx4TileBytes * (1 + groups)));
-    };
-    auto load_w = [&](int b) {
-      uint8_t* st = ring + (b % NST) * stage_pitch(BN);
-      const int64_t k = k0 + (int64_t)b * kBK;
-      tma_load_2d(st, &p.tm_w, (int)(k / 4), (int)n0, &ctl->full[b % NST]);
-      bulk_g2s(st + kWBytes + x_bytes(BN),
-               p.ws + ((n0 / 128) * p.kt + k / 128) * kMx4TileBytes, atoms(b) * kMx4TileBytes,
-               &ctl->full[b % NST]);
-    };
-    auto load_x = [&](int b) {
-      uint8_t* st = ring + (b % NST) * stage_pitch(BN);
-      const int64_t k = k0 + (int64_t)b * kBK;
-      tma_load_2d(st + kWBytes, &p.tm_x, (int)(k / 4), (int)m0, &ctl->full[b % NST]);
-      for (int g = 0; g < groups; ++g)
-        bulk_g2s(st + kWBytes + x_bytes(BN) + 2 * kMx4TileBytes * (1 + g),
-                 p.xs + ((m0 / 128 + g) * p.kt + k / 128) * kMx4TileBytes,
-                 atoms(b) * kMx4TileBytes, &ctl->full[b % NST]);
-    };
-    const int first = min(nk, NST);
-    const bool early = (p.flags & IG_FLAG_STATIC_WEIGHTS) != 0;
-    for (int b = 0; b < first; ++b) {
-      arm(b);
-      if (early) load_w(b);
+  bool ok = true;
+  if (warp == kCopyWarp || warp == kCopyXWarp) {
+    // Whole warps go through the loop and one lane issues.
+    const bool leader = elect_one();
+    const bool w = warp == kCopyWarp;
+    const bool early = w && (p.flags & IG_FLAG_STATIC_WEIGHTS) != 0;
+    const CUtensorMap* map = w ? &p.tm_w : &p.tm_x;
+    const int row = (int)(w ? n0 : m0);
+    const int sfs = w ? 1 : groups;                       // groups of scale rows
+    const uint8_t* sf = (w ? p.ws : p.xs) + ((int64_t)(row >> 7) * p.kt + k0 / 128) * kMx4TileBytes;
+    const int64_t sf_pitch = p.kt * kMx4TileBytes;
+    const uint32_t bytes = w ? kWBytes : x_bytes(BN);
+    const int kc = (int)(k0 / 4);
+    const int ntile = (int)((k1 - k0 + 127) / 128);       // scale tiles of a group
+    if (leader) prefetch_tensormap(map);
+    if (!early) griddep_wait();
+    int b = 0, s = 0;
+    uint32_t parity = 1;      // a stage's first use finds its barrier in the phase before
+    for (; b < nk; ++b) {
+      if (!warp_wait(&ctl->empty[s], parity, p.status)) break;
+      if (leader) {
+        const uint32_t sfb = (2 * b + 1 < ntile ? 2 : 1) * kMx4TileBytes;
+        uint8_t* st = ring + s * kStage;
+        uint8_t* st_sf = st + kWBytes + x_bytes(BN);
+        mbar_arrive_expect_tx(&ctl->full[s], bytes + sfb * sfs);
+        tma_load_2d(w ? st : st + kWBytes, map, kc + b * 64, row, &ctl->full[s]);
+        bulk_g2s(w ? st_sf : st_sf + 2 * kMx4TileBytes, sf, sfb, &ctl->full[s]);
+        if (sfs == 2)
+          bulk_g2s(st_sf + 4 * kMx4TileBytes, sf + sf_pitch, sfb, &ctl->full[s]);
+        sf += 2 * kMx4TileBytes;
+      }
+      if (++s == NST) {
+        s = 0;
+        parity ^= 1;
+      }
+    }
+    if (leader) ctl->issued[w ? 0 : 1] = b;
+    __syncwarp();
+    griddep_wait();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t idesc0 = umma_idesc_mx4(kBM, BN), idesc1 = umma_idesc_sf(idesc0, 2);
+      const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
+                     xd = umma_desc_sw128(smem_u32(ring) + kWBytes);
+      int b = 0, s = 0;
+      uint32_t parity = 0;
+      for (; b < nk; ++b) {
+        if (!mbar_wait_bounded(&ctl->full[s], parity, p.status) ||
+            !mbar_wait_bounded(&ctl->sf_ready[s], parity, p.status))
+          break;
+        tc_fence_after();
+        const uint64_t w = wd + s * (kStage >> 4), x = xd + s * (kStage >> 4);
+        const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8;
+        const int64_t rem = k1 - k0 - (int64_t)b * kBK;
+        umma_mx4(tmem, w, x, idesc0, sfa, sfb, b > 0);
+        if (rem > 64) umma_mx4(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
+        if (rem > 128) umma_mx4(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 4 * SG, true);
+        if (rem > 192) umma_mx4(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 4 * SG, true);
+        umma_commit(&ctl->empty[s]);
+        if (++s == NST) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+      umma_commit(&ctl->done);
+      ctl->consumed = b;
+    }
+    __syncwarp();
+    griddep_wait();
+  } else {
+    int s = 0;
+    uint32_t parity = 0;
+    for (int b = 0; b < nk; ++b) {
+      if (!warp_wait(&ctl->full[s], parity, p.status)) break;
+      sf_to_tmem<SG>(tmem + sf_col(BN) + s * sf_cols(BN), ring + s * kStage + kWBytes + x_bytes(BN),
+                     warp, lane);
+      if (lane == 0) mbar_arrive(&ctl->sf_ready[s]);
+      if (++s == NST) {
+        s = 0;
+        parity ^= 1;
+      }
     }
     griddep_wait();
-    for (int b = 0; b < first; ++b) {
-      if (!early) load_w(b);
-      load_x(b);
-    }
-    int b = first;
-    for (; b < nk; ++b) {
-      if (!mbar_wait_bounded(&ctl->empty[b % NST], (uint32_t)((b / NST - 1) & 1), p.status)) break;
-      arm(b);
-      load_w(b);
-      load_x(b);
-    }
-    ctl->issued = b;
-  } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc = umma_idesc_mx4(kBM, BN);
-    int b = 0;
-    for (; b < nk; ++b) {
-      const int s = b % NST;
-      if (!mbar_wait_bounded(&ctl->full[s], (uint32_t)((b / NST) & 1), p.status)) break;
-      tc_fence_after();
-      const uint32_t wa = smem_u32(ring + s * stage_pitch(BN)), xa = wa + kWBytes;
-      const uint32_t sfs = xa + x_bytes(BN);
-      const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8;
-      const int64_t rem = k1 - k0 - (int64_t)b * kBK;
-      const int steps = (int)min((int64_t)4, (rem + 63) / 64);
-      for (int a = 0; a < (steps + 1) / 2; ++a) {
-        sf_tile_to_tmem(sfa + 4 * a, sf_tile_desc(sfs + a * kMx4TileBytes));
-        for (int g = 0; g < SG; ++g)
-          sf_tile_to_tmem(sfb + 4 * (a * SG + g),
-                          sf_tile_desc(sfs + (2 * (1 + g) + a) * kMx4TileBytes));
-      }
-      for (int i = 0; i < steps; ++i)
-        umma_mx4(tmem, umma_desc_sw128(wa + 32 * i), umma_desc_sw128(xa + 32 * i),
-                 umma_idesc_sf(idesc, 2 * (i & 1)), sfa + 4 * (i >> 1), sfb + 4 * SG * (i >> 1),
-                 b > 0 || i > 0);
-      umma_commit(&ctl->empty[s]);
-    }
-    umma_commit(&ctl->done);
-    ctl->consumed = b;
+    ok = warp_wait(&ctl->done, 0, p.status);
+    tc_fence_after();
   }
-  __syncwarp();
-  griddep_wait();
-  bool ok = mbar_wait_bounded(&ctl->done, 0, p.status);
+  if (!own_sums(BN)) {
+    // the sums take the place of the stages
+    __syncthreads();
+    if (S > 1) cluster_arrive_relaxed();
+  }
+  if (S > 1) cluster_wait();
+
+  if (warp < 4 && ok) {
+    int owner = 0, at = 0;
+    for (int c = 0; c < tok; c += 32) {
+      float v[32];
+      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        if (c + i >= tok) continue;
+        const float4 q = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (S == 1) {
+          sums[(c + i) / 4 * kBM + tid] = q;
+        } else {
+          st_async_v4(map_rank(sums + (part * share + at) * kBM + tid, owner), q,
+                      map_rank(&ctl->parts, owner));
+          if (++owner == S) {
+            owner = 0;
+            ++at;
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
   __syncthreads();
-  if (ctl->issued != nk || ctl->consumed != nk) {
-    ok = false;                       // a copy never came: wait for those in flight
+  if (warp == kMmaWarp) tmem_dealloc(tmem, p.tmem_cols);
+  if (ctl->issued[0] != nk || ctl->issued[1] != nk || ctl->consumed != nk) {
+    // a copy never came: wait for those in flight, store nothing
+    ok = false;
     if (tid == 0)
-      for (int b = ctl->consumed; b < ctl->issued; ++b)
-        mbar_wait_bounded(&ctl->full[b % NST], (uint32_t)((b / NST) & 1), p.status);
+      for (int b = 0; b < 2 * NST; ++b)
+        mbar_wait_bounded(&ctl->full[b % NST], b / NST, p.status, 1ll << 28);
     __syncthreads();
   }
-  tc_fence_after();
+  if (S > 1) ok = mbar_wait_bounded(&ctl->parts, 0, p.status) && ok;
 
-  // the part's sums -> shared memory [token][n], where the stages were
-  float* sums = reinterpret_cast<float*>(ring);
-  for (int c = 0; c < BN && c < tok; c += 32) {
-    float v[32];
-    tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (BN >= 32 || i < BN) sums[(c + i) * kBM + tid] = v[i];
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, tmem_cols(BN));
-  if (S > 1) cluster_sync_all();
-
-  // block `part` of the cluster adds up and stores its share of the tokens
-  const int share = (BN + S - 1) / S;
-  const int n = 4 * lane;
-  if (n0 + n < p.N && ok) {
-    for (int t = part * share + warp; t < min((part + 1) * share, tok); t += kThreads / 32) {
-      const float* own = sums + t * kBM + n;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int s = 0; s < S; ++s) {
-        const float4 u = S == 1 ? *reinterpret_cast<const float4*>(own)
-                                : ld_cluster_v4(map_rank(own, s));
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-      }
-      const int64_t at = (m0 + t) * p.ldy + n0 + n;
-      if (p.y_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
-      else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
-            make_uint2(f32x2_to_bf16x2_bits(v.x, v.y), f32x2_to_bf16x2_bits(v.z, v.w));
+  // the owner of four tokens adds their sums up in order and stores them
+  if (!__all_sync(0xffffffffu, ok)) return;
+  for (int u = warp; u < 4 * owned; u += kThreads / 32) {
+    const int g = u >> 2, n = (u & 3) * 32 + lane;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < S; ++s) {
+      const float4 t = sums[(s * share + g) * kBM + n];
+      v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+    }
+    const int t0 = 4 * (part + g * S);
+    const bool in = n0 + n < p.N;
+    if (p.y_f32) {
+      float* y = static_cast<float*>(p.y) + (m0 + t0) * p.ldy + n0 + n;
+      if (in) *y = v.x;
+      if (in && t0 + 1 < tok) y[p.ldy] = v.y;
+      if (in && t0 + 2 < tok) y[2 * p.ldy] = v.z;
+      if (in && t0 + 3 < tok) y[3 * p.ldy] = v.w;
+    } else {
+      // lanes 2 l, 2 l + 1 trade values: the even one stores both columns of
+      // tokens 0 and 2, the odd one of 1 and 3
+      const bool odd = lane & 1;
+      const float a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
+      const float b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
+      __nv_bfloat16* y =
+          static_cast<__nv_bfloat16*>(p.y) + (m0 + t0 + odd) * p.ldy + n0 + (n & ~1);
+      if (in && t0 + odd < tok)
+        *reinterpret_cast<uint32_t*>(y) =
+            odd ? f32x2_to_bf16x2_bits(a, v.y) : f32x2_to_bf16x2_bits(v.x, a);
+      if (in && t0 + 2 + odd < tok)
+        *reinterpret_cast<uint32_t*>(y + 2 * p.ldy) =
+            odd ? f32x2_to_bf16x2_bits(b, v.w) : f32x2_to_bf16x2_bits(v.z, b);
     }
   }
-  if (S > 1) cluster_sync_all();    // no block leaves while its sums are being read
 }
 
 template <int BN>
 cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
+  const int64_t grid = (p.M + BN - 1) / BN * p.ntiles * p.S;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  // The ring: all of shared memory where every block has an SM to itself, else
+  // half of it. Stages past the part's are of no use.
+  const int sums = sums_bytes(BN, p.S);
+  const int room = (grid <= sm_count() ? 220 : 110) * 1024 - (own_sums(BN) ? sums : 0);
+  const int64_t nk = p.k_part / kBK;
+  p.stages = (int32_t)std::min<int64_t>({kMaxStages, room / stage_bytes(BN), nk});
+  const int cols = sf_col(BN) + p.stages * sf_cols(BN);
+  p.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  const int ring = p.stages * stage_bytes(BN);
+  const int smem = 2048 + (own_sums(BN) ? ring + sums : std::max(ring, sums));
   auto kern = gemm_kernel<BN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem_bytes(BN));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   if (encode_map_2d(&p.tm_x, p.xc, (uint64_t)p.M, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, BN,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
     return cudaErrorInvalidValue;
-  const int64_t grid = (p.M + BN - 1) / BN * p.ntiles * p.S;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -259,7 +324,7 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   p.ntiles = (int32_t)((p.N + kBM - 1) / kBM);
   const int64_t stages = (p.K + kBK - 1) / kBK;
   int S = 1;
-  while (S < 8 && (int64_t)p.ntiles * S < 128 && stages >= 4 * S) S *= 2;
+  while (S < 8 && (int64_t)p.ntiles * S < 96 && stages >= 8 * S) S *= 2;
   const int64_t per = (stages + S - 1) / S;
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty

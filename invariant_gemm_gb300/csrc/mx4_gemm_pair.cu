@@ -8,15 +8,10 @@
 // products. Both blocks keep 128 x 256 sums in tensor memory.
 //
 // Warps: 0-15 take the sums out of tensor memory (32 lanes and a quarter of
-// the columns each), 16-19 put the scale factors there, 20 copies, 21 (of the
-// first block) issues the MMAs. The sums of a part of K go to registers at
+// the columns each), 16-19 put the scale factors there, 20 copies codes, 22
+// scales, 21 (of the first block) issues the MMAs. The sums of a part of K go to registers at
 // once (64 a thread) and tensor memory is free again: the stores of a tile run
 // beside the products of the next.
-//
-// Scale factors go through registers (shared memory -> tcgen05.st) and not by
-// tcgen05.cp: a copy waits for the MMAs before it and holds up those after
-// it, which cost 40% of the products' time (646 against 1056 us at M = N =
-// 8192, K = 28672).
 #include "mx4.cuh"
 #include "umma_mx4.cuh"
 
@@ -32,8 +27,9 @@ constexpr int kStage = 2 * kHalf + 6 * kMx4TileBytes;   // w, x, w scales (2 til
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 16;
 constexpr int kCols = kBT / (kEpiWarps / 4);   // token columns per warp
-constexpr int kSfWarp = kEpiWarps, kCopyWarp = kEpiWarps + 4, kMmaWarp = kEpiWarps + 5;
-constexpr int kThreads = 32 * (kEpiWarps + 6);
+constexpr int kSfWarp = kEpiWarps, kCopyWarp = kEpiWarps + 4, kMmaWarp = kEpiWarps + 5,
+              kCopySfWarp = kEpiWarps + 6;
+constexpr int kThreads = 32 * (kEpiWarps + 7);
 constexpr uint32_t kSfCol = 256;         // tensor memory: sums 0-255, then scales
 constexpr uint32_t kSfCols = 8 + 16;     // per stage: w 2 x 4, x 2 x 8
 constexpr uint32_t kTmemCols = 512;
@@ -114,13 +110,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 8 columns of this thread's lane <- two 16-byte vectors.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"r"(taddr), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                 "r"(b.z), "r"(b.w) : "memory");
-}
-
 struct Tile {
   int n0, m0;
 };
@@ -147,7 +136,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const uint32_t nt = (uint32_t)((p.N + kBN - 1) / kBN), mt = (uint32_t)((p.M + kBT - 1) / kBT);
   const uint32_t tiles = nt * mt, pairs = gridDim.x / 2;
-  const int64_t stages_all = (p.K + kBK - 1) / kBK, per_part = p.k_part / kBK;
+  // k-blocks (stages) of a tile and of a part of K
+  const int nkb = (int)((p.K + kBK - 1) / kBK), per_part = (int)(p.k_part / kBK);
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -176,65 +166,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // this pair's tiles, and their stages one after the other
   const uint32_t first = blockIdx.x / 2;
-  const int64_t total = first < tiles ? (int64_t)((tiles - first - 1) / pairs + 1) * stages_all : 0;
+  const int64_t total = first < tiles ? (int64_t)((tiles - first - 1) / pairs + 1) * nkb : 0;
 
+  // Copies: one warp for the codes, one for the scales, since a thread takes
+  // about 60 cycles to issue a copy or an expected count, and one alone would
+  // take longer over a stage than its MMAs do. Whole warps go through the
+  // loops and one lane issues.
   if (warp == kCopyWarp) {
-    if (lane == 0) {
-      prefetch_tensormap(&p.tm_w);
-      prefetch_tensormap(&p.tm_x);
-      prefetch_tensormap(&p.tm_ws);
-      prefetch_tensormap(&p.tm_xs);
-      Slot at;
-      bool ok = true;
-      for (uint32_t i = first; i < tiles && ok; i += pairs) {
-        const Tile t = tile_at(i, nt, mt);
-        const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
-        // scale tiles, as rows of the maps; rows past the last one (of rows of
-        // the operands that do not exist) are filled with zeros
-        const int ws_row = (wr >> 7) * (int)p.kt, xs_row = (t.m0 >> 7) * (int)p.kt;
-        for (int64_t kb = 0; kb < stages_all; ++kb, at.next()) {
-          // a stage's first use finds its barrier in the phase before: parity 1 passes
-          if (!mbar_wait_bounded(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
-            ok = false;
-            break;
-          }
+    const bool leader = elect_one();
+    const uint32_t bar0 = map_rank(ctl->full, 0);
+    bool ok = true;
+    Slot at;
+    for (uint32_t i = first; i < tiles && ok; i += pairs) {
+      const Tile t = tile_at(i, nt, mt);
+      const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
+      for (int kb = 0; kb < nkb; ++kb, at.next()) {
+        // a stage's first use finds its barrier in the phase before: parity 1 passes
+        if (!warp_wait(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 4 * kHalf);
-          const uint32_t bar = map_rank(&ctl->full[at.s], 0);
           uint8_t* st = ring + at.s * kStage;
-          tma_load_pair(st, &p.tm_w, (int)kb * 64, wr, bar);
-          tma_load_pair(st + kHalf, &p.tm_x, (int)kb * 64, xr, bar);
-          uint8_t* sf = st + 2 * kHalf;
-          const int k2 = 2 * (int)kb;
-          mbar_arrive_expect_tx(&ctl->sf_full[at.s], 6 * kMx4TileBytes);
-          tma_load_2d(sf, &p.tm_ws, 0, ws_row + k2, &ctl->sf_full[at.s]);
-          tma_load_2d(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xs_row + k2, &ctl->sf_full[at.s]);
-          tma_load_2d(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xs_row + (int)p.kt + k2,
-                      &ctl->sf_full[at.s]);
+          tma_load_pair(st, &p.tm_w, kb * 64, wr, bar0 + 8 * at.s);
+          tma_load_pair(st + kHalf, &p.tm_x, kb * 64, xr, bar0 + 8 * at.s);
         }
       }
-      if (!ok) ctl->fail = 1;
     }
+    if (!ok && leader) ctl->fail = 1;
+  } else if (warp == kCopySfWarp) {
+    const bool leader = elect_one();
+    const int kt = (int)p.kt;
+    bool ok = true;
+    Slot at;
+    for (uint32_t i = first; i < tiles && ok; i += pairs) {
+      const Tile t = tile_at(i, nt, mt);
+      // scale tiles, as rows of the maps; rows past the last one (of rows of
+      // the operands that do not exist) are filled with zeros
+      int wrow = ((t.n0 >> 7) + (int)rank) * kt, xrow = (t.m0 >> 7) * kt;
+      for (int kb = 0; kb < nkb; ++kb, at.next(), wrow += 2, xrow += 2) {
+        if (!warp_wait(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          uint8_t* sf = ring + at.s * kStage + 2 * kHalf;
+          mbar_arrive_expect_tx(&ctl->sf_full[at.s], 6 * kMx4TileBytes);
+          tma_load_2d(sf, &p.tm_ws, 0, wrow, &ctl->sf_full[at.s]);
+          tma_load_2d(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, &ctl->sf_full[at.s]);
+          tma_load_2d(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, &ctl->sf_full[at.s]);
+        }
+      }
+    }
+    if (!ok && leader) ctl->fail = 1;
   } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
-    // a lane holds row `lane` of a tile (16 bytes: 4 rows of the operand x 4
-    // blocks) and stores it to its lane of this warp's partition
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     Slot at;
     bool ok = true;
     for (int64_t it = 0; it < total; ++it, at.next()) {
-      if (!mbar_wait_bounded(&ctl->sf_full[at.s], at.parity, p.status)) {
+      if (!warp_wait(&ctl->sf_full[at.s], at.parity, p.status)) {
         ok = false;
         break;
       }
-      const uint4* sf =
-          reinterpret_cast<const uint4*>(ring + at.s * kStage + 2 * kHalf) + lane;
-      constexpr int kT = kMx4TileBytes / 16;
-      const uint32_t dst = tmem + kSfCol + at.s * kSfCols + lanes;
-      tmem_st8(dst, sf[0], sf[kT]);
-      tmem_st8(dst + 8, sf[2 * kT], sf[4 * kT]);     // k 0-127: tokens 0-127, 128-255
-      tmem_st8(dst + 16, sf[3 * kT], sf[5 * kT]);    // k 128-255
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tc_fence_before();
-      __syncwarp();
+      sf_to_tmem<2>(tmem + kSfCol + at.s * kSfCols, ring + at.s * kStage + 2 * kHalf, warp, lane);
       if (lane == 0) mbar_arrive_cluster(map_rank(&ctl->sf_ready[at.s], 0));
     }
     if (!ok && lane == 0) ctl->fail = 1;
@@ -244,13 +238,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc1 = umma_idesc_sf(idesc0, 2);
       const uint64_t wd = umma_desc_sw128(smem_u32(ring)), xd = umma_desc_sw128(smem_u32(ring) + kHalf);
       Slot at;
-      int64_t kb = 0, part_end = 0;
+      int kb = 0, part_end = 0;
       uint32_t part = 0;
       bool ok = true;
       for (int64_t it = 0; it < total; ++it, at.next()) {
         const bool begin = kb == part_end || kb == 0;
         if (begin) {
-          part_end = min(stages_all, kb + per_part);
+          part_end = min(nkb, kb + per_part);
           ok = part == 0 || mbar_wait_bounded(&ctl->sums_empty, (part - 1) & 1, p.status);
         }
         ok = ok && mbar_wait_bounded(&ctl->sf_ready[at.s], at.parity, p.status) &&
@@ -259,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);
         const uint32_t sfa = tmem + kSfCol + at.s * kSfCols, sfb = sfa + 8;
-        const int64_t rem = p.K - kb * kBK;
+        const int64_t rem = p.K - (int64_t)kb * kBK;
         umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
         if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
         if (rem > 128) umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
@@ -268,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++kb == part_end) {
           umma_commit_pair(&ctl->sums_full);
           ++part;
-          if (kb == stages_all) kb = 0;
+          if (kb == nkb) kb = 0;
         }
       }
       if (!ok) ctl->fail = 1;
@@ -284,8 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float acc[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-      for (int64_t kb0 = 0; kb0 < stages_all; kb0 += per_part, ++part) {
-        if (!mbar_wait_bounded(&ctl->sums_full, part & 1, p.status)) {
+      for (int kb0 = 0; kb0 < nkb; kb0 += per_part, ++part) {
+        if (!warp_wait(&ctl->sums_full, part & 1, p.status)) {
           ok = false;
           break;
         }

@@ -8,6 +8,12 @@
 // 32 c + l, in all four 32-lane partitions. The MMA of K step s (of the two in
 // those 128 k) takes bytes 2 s, 2 s + 1, chosen by the scale factor ID 2 s of
 // the instruction descriptor. 256 rows take 8 columns.
+//
+// The scale factors get there through registers (shared memory ->
+// tcgen05.st, by warps of their own) and not by tcgen05.cp: a copy waits for the
+// MMAs before it and holds up those after it, which cost the block-pair
+// kernel 40% of its time (646 us without the copies, 1056 with, at M = N =
+// 8192, K = 28672).
 #pragma once
 
 #include "umma.cuh"
@@ -29,22 +35,55 @@ __host__ __device__ constexpr uint32_t umma_idesc_sf(uint32_t idesc, uint32_t sf
   return idesc | (sf << 4) | (sf << 29);
 }
 
-// Descriptor of a 512-byte scale tile in shared memory: 32 rows of 16 bytes,
-// no swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sf_tile_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Scale tile, shared memory -> 4 columns of tensor memory, the 32 lanes
-// repeated in the four partitions. Ordered before later MMAs of the thread.
-__device__ __forceinline__ void sf_tile_to_tmem(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+
+// mbar_wait_bounded by a whole warp, with one answer for all its lanes (what
+// follows a wait here are warp-wide tcgen05 instructions).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status));
+}
+
+// 8 columns of this thread's lane <- two 16-byte vectors.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                 "r"(b.z), "r"(b.w) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Scale factors of a stage (256 k) from shared memory to tensor memory, by the
+// four warps of a warpgroup, each into its own 32 lanes: lane l of every
+// partition holds row l of each 512-byte tile. sf: 2 tiles of A, then 2 of
+// each of the G groups of 128 rows of B. Columns at dst: A, k 0-127 and
+// 128-255 (4 each); then B, all groups of k 0-127, all of k 128-255.
+template <int G>
+__device__ __forceinline__ void sf_to_tmem(uint32_t dst, const uint8_t* smem_sf, int warp,
+                                           int lane) {
+  constexpr int kTile = 512 / 16;
+  const uint4* sf = reinterpret_cast<const uint4*>(smem_sf) + lane;
+  dst += (uint32_t)((warp & 3) * 32) << 16;
+  tmem_st8(dst, sf[0], sf[kTile]);
+  if (G == 1) {
+    tmem_st8(dst + 8, sf[2 * kTile], sf[3 * kTile]);
+  } else {
+    tmem_st8(dst + 8, sf[2 * kTile], sf[4 * kTile]);
+    tmem_st8(dst + 16, sf[3 * kTile], sf[5 * kTile]);
+  }
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
 }
 
 // One block-scaled MMA (issued by a single thread): D = A B^T (+ D).
