@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   const int S = p.S, NST = p.stages;
   uint8_t* ring = smem + 1024;
   float4* sums = reinterpret_cast<float4*>(own_sums(BN) ? ring + NST * kStage : ring);
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = uniform(ctl->tmem);
   if (S > 1 && own_sums(BN)) cluster_arrive_relaxed();
   // The next kernel may start once every block is here: each has its tensor
   // memory by then, so no early block can hold what one of these still needs.
@@ -157,30 +157,34 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     __syncwarp();
     griddep_wait();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t idesc0 = umma_idesc_mx4(kBM, BN), idesc1 = umma_idesc_sf(idesc0, 2);
-      const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
-                     xd = umma_desc_sw128(smem_u32(ring) + kWBytes);
-      int b = 0, s = 0;
-      uint32_t parity = 0;
-      for (; b < nk; ++b) {
-        if (!mbar_wait_bounded(&ctl->full[s], parity, p.status) ||
-            !mbar_wait_bounded(&ctl->sf_ready[s], parity, p.status))
-          break;
-        tc_fence_after();
-        const uint64_t w = wd + s * (kStage >> 4), x = xd + s * (kStage >> 4);
-        const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8;
-        const int64_t rem = k1 - k0 - (int64_t)b * kBK;
+    constexpr uint32_t idesc0 = umma_idesc_mx4(kBM, BN), idesc1 = umma_idesc_sf(idesc0, 2);
+    const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
+                   xd = umma_desc_sw128(smem_u32(ring) + kWBytes);
+    const bool leader = elect_one();
+    int b = 0, s = 0;
+    uint32_t parity = 0;
+    for (; b < nk; ++b) {
+      if (!warp_wait(&ctl->full[s], parity, p.status) ||
+          !warp_wait(&ctl->sf_ready[s], parity, p.status))
+        break;
+      tc_fence_after();
+      const uint64_t w = wd + s * (kStage >> 4), x = xd + s * (kStage >> 4);
+      const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8;
+      const int rem = (int)min((int64_t)kBK, k1 - k0 - (int64_t)b * kBK);
+      if (leader) {
         umma_mx4(tmem, w, x, idesc0, sfa, sfb, b > 0);
         if (rem > 64) umma_mx4(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
         if (rem > 128) umma_mx4(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 4 * SG, true);
         if (rem > 192) umma_mx4(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 4 * SG, true);
         umma_commit(&ctl->empty[s]);
-        if (++s == NST) {
-          s = 0;
-          parity ^= 1;
-        }
       }
+      __syncwarp();
+      if (++s == NST) {
+        s = 0;
+        parity ^= 1;
+      }
+    }
+    if (leader) {
       umma_commit(&ctl->done);
       ctl->consumed = b;
     }

@@ -132,8 +132,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem);
   uint8_t* ring = smem + 1024;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
+  const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
+  const uint32_t rank = uniform(cluster_rank());
   const uint32_t nt = (uint32_t)((p.N + kBN - 1) / kBN), mt = (uint32_t)((p.M + kBT - 1) / kBT);
   const uint32_t tiles = nt * mt, pairs = gridDim.x / 2;
   // k-blocks (stages) of a tile and of a part of K
@@ -160,7 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();        // barriers of both blocks are ready, both have their tensor memory
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = uniform(ctl->tmem);
   griddep_wait();
   griddep_launch();
 
@@ -233,10 +233,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) ctl->fail = 1;
   } else if (warp == kMmaWarp) {
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc0 = umma_idesc_mx4(256, kBT);
-      constexpr uint32_t idesc1 = umma_idesc_sf(idesc0, 2);
-      const uint64_t wd = umma_desc_sw128(smem_u32(ring)), xd = umma_desc_sw128(smem_u32(ring) + kHalf);
+    if (rank == 0) {
+      constexpr uint32_t idesc0 = umma_idesc_mx4(256, kBT), idesc1 = umma_idesc_sf(idesc0, 2);
+      const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
+                     xd = umma_desc_sw128(smem_u32(ring) + kHalf);
+      const bool leader = elect_one();
       Slot at;
       int kb = 0, part_end = 0;
       uint32_t part = 0;
@@ -245,27 +246,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool begin = kb == part_end || kb == 0;
         if (begin) {
           part_end = min(nkb, kb + per_part);
-          ok = part == 0 || mbar_wait_bounded(&ctl->sums_empty, (part - 1) & 1, p.status);
+          ok = part == 0 || warp_wait(&ctl->sums_empty, (part - 1) & 1, p.status);
         }
-        ok = ok && mbar_wait_bounded(&ctl->sf_ready[at.s], at.parity, p.status) &&
-             mbar_wait_bounded(&ctl->full[at.s], at.parity, p.status);
+        ok = ok && warp_wait(&ctl->sf_ready[at.s], at.parity, p.status) &&
+             warp_wait(&ctl->full[at.s], at.parity, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);
         const uint32_t sfa = tmem + kSfCol + at.s * kSfCols, sfb = sfa + 8;
-        const int64_t rem = p.K - (int64_t)kb * kBK;
-        umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
-        if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
-        if (rem > 128) umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
-        if (rem > 192) umma_mx4_pair(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 8, true);
-        umma_commit_pair(&ctl->empty[at.s]);
-        if (++kb == part_end) {
-          umma_commit_pair(&ctl->sums_full);
+        const int rem = (int)min((int64_t)kBK, p.K - (int64_t)kb * kBK);
+        const bool end = kb + 1 == part_end;
+        if (leader) {
+          umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
+          if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
+          if (rem > 128) umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
+          if (rem > 192) umma_mx4_pair(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 8, true);
+          umma_commit_pair(&ctl->empty[at.s]);
+          if (end) umma_commit_pair(&ctl->sums_full);
+        }
+        __syncwarp();
+        ++kb;
+        if (end) {
           ++part;
           if (kb == nkb) kb = 0;
         }
       }
-      if (!ok) ctl->fail = 1;
+      if (!ok && leader) ctl->fail = 1;
     }
   } else {
     const uint32_t empty = map_rank(&ctl->sums_empty, 0);

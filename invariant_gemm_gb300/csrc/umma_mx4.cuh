@@ -39,6 +39,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A value that is the same in all lanes, known as such to the compiler. Copies
+// and MMAs take their operands from uniform registers: with a warp number,
+// loop counters and addresses that it can see to be uniform they are there
+// already, else each instruction is preceded by moves (75 cycles to an MMA
+// issued by `if (lane == 0)`).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
