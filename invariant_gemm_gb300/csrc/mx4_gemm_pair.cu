@@ -8,10 +8,10 @@
 // products. Both blocks keep 128 x 256 sums in tensor memory.
 //
 // Warps: 0-15 take the sums out of tensor memory (32 lanes and a quarter of
-// the columns each), 16-19 put the scale factors there, 20 copies codes, 22
-// scales, 21 (of the first block) issues the MMAs. The sums of a part of K go to registers at
-// once (64 a thread) and tensor memory is free again: the stores of a tile run
-// beside the products of the next.
+// the columns each), 16 copies codes, 17 scales, 18 (of the first block) issues
+// the MMAs. The sums of a part of K go to registers at once (64 a thread) and
+// tensor memory is free again: the stores of a tile run beside the products of
+// the next.
 #include "mx4.cuh"
 #include "umma_mx4.cuh"
 
@@ -27,18 +27,15 @@ constexpr int kStage = 2 * kHalf + 6 * kMx4TileBytes;   // w, x, w scales (2 til
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 16;
 constexpr int kCols = kBT / (kEpiWarps / 4);   // token columns per warp
-constexpr int kSfWarp = kEpiWarps, kCopyWarp = kEpiWarps + 4, kMmaWarp = kEpiWarps + 5,
-              kCopySfWarp = kEpiWarps + 6;
-constexpr int kThreads = 32 * (kEpiWarps + 7);
+constexpr int kCopyWarp = kEpiWarps, kCopySfWarp = kEpiWarps + 1, kMmaWarp = kEpiWarps + 2;
+constexpr int kThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kSfCol = 256;         // tensor memory: sums 0-255, then scales
 constexpr uint32_t kSfCols = 8 + 16;     // per stage: w 2 x 4, x 2 x 8
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGroup = 8;                // token tiles that run through the columns together
 
 struct Ctl {
-  uint64_t full[kStages];       // of the first block: the codes of both blocks
-  uint64_t sf_full[kStages];    // own: the scale tiles
-  uint64_t sf_ready[kStages];   // of the first block: scales of both in tensor memory
+  uint64_t full[kStages];       // of the first block: the copies of both blocks
   uint64_t empty[kStages];      // own: the MMAs that read the stage are done
   uint64_t sums_full;           // own: a part's sums are complete
   uint64_t sums_empty;          // of the first block: all warps have taken them out
@@ -66,6 +63,12 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
       ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
+}
+
+// Scale tile of each block's own shared memory -> its own tensor memory.
+__device__ __forceinline__ void sf_tile_to_tmem_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
 }
 
 __device__ __forceinline__ void umma_mx4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -141,9 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->sf_full[i], 1);
-      mbar_init(&ctl->sf_ready[i], 2 * 4);
+      mbar_init(&ctl->full[i], 2);
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->sums_full, 1);
@@ -197,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok && leader) ctl->fail = 1;
   } else if (warp == kCopySfWarp) {
     const bool leader = elect_one();
+    const uint32_t bar0 = map_rank(ctl->full, 0);
     const int kt = (int)p.kt;
     bool ok = true;
     Slot at;
@@ -212,31 +214,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (leader) {
           uint8_t* sf = ring + at.s * kStage + 2 * kHalf;
-          mbar_arrive_expect_tx(&ctl->sf_full[at.s], 6 * kMx4TileBytes);
-          tma_load_2d(sf, &p.tm_ws, 0, wrow, &ctl->sf_full[at.s]);
-          tma_load_2d(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, &ctl->sf_full[at.s]);
-          tma_load_2d(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, &ctl->sf_full[at.s]);
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 12 * kMx4TileBytes);
+          tma_load_pair(sf, &p.tm_ws, 0, wrow, bar0 + 8 * at.s);
+          tma_load_pair(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, bar0 + 8 * at.s);
+          tma_load_pair(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, bar0 + 8 * at.s);
         }
       }
     }
     if (!ok && leader) ctl->fail = 1;
-  } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
-    Slot at;
-    bool ok = true;
-    for (int64_t it = 0; it < total; ++it, at.next()) {
-      if (!warp_wait(&ctl->sf_full[at.s], at.parity, p.status)) {
-        ok = false;
-        break;
-      }
-      sf_to_tmem<2>(tmem + kSfCol + at.s * kSfCols, ring + at.s * kStage + 2 * kHalf, warp, lane);
-      if (lane == 0) mbar_arrive_cluster(map_rank(&ctl->sf_ready[at.s], 0));
-    }
-    if (!ok && lane == 0) ctl->fail = 1;
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
       constexpr uint32_t idesc0 = umma_idesc_mx4(256, kBT), idesc1 = umma_idesc_sf(idesc0, 2);
       const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
-                     xd = umma_desc_sw128(smem_u32(ring) + kHalf);
+                     xd = umma_desc_sw128(smem_u32(ring) + kHalf),
+                     sfd = sf_tile_desc(smem_u32(ring) + 2 * kHalf);
       const bool leader = elect_one();
       Slot at;
       int kb = 0, part_end = 0;
@@ -248,18 +239,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           part_end = min(nkb, kb + per_part);
           ok = part == 0 || warp_wait(&ctl->sums_empty, (part - 1) & 1, p.status);
         }
-        ok = ok && warp_wait(&ctl->sf_ready[at.s], at.parity, p.status) &&
-             warp_wait(&ctl->full[at.s], at.parity, p.status);
+        ok = ok && warp_wait(&ctl->full[at.s], at.parity, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);
         const uint32_t sfa = tmem + kSfCol + at.s * kSfCols, sfb = sfa + 8;
         const int rem = (int)min((int64_t)kBK, p.K - (int64_t)kb * kBK);
         const bool end = kb + 1 == part_end;
+        const uint64_t sf = sfd + at.s * (kStage >> 4);      // tiles w0 w1 x0 x0' x1 x1'
         if (leader) {
+          sf_tile_to_tmem_pair(sfa, sf);
+          sf_tile_to_tmem_pair(sfb, sf + 64);
+          sf_tile_to_tmem_pair(sfb + 4, sf + 128);
           umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
           if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
-          if (rem > 128) umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
+          if (rem > 128) {
+            sf_tile_to_tmem_pair(sfa + 4, sf + 32);
+            sf_tile_to_tmem_pair(sfb + 8, sf + 96);
+            sf_tile_to_tmem_pair(sfb + 12, sf + 160);
+            umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
+          }
           if (rem > 192) umma_mx4_pair(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 8, true);
           umma_commit_pair(&ctl->empty[at.s]);
           if (end) umma_commit_pair(&ctl->sums_full);
@@ -334,13 +333,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) ctl->fail = 1;
   }
   __syncthreads();
-  if (ctl->fail && tid == 0)
+  if (ctl->fail && rank == 0 && tid == 0)
     // a wait ran out: give copies in flight time to land before leaving
     for (int s = 0; s < kStages; ++s)
-      for (int ph = 0; ph < 2; ++ph) {
-        if (rank == 0) mbar_wait_bounded(&ctl->full[s], ph, p.status, 1ll << 28);
-        mbar_wait_bounded(&ctl->sf_full[s], ph, p.status, 1ll << 28);
-      }
+      for (int ph = 0; ph < 2; ++ph) mbar_wait_bounded(&ctl->full[s], ph, p.status, 1ll << 28);
   tc_fence_before();
   cluster_sync_all();
   if (warp == kMmaWarp)

@@ -8,12 +8,6 @@
 // 32 c + l, in all four 32-lane partitions. The MMA of K step s (of the two in
 // those 128 k) takes bytes 2 s, 2 s + 1, chosen by the scale factor ID 2 s of
 // the instruction descriptor. 256 rows take 8 columns.
-//
-// The scale factors get there through registers (shared memory ->
-// tcgen05.st, by warps of their own) and not by tcgen05.cp: a copy waits for the
-// MMAs before it and holds up those after it, which cost the block-pair
-// kernel 40% of its time (646 us without the copies, 1056 with, at M = N =
-// 8192, K = 28672).
 #pragma once
 
 #include "umma.cuh"
@@ -60,6 +54,24 @@ __device__ __forceinline__ bool elect_one() {
 // follows a wait here are warp-wide tcgen05 instructions).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status));
+}
+
+// Descriptor of a 512-byte scale tile in shared memory: 32 rows of 16 bytes,
+// no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sf_tile_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// Scale tile, shared memory -> 4 columns of tensor memory, the 32 lanes
+// repeated in the four partitions. Ordered before later MMAs of the thread.
+__device__ __forceinline__ void sf_tile_to_tmem(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
 }
 
 // 8 columns of this thread's lane <- two 16-byte vectors.
