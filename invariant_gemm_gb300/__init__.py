@@ -267,35 +267,40 @@ def check_status(ws, stream=None) -> int:
 # device or inner stride than its place asks for raises IGError (IG_ERR_ARG or
 # IG_ERR_SHAPE) before the library is called; the library checks the rest.
 
-def _rows(what, name, t, dev, dtype, rows, cols):
-    """Checks a [rows][cols] operand with contiguous rows on GPU `dev` (an
-    index); returns its row stride. A single row's stride means nothing."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
-    if t.shape != (rows, cols):
-        raise IGError(-2, f"{what}: {name} is {tuple(t.shape)}, ({rows}, {cols}) wanted")
-    ld, inner = t.stride()
-    if inner != 1 and cols != 1:
-        raise IGError(-2, f"{what}: {name} has strides ({ld}, {inner}), contiguous rows wanted")
-    return ld if rows > 1 else cols
+# A call's checks take as long as its launch, so each is one test that passes;
+# _why finds out what is wrong once one has not.
+
+def _rows(what, name, t, dev, dtype, shape):
+    """Checks an operand of `shape` with contiguous rows on GPU `dev` (an index);
+    returns its row stride. A single row's stride means nothing."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return shape[1]
+        ld, inner = t.stride()
+        if inner == 1 or shape[1] == 1:
+            return ld if shape[0] > 1 else shape[1]
+    _why(what, name, t, dev, dtype, shape)
 
 
 def _flat(what, name, t, dev, dtype, count):
     """Checks a contiguous operand of at least `count` elements."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise IGError(-1, f"{what}: {name} is {t.dtype} on {t.device}")
-    if t.numel() < count or not t.is_contiguous():
-        raise IGError(-2, f"{what}: {name} has {t.numel()} elements, {count} contiguous wanted")
+    if not (t.dtype is dtype and t.numel() >= count and t.is_contiguous() and
+            t.get_device() == dev):
+        _why(what, name, t, dev, dtype, (count,))
 
 
 def _packed(what, name, codes, scales, dev, u8, rows, K):
     """Checks the two tensors of a [rows][K] MX4 matrix."""
-    if codes.dtype is not u8 or codes.get_device() != dev:
-        raise IGError(-1, f"{what}: {name} codes are {codes.dtype} on {codes.device}")
-    if K & 1 or codes.shape != (rows, K >> 1) or not codes.is_contiguous():
-        raise IGError(-2, f"{what}: {name} codes are {tuple(codes.shape)}, "
-                          f"({rows}, {K // 2}) contiguous wanted")
+    if K & 1 or not (codes.dtype is u8 and codes.shape == (rows, K >> 1) and
+                     codes.is_contiguous() and codes.get_device() == dev):
+        _why(what, name + " codes", codes, dev, u8, (rows, K // 2))
     _flat(what, name + " scales", scales, dev, u8, ((rows + 127) >> 7) * ((K + 127) >> 7) * 512)
+
+
+def _why(what, name, t, dev, dtype, shape):
+    code = -1 if t.dtype is not dtype or t.get_device() != dev else -2
+    raise IGError(code, f"{what}: {name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
+                        f"{t.device}; {dtype} {tuple(shape)} with contiguous rows on GPU {dev} wanted")
 
 
 def _value_type(what, name, t, torch):
@@ -328,10 +333,10 @@ def mx4_quantize(x, codes, scales, stream=None):
     """x [rows][K] (bf16 or FP32, rows may be strided) -> MX4: codes uint8
     [rows][K/2] and scales, uint8 of mx4_scale_bytes(rows, K) elements."""
     import torch
-    rows, K = x.shape
+    rows, K = shape = x.shape
     dev = x.get_device()
     t = _value_type("mx4_quantize", "x", x, torch)
-    ld = _rows("mx4_quantize", "x", x, dev, x.dtype, rows, K)
+    ld = _rows("mx4_quantize", "x", x, dev, x.dtype, shape)
     _packed("mx4_quantize", "x", codes, scales, dev, torch.uint8, rows, K)
     rc = (_LIB or lib()).ig_mx4_quantize(rows, K, x.data_ptr(), ld, t, codes.data_ptr(),
                                          scales.data_ptr(), _on(dev, stream, torch))
@@ -342,10 +347,10 @@ def mx4_quantize(x, codes, scales, stream=None):
 def mx4_dequantize(codes, scales, out, stream=None):
     """The values of an MX4 matrix into out [rows][K] (bf16 or FP32)."""
     import torch
-    rows, K = out.shape
+    rows, K = shape = out.shape
     dev = out.get_device()
     t = _value_type("mx4_dequantize", "out", out, torch)
-    ld = _rows("mx4_dequantize", "out", out, dev, out.dtype, rows, K)
+    ld = _rows("mx4_dequantize", "out", out, dev, out.dtype, shape)
     _packed("mx4_dequantize", "input", codes, scales, dev, torch.uint8, rows, K)
     rc = (_LIB or lib()).ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(),
                                            out.data_ptr(), ld, t, _on(dev, stream, torch))
@@ -364,11 +369,11 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
     """y [M][N] (bf16 or FP32) = x w^T, x [M][K] and w [N][K] in MX4. flags: 0 or
     FLAG_STATIC_WEIGHTS."""
     import torch
-    M, N = y.shape
+    M, N = shape = y.shape
     K = 2 * x_codes.shape[-1]
     dev = y.get_device()
     t = _value_type("mx4_gemm", "y", y, torch)
-    ld = _rows("mx4_gemm", "y", y, dev, y.dtype, M, N)
+    ld = _rows("mx4_gemm", "y", y, dev, y.dtype, shape)
     u8 = torch.uint8
     _packed("mx4_gemm", "x", x_codes, x_scales, dev, u8, M, K)
     _packed("mx4_gemm", "w", w_codes, w_scales, dev, u8, N, K)
@@ -383,18 +388,18 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
 
 def _gate(what, gate, dev, torch, M, H):
     """(row stride, column stride) of a gate that broadcasts to [M][H]."""
-    if gate.dtype is not torch.bfloat16 or gate.get_device() != dev:
-        raise IGError(-1, f"{what}: gate is {gate.dtype} on {gate.device}")
-    g = gate if gate.dim() == 2 else gate[None] if gate.dim() == 1 else None
-    if g is None or g.shape[0] not in (1, M) or g.shape[1] not in (1, H):
-        raise IGError(-2, f"{what}: gate is {tuple(gate.shape)}, which does not broadcast "
-                          f"to ({M}, {H})")
-    (rows, cols), (rs, cs) = g.shape, g.stride()
-    if cols == 1:
-        cs = 0
-    if cs not in (0, 1):
-        raise IGError(-2, f"{what}: gate has strides {g.stride()}, contiguous rows wanted")
-    return rs if rows > 1 else 0, cs
+    shape, strides = gate.shape, gate.stride()
+    if len(shape) == 1:
+        shape, strides = (1, *shape), (0, *strides)
+    if gate.dtype is torch.bfloat16 and len(shape) == 2 and gate.get_device() == dev:
+        rows, cols = shape
+        rs, cs = strides
+        if (rows == M or rows == 1) and (cols == H or cols == 1):
+            if cols == 1:
+                cs = 0
+            if cs == 0 or cs == 1:
+                return rs if rows > 1 else 0, cs
+    _why(what, "gate", gate, dev, torch.bfloat16, (M, H))
 
 
 def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=1e-6,
@@ -411,7 +416,7 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
     lead = h if h is not None else y
     if lead is None:
         raise IGError(-1, "block_norm: neither h nor y")
-    M, H = lead.shape
+    M, H = shape = lead.shape
     dev = lead.get_device()
     res = h if h is not None else h_out
     t = 0 if res is None else _value_type(what, "h", res, torch)
@@ -419,16 +424,16 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
     ph = py = pg = p_post = p_pre = pho = pn = pc = ps = None
     grs = gcs = 0
     if h is not None:
-        ld_h = _rows(what, "h", h, dev, h.dtype, M, H)
+        ld_h = _rows(what, "h", h, dev, h.dtype, shape)
         ph = h.data_ptr()
     if y is not None:
-        ld_y = _rows(what, "y", y, dev, b16, M, H)
+        ld_y = _rows(what, "y", y, dev, b16, shape)
         py = y.data_ptr()
     if h_out is not None:
-        ld_ho = _rows(what, "h_out", h_out, dev, res.dtype, M, H)
+        ld_ho = _rows(what, "h_out", h_out, dev, res.dtype, shape)
         pho = h_out.data_ptr()
     if n_out is not None:
-        ld_n = _rows(what, "n_out", n_out, dev, b16, M, H)
+        ld_n = _rows(what, "n_out", n_out, dev, b16, shape)
         pn = n_out.data_ptr()
     if w_post is not None:
         _flat(what, "w_post", w_post, dev, b16, H)

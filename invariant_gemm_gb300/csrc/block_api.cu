@@ -123,6 +123,8 @@ int ig_block_norm(const ig_norm_shape* s, const void* h, const void* y, const vo
   if (s->gate_col_stride != 0 && s->gate_col_stride != 1) return IG_ERR_ARG;
   if (s->M < 0 || s->H < 8 || s->H % 8) return IG_ERR_SHAPE;
   if (s->M > (1ll << 31) - 1 || s->H > kNormMaxH) return IG_ERR_UNSUPPORTED;
+  if (!(s->eps >= 0.0f)) return IG_ERR_ARG;
+  if (s->M == 0) return IG_OK;        // an empty tensor may have no address
   // something to read, something to write; what belongs to a part of the
   // operator is given with that part only
   if ((!h && !y) || (!h_out && !n_out && !codes)) return IG_ERR_ARG;
@@ -136,8 +138,6 @@ int ig_block_norm(const ig_norm_shape* s, const void* h, const void* y, const vo
     return IG_ERR_SHAPE;
   if (gate && (s->gate_row_stride < 0 || (s->gate_col_stride && s->gate_row_stride % 8)))
     return IG_ERR_SHAPE;
-  if (!(s->eps >= 0.0f)) return IG_ERR_ARG;
-  if (s->M == 0) return IG_OK;
   if (!aligned16(h) || !aligned16(y) || !aligned16(w_post) || !aligned16(w_pre) ||
       !aligned16(h_out) || !aligned16(n_out) || !aligned16(codes) || !aligned16(scales) ||
       !aligned16(gate))

@@ -9,6 +9,8 @@
 // of 16 bytes), so the product copies a tile as it stands.
 #pragma once
 
+#include <atomic>
+
 #include "ig_common.cuh"
 
 namespace ig {
@@ -78,6 +80,20 @@ cudaError_t launch_mx4_dequantize(const Mx4DequantParams& p, bool f32, cudaStrea
 cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st);
 cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st);
 cudaError_t launch_block_norm(const NormParams& p, bool h_f32, cudaStream_t st);
+
+// Lets a kernel use all of an SM's shared memory (227 KB), once per device:
+// `done` has a bit for each device it was set on. The call costs a product of
+// one token a tenth of its host time.
+inline cudaError_t allow_smem(const void* kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 #ifdef __CUDACC__
 

@@ -22,6 +22,7 @@
 // thread takes about 60 cycles to issue a copy or an expected count: one alone
 // took 640 over a stage, which held a block at 46 GB/s.
 #include <algorithm>
+#include <atomic>
 
 #include "mx4.cuh"
 #include "umma_mx4.cuh"
@@ -160,6 +161,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     constexpr uint32_t idesc0 = umma_idesc_mx4(kBM, BN), idesc1 = umma_idesc_sf(idesc0, 2);
     const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
                    xd = umma_desc_sw128(smem_u32(ring) + kWBytes);
+    // A column holds the scales of 32 rows, and a 64-token tile may start at
+    // row 64 of its group of 128, two columns on. (An odd column is not a valid
+    // start: 32-token tiles only ever start at row 0.)
+    const uint32_t shift = (uint32_t)(m0 & 127) / 32;
     const bool leader = elect_one();
     int b = 0, s = 0;
     uint32_t parity = 0;
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         break;
       tc_fence_after();
       const uint64_t w = wd + s * (kStage >> 4), x = xd + s * (kStage >> 4);
-      const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8;
+      const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8 + shift;
       const int rem = (int)min((int64_t)kBK, k1 - k0 - (int64_t)b * kBK);
       if (leader) {
         umma_mx4(tmem, w, x, idesc0, sfa, sfb, b > 0);
@@ -299,7 +304,8 @@ cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
   const int ring = p.stages * stage_bytes(BN);
   const int smem = 2048 + (own_sums(BN) ? ring + sums : std::max(ring, sums));
   auto kern = gemm_kernel<BN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), allowed);
   if (e != cudaSuccess) return e;
   if (encode_map_2d(&p.tm_x, p.xc, (uint64_t)p.M, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, BN,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
@@ -326,21 +332,35 @@ cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
 
 cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   p.ntiles = (int32_t)((p.N + kBM - 1) / kBM);
+  // Parts of K: enough blocks for most SMs where the columns alone are few, and
+  // no part under 8 stages, since the pairs of many tokens pay for each part.
+  // N = K = 4096, us for M = 1 / 256 / 4096: S = 1 5.4 / 8.9 / 27, S = 2 3.9 /
+  // 8.6 / 32, S = 4 3.5 / 9.7 / 35; N = 8192, K = 28672, M = 16 / 8192: 25.2 / 519,
+  // 21.4 / 521, 20.8 / 529.
   const int64_t stages = (p.K + kBK - 1) / kBK;
   int S = 1;
-  while (S < 8 && (int64_t)p.ntiles * S < 96 && stages >= 8 * S) S *= 2;
+  while (S < 8 && (int64_t)p.ntiles * S < 96 && stages >= 16 * S) S *= 2;
   const int64_t per = (stages + S - 1) / S;
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
-  if (p.M > 512) return launch_mx4_gemm_pair(p, sm_count(), st);
+  // Pairs where their tiles of 256 x 256 come to 32 or more, about half of the
+  // pairs: M = 512, N = K = 4096 (32 tiles) 10.8 us against 12.4 with 128-token
+  // tiles here, M = 256 (16) 10.7 against 8.6. With up to 128 tokens half of a
+  // pair's tile is empty, and it takes more of them: N = 8192 (32) 15.6 us
+  // against 13.0, N = 12288 (48) 11.4 against 13.1.
+  const int64_t pair_tiles = (p.N + 255) / 256 * ((p.M + 255) / 256);
+  if (p.M > 64 && pair_tiles >= (p.M > 128 ? 32 : 48))
+    return launch_mx4_gemm_pair(p, sm_count(), st);
   if (encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, kBM,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
     return cudaErrorInvalidValue;
   if (p.M <= 16) return launch_bn<16>(p, st);
   if (p.M <= 32) return launch_bn<32>(p, st);
-  if (p.M <= 64) return launch_bn<64>(p, st);
-  if (p.M <= 128) return launch_bn<128>(p, st);
-  return launch_bn<256>(p, st);
+  // 64-token tiles while all of them are at work at once, two to an SM: M = 256,
+  // N = K = 4096 (256 blocks) 8.6 us against 8.9 with 128; K = 11008 (512) 18.2
+  // against 13.7.
+  if (p.M <= 64 || (p.M + 63) / 64 * p.ntiles * p.S <= 2 * sm_count()) return launch_bn<64>(p, st);
+  return launch_bn<128>(p, st);
 }
 
 }  // namespace ig

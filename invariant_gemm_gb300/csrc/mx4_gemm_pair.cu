@@ -12,6 +12,8 @@
 // the MMAs. The sums of a part of K go to registers at once (64 a thread) and
 // tensor memory is free again: the stores of a tile run beside the products of
 // the next.
+#include <atomic>
+
 #include "mx4.cuh"
 #include "umma_mx4.cuh"
 
@@ -32,7 +34,7 @@ constexpr int kThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kSfCol = 256;         // tensor memory: sums 0-255, then scales
 constexpr uint32_t kSfCols = 8 + 16;     // per stage: w 2 x 4, x 2 x 8
 constexpr uint32_t kTmemCols = 512;
-constexpr int kGroup = 8;                // token tiles that run through the columns together
+constexpr int kGroup = 16;               // token tiles that run through the columns together
 
 struct Ctl {
   uint64_t full[kStages];       // of the first block: the copies of both blocks
@@ -358,8 +360,8 @@ cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st) {
       encode_map_2d(&p.tm_xs, p.xs, xt, 256, kMx4TileBytes, 256, 2,
                     CU_TENSOR_MAP_SWIZZLE_NONE) != IG_OK)
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(gemm_pair_kernel), allowed);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (p.N + kBN - 1) / kBN * ((p.M + kBT - 1) / kBT);
   if (tiles > 0x3fffffffLL) return cudaErrorInvalidConfiguration;

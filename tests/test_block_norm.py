@@ -250,6 +250,16 @@ def test_refusals(kw, code):
 
 def test_no_rows_is_a_no_op():
     assert c_norm(M=0) == 0
+    assert c_norm(M=0, h=None, y=None, gate=None, h_out=None, n_out=None) == 0
+
+
+@gpu
+def test_empty_tensors():
+    need_gpu()
+    d = make(0, 64, "bf16", "full", 1)
+    o = run(d, "bf16", codes=True)
+    assert o["h"].shape == (0, 64)
+    assert run(make(0, 64, "f32", "token", 1), "f32")["n"].shape == (0, 64)
 
 
 def test_binding_refuses_wrong_tensors():

@@ -140,6 +140,17 @@ def test_quantize_offsets_past_32_bits():
     assert not out[:8].any() and not out[R // 2:R // 2 + 8].any()
 
 
+@gpu
+def test_empty_tensors():
+    need_gpu()
+    codes, scales = quantize(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"))
+    ig.mx4_dequantize(codes, scales, torch.zeros(0, 64, device="cuda"))
+    w = held(values(64, 64, 1))
+    y = torch.zeros(0, 64, device="cuda")
+    ig.mx4_gemm(codes, scales, w[0], w[1], y, ig.mx4_workspace())
+    torch.cuda.synchronize()
+
+
 # ---------------------------------------------------------------- product
 
 def gemm(x, w, N, y_t, ws=None, y=None, flags=0):
