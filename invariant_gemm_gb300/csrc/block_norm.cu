@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(max_threads(F32, W), W) norm_kernel(NormParams
       }
       if (p.codes) {
         // places past the row's end are those that pad K to 128
-        uint32_t byte;
         float n[8];
         unpack8(o, n);
-        const uint32_t codes = mx4_encode8(n, top_of(o), byte);
-        const uint32_t word = mx4_scale_word(in ? byte : 127u);
+        const uint32_t byte = mx4_block_byte<4>(top_of(o));
+        const uint32_t codes = mx4_encode8(n, byte);
+        const uint32_t word = mx4_scale_word<4>(in ? byte : 127u);
         if (in) reinterpret_cast<uint32_t*>(p.codes)[row * vecs + c] = codes;
         if (c % 16 == 0 && c < p.kt * 16)
           *reinterpret_cast<uint32_t*>(p.scales + mx4_scale_at(row, c / 4, p.kt)) = word;

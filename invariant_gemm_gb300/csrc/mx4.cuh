@@ -176,14 +176,17 @@ __device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
   return __float_as_uint(t);
 }
 
-// One thread's 8 values v of a row (k = 8 t .. 8 t + 7 for lane t of an aligned
-// group of 4 lanes that hold one block) and their top_of: returns the codes,
-// and the scale byte of the block in all four lanes. Whole warps call it.
-__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t top,
-                                                uint32_t& byte) {
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  byte = e8m0_of(top);
+// The scale byte of the block that an aligned group of LANES lanes holds, in
+// all of them, from each lane's top_of. Whole warps call it.
+template <int LANES>
+__device__ __forceinline__ uint32_t mx4_block_byte(uint32_t top) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return e8m0_of(top);
+}
+
+// Codes of 8 values of a block with scale byte `byte`.
+__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t byte) {
   const float inv = e8m0_inverse(byte);
   float q[8];
 #pragma unroll
@@ -192,11 +195,12 @@ __device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8], uint32_t to
   return byte == 255u ? 0u : codes;
 }
 
-// The 4 scale bytes of 16 lanes (one block to 4 of them), in the first of the
-// 16. Whole warps call it.
+// The 4 scale bytes of 4 blocks of LANES lanes each, in the first of those
+// lanes. Whole warps call it.
+template <int LANES>
 __device__ __forceinline__ uint32_t mx4_scale_word(uint32_t byte) {
-  byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 8;
-  return byte | __shfl_down_sync(0xffffffffu, byte, 8) << 16;
+  byte |= __shfl_down_sync(0xffffffffu, byte, LANES) << 8;
+  return byte | __shfl_down_sync(0xffffffffu, byte, 2 * LANES) << 16;
 }
 
 #endif  // __CUDACC__
