@@ -18,6 +18,10 @@
 // (launch_block_norm has the figures). Copying rows ahead through shared memory by
 // blocks that stay (cp.async, 3 rows deep) was slower than fresh blocks: 107
 // against 87 us at 8192 x 8192.
+//
+// The next kernel on the stream starts when this one is complete (no early
+// release): it may be one that reads n before its own wait, as the fused LoRA
+// kernel does with IG_FLAG_INPUT_READY once one more kernel lies between.
 #include "mx4.cuh"
 
 namespace ig {
@@ -114,7 +118,6 @@ __global__ void __launch_bounds__(max_threads(F32, W), W) norm_kernel(NormParams
   };
   // place of vector j of this thread's i-th sum
   auto place = [&](int i, int j) { return tid + i * (int)blockDim.x + j * T; };
-  griddep_launch();
   griddep_wait();
 
   uint4 y[W][V], h[W][V][HV], g[W][V];
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(max_threads(F32, W), W) norm_kernel(NormParams
       const int c = place(i, j);
       y[i][j] = make_uint4(0, 0, 0, 0);
       if (p.y && c < vecs)
-        y[i][j] = __ldcs(reinterpret_cast<const uint4*>(p.y + row * p.ld_y) + c);
+        y[i][j] = *(reinterpret_cast<const uint4*>(p.y + row * p.ld_y) + c);
     }
 #pragma unroll
   for (int i = 0; i < W; ++i)
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(max_threads(F32, W), W) norm_kernel(NormParams
               : reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.h) +
                                                row * p.ld_h);
 #pragma unroll
-      for (int q = 0; q < HV; ++q) h[i][j][q] = __ldcs(at + c * HV + q);
+      for (int q = 0; q < HV; ++q) h[i][j][q] = at[c * HV + q];
     }
   const bool gates = p.gate && p.gate_cs;     // a gate value for each place
 #pragma unroll

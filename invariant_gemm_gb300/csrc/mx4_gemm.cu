@@ -114,9 +114,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = uniform(ctl->tmem);
   if (S > 1 && own_sums(BN)) cluster_arrive_relaxed();
-  // The next kernel may start once every block is here: each has its tensor
-  // memory by then, so no early block can hold what one of these still needs.
-  griddep_launch();
 
   bool ok = true;
   if (warp == kCopyWarp || warp == kCopyXWarp) {
@@ -134,6 +131,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     const int ntile = (int)((k1 - k0 + 127) / 128);       // scale tiles of a group
     if (leader) prefetch_tensormap(map);
     if (!early) griddep_wait();
+    // The next kernel may start once every block is here, all work before this
+    // kernel is complete, and each block has its tensor memory: so no early
+    // block can hold what one of these still needs.
+    if (!w) griddep_launch();
     int b = 0, s = 0;
     uint32_t parity = 1;      // a stage's first use finds its barrier in the phase before
     for (; b < nk; ++b) {

@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(Mx4QuantParams p) {
   constexpr int G = Raw<T>::kValues, kLanes = kMx4Block / G;
   const Walk<U, G> start(p.kt);
   const uint32_t groups = (uint32_t)(p.K / G);
-  griddep_launch();
   griddep_wait();
   Raw<T> raw[U];
   Walk<U, G> w = start;
@@ -119,7 +118,6 @@ template <typename T, int U>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(Mx4DequantParams p) {
   const Walk<U, 8> start(p.kt);
   const uint32_t groups = (uint32_t)(p.K / 8);
-  griddep_launch();
   griddep_wait();
   uint32_t codes[U], byte[U];
   Walk<U, 8> w = start;
