@@ -360,7 +360,10 @@ typedef struct ig_mx4_shape {
   int64_t K;      /* reduction length (a multiple of 32) */
   int64_t ld_y;   /* row stride of y */
   int32_t y_type; /* ig_type */
-  int32_t flags;  /* 0 or IG_FLAG_STATIC_WEIGHTS (of w_codes and w_scales) */
+  int32_t flags;  /* 0, IG_FLAG_STATIC_WEIGHTS (of w_codes and w_scales) and, for
+                     tests only, IG_FLAG_TEST_COPY_TIMEOUT: the first wait for a
+                     copy expires in every block, nothing is stored for its
+                     tile and the status becomes IG_ERR_TIMEOUT */
 } ig_mx4_shape;
 
 /* Bytes of the workspace of ig_mx4_gemm: the status word and counters that a

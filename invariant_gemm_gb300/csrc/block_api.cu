@@ -82,7 +82,7 @@ int ig_mx4_gemm(const ig_mx4_shape* shape, const void* x_codes, const void* x_sc
                 const void* w_codes, const void* w_scales, void* y, void* ws, size_t ws_bytes,
                 void* stream) {
   if (!shape) return IG_ERR_ARG;
-  if (shape->flags & ~IG_FLAG_STATIC_WEIGHTS) return IG_ERR_ARG;
+  if (shape->flags & ~(IG_FLAG_STATIC_WEIGHTS | IG_FLAG_TEST_COPY_TIMEOUT)) return IG_ERR_ARG;
   if (!known_type(shape->y_type)) return IG_ERR_ARG;
   int rc = check_mx4(shape->M, shape->K);
   if (rc != IG_OK) return rc;

@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     int b = 0, s = 0;
     uint32_t parity = 0;
     for (; b < nk; ++b) {
-      if (!warp_wait(&ctl->full[s], parity, p.status) ||
+      const bool expire = b == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT) != 0;
+      if (!warp_wait(&ctl->full[s], parity, p.status, expire ? 0 : 1ll << 31) ||
           !warp_wait(&ctl->sf_ready[s], parity, p.status))
         break;
       tc_fence_after();

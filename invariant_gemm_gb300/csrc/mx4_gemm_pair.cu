@@ -241,7 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           part_end = min(nkb, kb + per_part);
           ok = part == 0 || warp_wait(&ctl->sums_empty, (part - 1) & 1, p.status);
         }
-        ok = ok && warp_wait(&ctl->full[at.s], at.parity, p.status);
+        const bool expire = it == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT) != 0;
+        ok = ok && warp_wait(&ctl->full[at.s], at.parity, p.status, expire ? 0 : 1ll << 31);
         if (!ok) break;
         tc_fence_after();
         const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);

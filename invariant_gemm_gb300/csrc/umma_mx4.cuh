@@ -52,8 +52,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // mbar_wait_bounded by a whole warp, with one answer for all its lanes (what
 // follows a wait here are warp-wide tcgen05 instructions).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status,
+                                          long long budget = 1ll << 31) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status, budget));
 }
 
 // Descriptor of a 512-byte scale tile in shared memory: 32 rows of 16 bytes,

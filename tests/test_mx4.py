@@ -341,6 +341,21 @@ def test_quantize_then_product_in_a_graph():
         check_product(y, held(new)[2], w[2], "f32")
 
 
+@gpu
+@pytest.mark.parametrize("M,N,K", [(4, 264, 256), (30, 1024, 8192), (100, 512, 4096),
+                                   (600, 4096, 1024)])
+def test_expired_wait_is_reported_and_the_workspace_is_usable(M, N, K):
+    """The first copy's wait runs out: IG_ERR_TIMEOUT, and the next call is
+    right."""
+    need_gpu()
+    x, w = held(values(M, K, 3)), held(values(N, K, 4))
+    ws = ig.mx4_workspace()
+    y = torch.full((M, N), 5.0, device="cuda")
+    ig.mx4_gemm(x[0], x[1], w[0], w[1], y, ws, flags=ig.FLAG_TEST_COPY_TIMEOUT)
+    assert ig.check_status(ws) == -8
+    check_product(gemm(x, w, N, "f32", ws=ws), x[2], w[2], "f32")
+
+
 # --------------------------------------------------------------- refusals
 
 FAKE = 1 << 20     # an aligned address that no call below reads
