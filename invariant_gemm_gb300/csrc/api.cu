@@ -11,6 +11,23 @@
 #include "ig_common.cuh"
 
 namespace ig {
+
+// SMs of the current device (cached per device; 152 on GB300).
+int sm_count() {
+  static std::mutex mu;
+  static std::map<int, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(dev);
+  if (it != cache.end()) return it->second;
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 152;
+  cache[dev] = n;
+  return n;
+}
+
 namespace {
 
 struct Plan {
@@ -375,22 +392,6 @@ int run_expand(const ig_shape* sh, const Plan& pl, const float* z, const void* B
 }
 
 }  // namespace
-
-// SMs of the current device (cached per device; 152 on GB300).
-int sm_count() {
-  static std::mutex mu;
-  static std::map<int, int> cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(dev);
-  if (it != cache.end()) return it->second;
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    n = 152;
-  cache[dev] = n;
-  return n;
-}
 
 // Workspace bytes lora_shrink itself touches: everything before the expand's
 // Z operand, which only lora_apply writes. 0 for an invalid shape.

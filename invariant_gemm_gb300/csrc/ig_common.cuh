@@ -114,9 +114,6 @@ struct ExpandParams {
   int32_t slices, L, ntiles, flags;
 };
 
-// SMs of the current device (cached per device; 152 on GB300).
-int sm_count();
-
 // 2-D bf16 tensor map [rows][cols] with the given row stride; box
 // box_cols x box_rows; swizzle is a CUtensorMapSwizzle value. IG_OK or
 // IG_ERR_CUDA (driver entry point missing or encode rejected).

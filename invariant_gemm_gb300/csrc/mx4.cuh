@@ -28,6 +28,9 @@ __host__ __device__ inline int64_t mx4_scale_at(int64_t row, int64_t kb, int64_t
          ((row >> 5) & 3) * 4 + (kb & 3);
 }
 
+// SMs of the current device (cached per device; 152 on GB300).
+int sm_count();
+
 struct Mx4QuantParams {
   const void* x;
   uint8_t* codes;
