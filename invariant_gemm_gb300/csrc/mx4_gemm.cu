@@ -42,7 +42,7 @@ struct Ctl {
   uint64_t full[kMaxStages];
   uint64_t sf_ready[kMaxStages];   // scales in tensor memory
   uint64_t empty[kMaxStages];
-  uint64_t done;
+  uint64_t done;       // `consumed` is known, and the MMAs are complete
   uint64_t parts;      // the other blocks' sums (and the own ones) have come
   uint32_t tmem;
   int32_t issued[2];   // stages filled: weights, tokens
@@ -60,11 +60,43 @@ __host__ __device__ constexpr int sf_col(int bn) { return bn < 32 ? 32 : bn; }
 __host__ __device__ constexpr int sf_cols(int bn) { return 8 * (1 + sf_groups(bn)); }
 // The parts' sums [S][groups of four tokens of this owner][128][4] FP32: BN *
 // 512 bytes, a little more where S does not divide the groups. Beside the ring
-// for up to 64 tokens; else in its place once every block of the cluster is
-// through with it.
-__host__ __device__ constexpr bool own_sums(int bn) { return bn <= 64; }
+// for up to 32 tokens; else in its place once every block of the cluster is
+// through with it (64 tokens, two blocks to an SM: a fourth stage instead, M =
+// 256, N = K = 4096 8.6 -> 8.2 us). With one part they are not needed: the sums
+// go from registers to memory.
+__host__ __device__ constexpr bool own_sums(int bn) { return bn <= 32; }
 __host__ __device__ inline int share_of(int bn, int S) { return (bn / 4 + S - 1) / S; }
-__host__ __device__ inline int sums_bytes(int bn, int S) { return share_of(bn, S) * S * kBM * 16; }
+__host__ __device__ inline int sums_bytes(int bn, int S) {
+  return S > 1 ? share_of(bn, S) * S * kBM * 16 : 0;
+}
+
+// Four tokens' results of column n (0-127 of the tile; lanes hold neighbouring
+// columns), tokens t0 ... of the tile, of which `tok` exist. y: the tile's
+// first token and column.
+template <typename T>
+__device__ __forceinline__ void store4(T* y, int64_t ld, int n, bool in, int t0, int tok,
+                                       const float4& v) {
+  if constexpr (sizeof(T) == 4) {
+    T* o = y + t0 * ld + n;
+    if (in && t0 < tok) *o = v.x;
+    if (in && t0 + 1 < tok) o[ld] = v.y;
+    if (in && t0 + 2 < tok) o[2 * ld] = v.z;
+    if (in && t0 + 3 < tok) o[3 * ld] = v.w;
+  } else {
+    // lanes 2 l, 2 l + 1 trade values: the even one stores both columns of
+    // tokens 0 and 2, the odd one of 1 and 3
+    const bool odd = n & 1;
+    const float a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
+    const float b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
+    T* o = y + (t0 + odd) * ld + (n & ~1);
+    if (in && t0 + odd < tok)
+      *reinterpret_cast<uint32_t*>(o) =
+          odd ? f32x2_to_bf16x2_bits(a, v.y) : f32x2_to_bf16x2_bits(v.x, a);
+    if (in && t0 + 2 + odd < tok)
+      *reinterpret_cast<uint32_t*>(o + 2 * ld) =
+          odd ? f32x2_to_bf16x2_bits(b, v.w) : f32x2_to_bf16x2_bits(v.z, b);
+  }
+}
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ Mx4GemmParams p) {
@@ -99,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       mbar_init(&ctl->sf_ready[i], 4);
       mbar_init(&ctl->empty[i], 1);
     }
-    mbar_init(&ctl->done, 1);
+    mbar_init(&ctl->done, 2);
     mbar_init(&ctl->parts, 1);
     ctl->issued[0] = ctl->issued[1] = ctl->consumed = 0;
     fence_mbar_init();
@@ -192,8 +224,9 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       }
     }
     if (leader) {
-      umma_commit(&ctl->done);
       ctl->consumed = b;
+      mbar_arrive(&ctl->done);
+      umma_commit(&ctl->done);
     }
     __syncwarp();
     griddep_wait();
@@ -211,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       }
     }
     griddep_wait();
-    ok = warp_wait(&ctl->done, 0, p.status);
+    ok = warp_wait(&ctl->done, 0, p.status) && ctl->consumed == nk;
     tc_fence_after();
   }
   if (!own_sums(BN)) {
@@ -221,6 +254,8 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   }
   if (S > 1) cluster_wait();
 
+  float* y32 = static_cast<float*>(p.y) + m0 * p.ldy + n0;
+  __nv_bfloat16* y16 = static_cast<__nv_bfloat16*>(p.y) + m0 * p.ldy + n0;
   if (warp < 4 && ok) {
     int owner = 0, at = 0;
     for (int c = 0; c < tok; c += 32) {
@@ -229,9 +264,12 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         if (c + i >= tok) continue;
-        const float4 q = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        float4 q = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         if (S == 1) {
-          sums[(c + i) / 4 * kBM + tid] = q;
+          q.x += 0.0f; q.y += 0.0f; q.z += 0.0f; q.w += 0.0f;
+          const bool in = n0 + tid < p.N;
+          if (p.y_f32) store4(y32, p.ldy, tid, in, c + i, tok, q);
+          else store4(y16, p.ldy, tid, in, c + i, tok, q);
         } else {
           st_async_v4(map_rank(sums + (part * share + at) * kBM + tid, owner), q,
                       map_rank(&ctl->parts, owner));
@@ -257,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   if (S > 1) ok = mbar_wait_bounded(&ctl->parts, 0, p.status) && ok;
 
   // the owner of four tokens adds their sums up in order and stores them
-  if (!__all_sync(0xffffffffu, ok)) return;
+  if (S == 1 || !__all_sync(0xffffffffu, ok)) return;
   for (int u = warp; u < 4 * owned; u += kThreads / 32) {
     const int g = u >> 2, n = (u & 3) * 32 + lane;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -267,27 +305,8 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     }
     const int t0 = 4 * (part + g * S);
     const bool in = n0 + n < p.N;
-    if (p.y_f32) {
-      float* y = static_cast<float*>(p.y) + (m0 + t0) * p.ldy + n0 + n;
-      if (in) *y = v.x;
-      if (in && t0 + 1 < tok) y[p.ldy] = v.y;
-      if (in && t0 + 2 < tok) y[2 * p.ldy] = v.z;
-      if (in && t0 + 3 < tok) y[3 * p.ldy] = v.w;
-    } else {
-      // lanes 2 l, 2 l + 1 trade values: the even one stores both columns of
-      // tokens 0 and 2, the odd one of 1 and 3
-      const bool odd = lane & 1;
-      const float a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
-      const float b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
-      __nv_bfloat16* y =
-          static_cast<__nv_bfloat16*>(p.y) + (m0 + t0 + odd) * p.ldy + n0 + (n & ~1);
-      if (in && t0 + odd < tok)
-        *reinterpret_cast<uint32_t*>(y) =
-            odd ? f32x2_to_bf16x2_bits(a, v.y) : f32x2_to_bf16x2_bits(v.x, a);
-      if (in && t0 + 2 + odd < tok)
-        *reinterpret_cast<uint32_t*>(y + 2 * p.ldy) =
-            odd ? f32x2_to_bf16x2_bits(b, v.w) : f32x2_to_bf16x2_bits(v.z, b);
-    }
+    if (p.y_f32) store4(y32, p.ldy, n, in, t0, tok, v);
+    else store4(y16, p.ldy, n, in, t0, tok, v);
   }
 }
 

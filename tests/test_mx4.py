@@ -353,6 +353,7 @@ def test_expired_wait_is_reported_and_the_workspace_is_usable(M, N, K):
     y = torch.full((M, N), 5.0, device="cuda")
     ig.mx4_gemm(x[0], x[1], w[0], w[1], y, ws, flags=ig.FLAG_TEST_COPY_TIMEOUT)
     assert ig.check_status(ws) == -8
+    assert (y == 5).sum() > y.numel() // 2       # expired blocks store nothing
     check_product(gemm(x, w, N, "f32", ws=ws), x[2], w[2], "f32")
 
 
