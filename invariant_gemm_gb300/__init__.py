@@ -267,15 +267,15 @@ def check_status(ws, stream=None) -> int:
 # device or inner stride than its place asks for raises IGError (IG_ERR_ARG or
 # IG_ERR_SHAPE) before the library is called; the library checks the rest.
 
-# A call's checks take as long as its launch, so each is one test that passes;
-# _why finds out what is wrong once one has not.
+# The checks of a call take longer than its launch. So each call tests all that
+# is usual (right types, one device, contiguous) in expressions of its own, and
+# goes through _rows and _flat, which take strides and name what is wrong, only
+# when one of them is false.
 
 def _rows(what, name, t, dev, dtype, shape):
     """Checks an operand of `shape` with contiguous rows on GPU `dev` (an index);
     returns its row stride. A single row's stride means nothing."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        if t.is_contiguous():
-            return shape[1]
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0:
         ld, inner = t.stride()
         if inner == 1 or shape[1] == 1:
             return ld if shape[0] > 1 else shape[1]
@@ -285,37 +285,40 @@ def _rows(what, name, t, dev, dtype, shape):
 def _flat(what, name, t, dev, dtype, count):
     """Checks a contiguous operand of at least `count` elements."""
     if not (t.dtype is dtype and t.numel() >= count and t.is_contiguous() and
-            t.get_device() == dev):
+            t.get_device() == dev >= 0):
         _why(what, name, t, dev, dtype, (count,))
 
 
-def _packed(what, name, codes, scales, dev, u8, rows, K):
-    """Checks the two tensors of a [rows][K] MX4 matrix."""
-    if K & 1 or not (codes.dtype is u8 and codes.shape == (rows, K >> 1) and
-                     codes.is_contiguous() and codes.get_device() == dev):
-        _why(what, name + " codes", codes, dev, u8, (rows, K // 2))
-    _flat(what, name + " scales", scales, dev, u8, ((rows + 127) >> 7) * ((K + 127) >> 7) * 512)
+def _packed(what, name, codes, scales, dev, u8, rows, half):
+    """Checks the two tensors of a [rows][2 half] MX4 matrix."""
+    count = ((rows + 127) >> 7) * ((half + 63) >> 6) * 512
+    if not (codes.dtype is u8 and scales.dtype is u8 and codes.shape == (rows, half) and
+            codes.is_contiguous() and scales.is_contiguous() and scales.numel() >= count and
+            codes.get_device() == scales.get_device() == dev >= 0):
+        if codes.shape != (rows, half) or not codes.is_contiguous():
+            _why(what, name + " codes", codes, dev, u8, (rows, half))
+        _flat(what, name + " codes", codes, dev, u8, 0)
+        _flat(what, name + " scales", scales, dev, u8, count)
 
 
 def _why(what, name, t, dev, dtype, shape):
+    if dev < 0:
+        raise IGError(-1, f"{what}: operands are not on a GPU")
     code = -1 if t.dtype is not dtype or t.get_device() != dev else -2
     raise IGError(code, f"{what}: {name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
                         f"{t.device}; {dtype} {tuple(shape)} with contiguous rows on GPU {dev} wanted")
 
 
-def _value_type(what, name, t, torch):
-    """ig_type of a bf16 or FP32 tensor."""
-    if t.dtype is torch.bfloat16:
-        return 0
-    if t.dtype is torch.float32:
-        return 1
-    raise IGError(-1, f"{what}: {name} is {t.dtype}")
+def _values(what, name, t, torch):
+    """(sizes, GPU, ig_type, row stride) of a 2-D bf16 or FP32 operand."""
+    shape, dev, dtype = t.shape, t.get_device(), t.dtype
+    if len(shape) != 2 or not (dtype is torch.bfloat16 or dtype is torch.float32):
+        raise IGError(-1, f"{what}: {name} is {dtype} {tuple(shape)}, 2-D bf16 or FP32 wanted")
+    ld = shape[1] if dev >= 0 and t.is_contiguous() else _rows(what, name, t, dev, dtype, shape)
+    return shape, dev, int(dtype is torch.float32), ld
 
 
-def _on(dev, stream, torch):
-    """The stream of a call whose operands live on GPU `dev`."""
-    if dev < 0:
-        raise IGError(-1, "operands are not on a GPU")
+def _stream_of(dev, stream, torch):
     # the current stream's handle without the Stream object around it, whose
     # construction costs 2 us a call
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -333,13 +336,10 @@ def mx4_quantize(x, codes, scales, stream=None):
     """x [rows][K] (bf16 or FP32, rows may be strided) -> MX4: codes uint8
     [rows][K/2] and scales, uint8 of mx4_scale_bytes(rows, K) elements."""
     import torch
-    rows, K = shape = x.shape
-    dev = x.get_device()
-    t = _value_type("mx4_quantize", "x", x, torch)
-    ld = _rows("mx4_quantize", "x", x, dev, x.dtype, shape)
-    _packed("mx4_quantize", "x", codes, scales, dev, torch.uint8, rows, K)
+    (rows, K), dev, t, ld = _values("mx4_quantize", "x", x, torch)
+    _packed("mx4_quantize", "x", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
     rc = (_LIB or lib()).ig_mx4_quantize(rows, K, x.data_ptr(), ld, t, codes.data_ptr(),
-                                         scales.data_ptr(), _on(dev, stream, torch))
+                                         scales.data_ptr(), _stream_of(dev, stream, torch))
     if rc:
         raise IGError(rc, "mx4_quantize")
 
@@ -347,13 +347,10 @@ def mx4_quantize(x, codes, scales, stream=None):
 def mx4_dequantize(codes, scales, out, stream=None):
     """The values of an MX4 matrix into out [rows][K] (bf16 or FP32)."""
     import torch
-    rows, K = shape = out.shape
-    dev = out.get_device()
-    t = _value_type("mx4_dequantize", "out", out, torch)
-    ld = _rows("mx4_dequantize", "out", out, dev, out.dtype, shape)
-    _packed("mx4_dequantize", "input", codes, scales, dev, torch.uint8, rows, K)
+    (rows, K), dev, t, ld = _values("mx4_dequantize", "out", out, torch)
+    _packed("mx4_dequantize", "input", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
     rc = (_LIB or lib()).ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(),
-                                           out.data_ptr(), ld, t, _on(dev, stream, torch))
+                                           out.data_ptr(), ld, t, _stream_of(dev, stream, torch))
     if rc:
         raise IGError(rc, "mx4_dequantize")
 
@@ -369,29 +366,27 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
     """y [M][N] (bf16 or FP32) = x w^T, x [M][K] and w [N][K] in MX4. flags: 0 or
     FLAG_STATIC_WEIGHTS."""
     import torch
-    M, N = shape = y.shape
-    K = 2 * x_codes.shape[-1]
-    dev = y.get_device()
-    t = _value_type("mx4_gemm", "y", y, torch)
-    ld = _rows("mx4_gemm", "y", y, dev, y.dtype, shape)
-    u8 = torch.uint8
-    _packed("mx4_gemm", "x", x_codes, x_scales, dev, u8, M, K)
-    _packed("mx4_gemm", "w", w_codes, w_scales, dev, u8, N, K)
-    _flat("mx4_gemm", "ws", ws, dev, u8, 0)
-    rc = (_LIB or lib()).ig_mx4_gemm(Mx4Shape(M, N, K, ld, t, flags), x_codes.data_ptr(),
-                                     x_scales.data_ptr(), w_codes.data_ptr(),
-                                     w_scales.data_ptr(), y.data_ptr(), ws.data_ptr(),
-                                     ws.numel(), _on(dev, stream, torch))
+    what, u8 = "mx4_gemm", torch.uint8
+    (M, N), dev, t, ld = _values(what, "y", y, torch)
+    half = x_codes.shape[-1]
+    _packed(what, "x", x_codes, x_scales, dev, u8, M, half)
+    _packed(what, "w", w_codes, w_scales, dev, u8, N, half)
+    if not (ws.dtype is u8 and ws.is_contiguous() and ws.get_device() == dev):
+        _flat(what, "ws", ws, dev, u8, 0)
+    rc = (_LIB or lib()).ig_mx4_gemm(Mx4Shape(M, N, 2 * half, ld, t, flags), x_codes.data_ptr(),
+                                     x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                     y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     _stream_of(dev, stream, torch))
     if rc:
-        raise IGError(rc, "mx4_gemm")
+        raise IGError(rc, what)
 
 
-def _gate(what, gate, dev, torch, M, H):
+def _gate(what, gate, dev, b16, M, H):
     """(row stride, column stride) of a gate that broadcasts to [M][H]."""
     shape, strides = gate.shape, gate.stride()
     if len(shape) == 1:
         shape, strides = (1, *shape), (0, *strides)
-    if gate.dtype is torch.bfloat16 and len(shape) == 2 and gate.get_device() == dev:
+    if gate.dtype is b16 and len(shape) == 2 and gate.get_device() == dev:
         rows, cols = shape
         rs, cs = strides
         if (rows == M or rows == 1) and (cols == H or cols == 1):
@@ -399,7 +394,7 @@ def _gate(what, gate, dev, torch, M, H):
                 cs = 0
             if cs == 0 or cs == 1:
                 return rs if rows > 1 else 0, cs
-    _why(what, "gate", gate, dev, torch.bfloat16, (M, H))
+    _why(what, "gate", gate, dev, b16, (M, H))
 
 
 def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=1e-6,
@@ -416,24 +411,32 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
     lead = h if h is not None else y
     if lead is None:
         raise IGError(-1, "block_norm: neither h nor y")
-    M, H = shape = lead.shape
-    dev = lead.get_device()
-    res = h if h is not None else h_out
-    t = 0 if res is None else _value_type(what, "h", res, torch)
+    shape, dev, t, ld = _values(what, "h" if h is not None else "y", lead, torch)
+    M, H = shape
+    h_type = lead.dtype
     ld_h = ld_y = ld_ho = ld_n = H
     ph = py = pg = p_post = p_pre = pho = pn = pc = ps = None
     grs = gcs = 0
     if h is not None:
-        ld_h = _rows(what, "h", h, dev, h.dtype, shape)
-        ph = h.data_ptr()
+        ld_h, ph = ld, h.data_ptr()
+    elif h_out is not None:
+        t, h_type = int(h_out.dtype is torch.float32), h_out.dtype
+        if t == 0 and h_type is not b16:
+            _why(what, "h_out", h_out, dev, b16, shape)
     if y is not None:
-        ld_y = _rows(what, "y", y, dev, b16, shape)
+        if not (y.dtype is b16 and y.shape == shape and y.is_contiguous() and
+                y.get_device() == dev):
+            ld_y = _rows(what, "y", y, dev, b16, shape)
         py = y.data_ptr()
     if h_out is not None:
-        ld_ho = _rows(what, "h_out", h_out, dev, res.dtype, shape)
+        if not (h_out.dtype is h_type and h_out.shape == shape and h_out.is_contiguous() and
+                h_out.get_device() == dev):
+            ld_ho = _rows(what, "h_out", h_out, dev, h_type, shape)
         pho = h_out.data_ptr()
     if n_out is not None:
-        ld_n = _rows(what, "n_out", n_out, dev, b16, shape)
+        if not (n_out.dtype is b16 and n_out.shape == shape and n_out.is_contiguous() and
+                n_out.get_device() == dev):
+            ld_n = _rows(what, "n_out", n_out, dev, b16, shape)
         pn = n_out.data_ptr()
     if w_post is not None:
         _flat(what, "w_post", w_post, dev, b16, H)
@@ -442,15 +445,15 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
         _flat(what, "w_pre", w_pre, dev, b16, H)
         p_pre = w_pre.data_ptr()
     if gate is not None:
-        grs, gcs = _gate(what, gate, dev, torch, M, H)
+        grs, gcs = _gate(what, gate, dev, b16, M, H)
         pg = gate.data_ptr()
     if codes is not None or scales is not None:
         if codes is None or scales is None:
             raise IGError(-1, "block_norm: codes and scales go together")
-        _packed(what, "n", codes, scales, dev, torch.uint8, M, H)
+        _packed(what, "n", codes, scales, dev, torch.uint8, M, (H + 1) >> 1)
         pc, ps = codes.data_ptr(), scales.data_ptr()
-    s = NormShape(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale)
-    rc = (_LIB or lib()).ig_block_norm(s, ph, py, pg, p_post, p_pre, pho, pn, pc, ps,
-                                       _on(dev, stream, torch))
+    rc = (_LIB or lib()).ig_block_norm(
+        NormShape(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale), ph, py, pg,
+        p_post, p_pre, pho, pn, pc, ps, _stream_of(dev, stream, torch))
     if rc:
         raise IGError(rc, what)

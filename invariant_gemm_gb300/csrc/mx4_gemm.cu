@@ -364,23 +364,21 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   const int64_t per = (stages + S - 1) / S;
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
-  // Pairs where their tiles of 256 x 256 come to 32 or more, about half of the
-  // pairs: M = 512, N = K = 4096 (32 tiles) 10.8 us against 12.4 with 128-token
-  // tiles here, M = 256 (16) 10.7 against 8.6. With up to 128 tokens half of a
-  // pair's tile is empty, and it takes more of them: N = 8192 (32) 15.6 us
-  // against 13.0, N = 12288 (48) 11.4 against 13.1.
-  const int64_t pair_tiles = (p.N + 255) / 256 * ((p.M + 255) / 256);
-  if (p.M > 64 && pair_tiles >= (p.M > 128 ? 32 : 48))
+  // Blocks of 64 tokens here while all of them are at work at once, two to an
+  // SM: M = 256, N = K = 4096 (256 blocks) 8.1 us against 8.9 with 128 tokens and
+  // 10.7 in pairs; M = 333, N = 4104, K = 1056, FP32 (198) 6.1, 7.2, 8.0. Else
+  // pairs if their tiles of 256 x 256 come to 24, a third of the pairs: M = 512,
+  // N = K = 4096 (32 tiles) 10.9 us against 12.2 with 128 tokens here; M = 256, N
+  // = 4096, K = 11008 (16) 18.8 against 13.7.
+  const bool fit = (p.M + 63) / 64 * p.ntiles * p.S <= 2 * sm_count();
+  if (p.M > 64 && !fit && (p.N + 255) / 256 * ((p.M + 255) / 256) >= 24)
     return launch_mx4_gemm_pair(p, sm_count(), st);
   if (encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, kBM,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
     return cudaErrorInvalidValue;
   if (p.M <= 16) return launch_bn<16>(p, st);
   if (p.M <= 32) return launch_bn<32>(p, st);
-  // 64-token tiles while all of them are at work at once, two to an SM: M = 256,
-  // N = K = 4096 (256 blocks) 8.6 us against 8.9 with 128; K = 11008 (512) 18.2
-  // against 13.7.
-  if (p.M <= 64 || (p.M + 63) / 64 * p.ntiles * p.S <= 2 * sm_count()) return launch_bn<64>(p, st);
+  if (p.M <= 64 || fit) return launch_bn<64>(p, st);
   return launch_bn<128>(p, st);
 }
 
