@@ -17,8 +17,8 @@
 // a ring of copies (17 KB of weights to a stage), and with
 // IG_FLAG_STATIC_WEIGHTS the ring is filled while the kernel before ends.
 //
-// Warps: 0-3 put scale factors into tensor memory and take the sums out, 4
-// copies the weights, 6 the tokens, 5 issues the MMAs. Two warps copy because a
+// Warps: 0-3 take the sums out of tensor memory, 4 copies the weights, 6 the
+// tokens, 5 issues the MMAs. Two warps copy because a
 // thread takes about 60 cycles to issue a copy or an expected count: one alone
 // took 640 over a stage, which held a block at 46 GB/s.
 #include <algorithm>
@@ -40,7 +40,6 @@ constexpr int kMaxStages = 10;
 
 struct Ctl {
   uint64_t full[kMaxStages];
-  uint64_t sf_ready[kMaxStages];   // scales in tensor memory
   uint64_t empty[kMaxStages];
   uint64_t done;       // `consumed` is known, and the MMAs are complete
   uint64_t parts;      // the other blocks' sums (and the own ones) have come
@@ -49,15 +48,15 @@ struct Ctl {
   int32_t consumed;    // stages whose copies the MMA thread saw arrive
 };
 
-// Stage: W codes, x codes, W scales (2 tiles), x scales (2 tiles per 128 tokens).
-__host__ __device__ constexpr int sf_groups(int bn) { return (bn + 127) / 128; }
+// Stage: W codes, x codes, W scales (2 tiles), x scales (2 tiles). A token tile
+// (up to 128 tokens) lies in one scale row group of 128.
 __host__ __device__ constexpr int x_bytes(int bn) { return bn * kBK / 2; }
 __host__ __device__ constexpr int stage_bytes(int bn) {
-  return kWBytes + x_bytes(bn) + 2 * kMx4TileBytes * (1 + sf_groups(bn));
+  return kWBytes + x_bytes(bn) + 4 * kMx4TileBytes;
 }
 // tensor memory: the sums, then the scale factors of each stage
 __host__ __device__ constexpr int sf_col(int bn) { return bn < 32 ? 32 : bn; }
-__host__ __device__ constexpr int sf_cols(int bn) { return 8 * (1 + sf_groups(bn)); }
+constexpr int kSfCols = 16;
 // The parts' sums [S][groups of four tokens of this owner][128][4] FP32: BN *
 // 512 bytes, a little more where S does not divide the groups. Beside the ring
 // for up to 32 tokens; else in its place once every block of the cluster is
@@ -100,7 +99,6 @@ __device__ __forceinline__ void store4(T* y, int64_t ld, int n, bool in, int t0,
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ Mx4GemmParams p) {
-  constexpr int SG = sf_groups(BN);
   constexpr int kStage = stage_bytes(BN);
   static_assert(kStage % 1024 == 0, "swizzled tiles start at multiples of 1024 bytes");
   extern __shared__ uint8_t smem_raw[];
@@ -120,7 +118,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   const int64_t k1 = min(p.K, k0 + p.k_part);
   const int nk = (int)((k1 - k0 + kBK - 1) / kBK);
   const int tok = (int)min((int64_t)BN, p.M - m0);         // tokens of the tile
-  const int groups = (tok + 127) / 128;                    // their scale row groups
   const int share = share_of(BN, S);
   const int quads = (tok + 3) / 4;                         // groups of four tokens
   const int owned = quads > part ? (quads - part - 1) / S + 1 : 0;
@@ -128,7 +125,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&ctl->full[i], 2);
-      mbar_init(&ctl->sf_ready[i], 4);
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->done, 2);
@@ -155,12 +151,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     const bool early = w && (p.flags & IG_FLAG_STATIC_WEIGHTS) != 0;
     const CUtensorMap* map = w ? &p.tm_w : &p.tm_x;
     const int row = (int)(w ? n0 : m0);
-    const int sfs = w ? 1 : groups;                       // groups of scale rows
     const uint8_t* sf = (w ? p.ws : p.xs) + ((int64_t)(row >> 7) * p.kt + k0 / 128) * kMx4TileBytes;
-    const int64_t sf_pitch = p.kt * kMx4TileBytes;
     const uint32_t bytes = w ? kWBytes : x_bytes(BN);
     const int kc = (int)(k0 / 4);
-    const int ntile = (int)((k1 - k0 + 127) / 128);       // scale tiles of a group
+    const int ntile = (int)((k1 - k0 + 127) / 128);       // scale tiles
     if (leader) prefetch_tensormap(map);
     if (!early) griddep_wait();
     // The next kernel may start once every block is here, all work before this
@@ -175,11 +169,9 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         const uint32_t sfb = (2 * b + 1 < ntile ? 2 : 1) * kMx4TileBytes;
         uint8_t* st = ring + s * kStage;
         uint8_t* st_sf = st + kWBytes + x_bytes(BN);
-        mbar_arrive_expect_tx(&ctl->full[s], bytes + sfb * sfs);
+        mbar_arrive_expect_tx(&ctl->full[s], bytes + sfb);
         tma_load_2d(w ? st : st + kWBytes, map, kc + b * 64, row, &ctl->full[s]);
         bulk_g2s(w ? st_sf : st_sf + 2 * kMx4TileBytes, sf, sfb, &ctl->full[s]);
-        if (sfs == 2)
-          bulk_g2s(st_sf + 4 * kMx4TileBytes, sf + sf_pitch, sfb, &ctl->full[s]);
         sf += 2 * kMx4TileBytes;
       }
       if (++s == NST) {
@@ -193,7 +185,8 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc0 = umma_idesc_mx4(kBM, BN), idesc1 = umma_idesc_sf(idesc0, 2);
     const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
-                   xd = umma_desc_sw128(smem_u32(ring) + kWBytes);
+                   xd = umma_desc_sw128(smem_u32(ring) + kWBytes),
+                   sfd = sf_tile_desc(smem_u32(ring) + kWBytes + x_bytes(BN));
     // A column holds the scales of 32 rows, and a 64-token tile may start at
     // row 64 of its group of 128, two columns on. (An odd column is not a valid
     // start: 32-token tiles only ever start at row 0.)
@@ -203,18 +196,23 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     uint32_t parity = 0;
     for (; b < nk; ++b) {
       const bool expire = b == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT) != 0;
-      if (!warp_wait(&ctl->full[s], parity, p.status, expire ? 0 : 1ll << 31) ||
-          !warp_wait(&ctl->sf_ready[s], parity, p.status))
-        break;
+      if (!warp_wait(&ctl->full[s], parity, p.status, expire ? 0 : 1ll << 31)) break;
       tc_fence_after();
       const uint64_t w = wd + s * (kStage >> 4), x = xd + s * (kStage >> 4);
-      const uint32_t sfa = tmem + sf_col(BN) + s * sf_cols(BN), sfb = sfa + 8 + shift;
+      const uint64_t sf = sfd + s * (kStage >> 4);
+      const uint32_t sfa = tmem + sf_col(BN) + s * kSfCols, sfc = sfa + 8, sfb = sfc + shift;
       const int rem = (int)min((int64_t)kBK, k1 - k0 - (int64_t)b * kBK);
       if (leader) {
+        sf_tile_to_tmem(sfa, sf);
+        sf_tile_to_tmem(sfc, sf + 64);
         umma_mx4(tmem, w, x, idesc0, sfa, sfb, b > 0);
         if (rem > 64) umma_mx4(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
-        if (rem > 128) umma_mx4(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 4 * SG, true);
-        if (rem > 192) umma_mx4(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 4 * SG, true);
+        if (rem > 128) {
+          sf_tile_to_tmem(sfa + 4, sf + 32);
+          sf_tile_to_tmem(sfc + 4, sf + 96);
+          umma_mx4(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 4, true);
+        }
+        if (rem > 192) umma_mx4(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 4, true);
         umma_commit(&ctl->empty[s]);
       }
       __syncwarp();
@@ -231,18 +229,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     __syncwarp();
     griddep_wait();
   } else {
-    int s = 0;
-    uint32_t parity = 0;
-    for (int b = 0; b < nk; ++b) {
-      if (!warp_wait(&ctl->full[s], parity, p.status)) break;
-      sf_to_tmem<SG>(tmem + sf_col(BN) + s * sf_cols(BN), ring + s * kStage + kWBytes + x_bytes(BN),
-                     warp, lane);
-      if (lane == 0) mbar_arrive(&ctl->sf_ready[s]);
-      if (++s == NST) {
-        s = 0;
-        parity ^= 1;
-      }
-    }
     griddep_wait();
     ok = warp_wait(&ctl->done, 0, p.status) && ctl->consumed == nk;
     tc_fence_after();
@@ -320,7 +306,7 @@ cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
   const int room = (grid <= sm_count() ? 220 : 110) * 1024 - (own_sums(BN) ? sums : 0);
   const int64_t nk = p.k_part / kBK;
   p.stages = (int32_t)std::min<int64_t>({kMaxStages, room / stage_bytes(BN), nk});
-  const int cols = sf_col(BN) + p.stages * sf_cols(BN);
+  const int cols = sf_col(BN) + p.stages * kSfCols;
   p.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
   const int ring = p.stages * stage_bytes(BN);
   const int smem = 2048 + (own_sums(BN) ? ring + sums : std::max(ring, sums));
@@ -355,9 +341,9 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   p.ntiles = (int32_t)((p.N + kBM - 1) / kBM);
   // Parts of K: enough blocks for most SMs where the columns alone are few, and
   // no part under 8 stages, since the pairs of many tokens pay for each part.
-  // N = K = 4096, us for M = 1 / 256 / 4096: S = 1 5.4 / 8.9 / 27, S = 2 3.9 /
-  // 8.6 / 32, S = 4 3.5 / 9.7 / 35; N = 8192, K = 28672, M = 16 / 8192: 25.2 / 519,
-  // 21.4 / 521, 20.8 / 529.
+  // N = K = 4096, us for M = 1 / 256 / 4096: S = 1 5.2 / 7.7 / 27.6, S = 2 3.9 /
+  // 7.9 / 29.7, S = 4 3.4 / 9.6 / 35.8; N = 8192, K = 28672, M = 16 / 8192: 25.3 /
+  // 506, 21.4 / 505, 20.7 / 512.
   const int64_t stages = (p.K + kBK - 1) / kBK;
   int S = 1;
   while (S < 8 && (int64_t)p.ntiles * S < 96 && stages >= 16 * S) S *= 2;
@@ -365,8 +351,8 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
   // Blocks of 64 tokens here while all of them are at work at once, two to an
-  // SM: M = 256, N = K = 4096 (256 blocks) 8.1 us against 8.9 with 128 tokens and
-  // 10.7 in pairs; M = 333, N = 4104, K = 1056, FP32 (198) 6.1, 7.2, 8.0. Else
+  // SM: M = 256, N = K = 4096 (256 blocks) 7.9 us against 8.9 with 128 tokens and
+  // 10.7 in pairs; M = 333, N = 4104, K = 1056, FP32 (198) 6.0, 7.2, 8.0. Else
   // pairs if their tiles of 256 x 256 come to 24, a third of the pairs: M = 512,
   // N = K = 4096 (32 tiles) 10.9 us against 12.2 with 128 tokens here; M = 256, N
   // = 4096, K = 11008 (16) 18.8 against 13.7.

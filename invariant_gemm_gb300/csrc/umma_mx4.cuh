@@ -75,39 +75,6 @@ __device__ __forceinline__ void sf_tile_to_tmem(uint32_t taddr, uint64_t desc) {
                : "memory");
 }
 
-// 8 columns of this thread's lane <- two 16-byte vectors.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"r"(taddr), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                 "r"(b.z), "r"(b.w) : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Scale factors of a stage (256 k) from shared memory to tensor memory, by the
-// four warps of a warpgroup, each into its own 32 lanes: lane l of every
-// partition holds row l of each 512-byte tile. sf: 2 tiles of A, then 2 of
-// each of the G groups of 128 rows of B. Columns at dst: A, k 0-127 and
-// 128-255 (4 each); then B, all groups of k 0-127, all of k 128-255.
-template <int G>
-__device__ __forceinline__ void sf_to_tmem(uint32_t dst, const uint8_t* smem_sf, int warp,
-                                           int lane) {
-  constexpr int kTile = 512 / 16;
-  const uint4* sf = reinterpret_cast<const uint4*>(smem_sf) + lane;
-  dst += (uint32_t)((warp & 3) * 32) << 16;
-  tmem_st8(dst, sf[0], sf[kTile]);
-  if (G == 1) {
-    tmem_st8(dst + 8, sf[2 * kTile], sf[3 * kTile]);
-  } else {
-    tmem_st8(dst + 8, sf[2 * kTile], sf[4 * kTile]);
-    tmem_st8(dst + 16, sf[3 * kTile], sf[5 * kTile]);
-  }
-  tmem_st_wait();
-  tc_fence_before();
-  __syncwarp();
-}
-
 // One block-scaled MMA (issued by a single thread): D = A B^T (+ D).
 __device__ __forceinline__ void umma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
