@@ -351,11 +351,11 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
   // Blocks of 64 tokens here while all of them are at work at once, two to an
-  // SM: M = 256, N = K = 4096 (256 blocks) 7.9 us against 8.9 with 128 tokens and
+  // SM: M = 256, N = K = 4096 (256 blocks) 7.8 us against 8.5 with 128 tokens and
   // 10.7 in pairs; M = 333, N = 4104, K = 1056, FP32 (198) 6.0, 7.2, 8.0. Else
   // pairs if their tiles of 256 x 256 come to 24, a third of the pairs: M = 512,
   // N = K = 4096 (32 tiles) 10.9 us against 12.2 with 128 tokens here; M = 256, N
-  // = 4096, K = 11008 (16) 18.8 against 13.7.
+  // = 4096, K = 11008 (16) 19.0 against 13.3.
   const bool fit = (p.M + 63) / 64 * p.ntiles * p.S <= 2 * sm_count();
   if (p.M > 64 && !fit && (p.N + 255) / 256 * ((p.M + 255) / 256) >= 24)
     return launch_mx4_gemm_pair(p, sm_count(), st);
