@@ -17,7 +17,8 @@
 // per SM and less work per row; few rows are over sooner with W = 1
 // (launch_block_norm has the figures). Copying rows ahead through shared memory by
 // blocks that stay (cp.async, 3 rows deep) was slower than fresh blocks: 107
-// against 87 us at 8192 x 8192.
+// against 87 us at 8192 x 8192 (bf16, 537 MB: 6.1 TB/s; FP32 rows 121 us, 6.7
+// TB/s; 1001 x 11008 FP32 with a gate for each value 28 us, 5.5 TB/s).
 //
 // The next kernel on the stream starts when this one is complete (no early
 // release): it may be one that reads n before its own wait, as the fused LoRA
