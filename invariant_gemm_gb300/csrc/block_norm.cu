@@ -7,7 +7,8 @@
 //
 // The order of the sums is fixed by H: a row has `slots` places for vectors,
 // cut into V runs of T places; the values of the vectors at places t, t + T,
-// ... are added one after the other (t < T), the T sums by a butterfly over
+// ... are added one after the other (t < T; even and odd values apart, then
+// together), the T sums by a butterfly over
 // each 32 of them, then one over those. A thread does this for one t, or, in
 // blocks of half the size, for two (W = 2) that lie T / 2 apart and so in
 // different groups of 32: the same sums, the same bits.
