@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "MODE_DET", "MODE_ATOMIC", "MODE_UNSPLIT", "MODE_DET_TREE", "PATH_AUTO", "PATH_WARP", "PATH_MMA", "PATH_FMA",
@@ -105,6 +106,10 @@ class NormShape(ctypes.Structure):
     ]
 
 
+# The same structs as bytes: half the time of a ctypes.Structure.
+_MX4_SHAPE = struct.Struct("qqqqii").pack
+_NORM_SHAPE = struct.Struct("qqqqqqqiiiff").pack
+
 _LIB = None
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(Shape)
@@ -152,10 +157,10 @@ def lib() -> ctypes.CDLL:
         L.ig_mx4_dequantize.restype = ctypes.c_int
         L.ig_mx4_dequantize.argtypes = [i64, i64, _P, _P, _P, i64, ctypes.c_int, _P]
         L.ig_mx4_gemm.restype = ctypes.c_int
-        L.ig_mx4_gemm.argtypes = [ctypes.POINTER(Mx4Shape), _P, _P, _P, _P, _P, _P,
-                                  ctypes.c_size_t, _P]
+        # the shape: Mx4Shape / NormShape by reference, or their bytes
+        L.ig_mx4_gemm.argtypes = [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.ig_block_norm.restype = ctypes.c_int
-        L.ig_block_norm.argtypes = [ctypes.POINTER(NormShape)] + [_P] * 10
+        L.ig_block_norm.argtypes = [_P] * 11
         _LIB = L
     return _LIB
 
@@ -373,7 +378,7 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
     _packed(what, "w", w_codes, w_scales, dev, u8, N, half)
     if not (ws.dtype is u8 and ws.is_contiguous() and ws.get_device() == dev):
         _flat(what, "ws", ws, dev, u8, 0)
-    rc = (_LIB or lib()).ig_mx4_gemm(Mx4Shape(M, N, 2 * half, ld, t, flags), x_codes.data_ptr(),
+    rc = (_LIB or lib()).ig_mx4_gemm(_MX4_SHAPE(M, N, 2 * half, ld, t, flags), x_codes.data_ptr(),
                                      x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                                      y.data_ptr(), ws.data_ptr(), ws.numel(),
                                      _stream_of(dev, stream, torch))
@@ -453,7 +458,7 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
         _packed(what, "n", codes, scales, dev, torch.uint8, M, (H + 1) >> 1)
         pc, ps = codes.data_ptr(), scales.data_ptr()
     rc = (_LIB or lib()).ig_block_norm(
-        NormShape(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale), ph, py, pg,
+        _NORM_SHAPE(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale), ph, py, pg,
         p_post, p_pre, pho, pn, pc, ps, _stream_of(dev, stream, torch))
     if rc:
         raise IGError(rc, what)

@@ -425,3 +425,12 @@ def test_binding_refuses_wrong_tensors():
                 lambda: ig.mx4_gemm(c, s, c[:, :16], s, torch.zeros(4, 4, dtype=b16), s)):
         with pytest.raises(ig.IGError):
             bad()
+
+
+def test_packed_shapes_are_the_structs():
+    """The bytes the binding hands over are those of the declared structs."""
+    a = bytes(ig.Mx4Shape(3, 64, 128, 72, 1, 1))
+    assert ig._MX4_SHAPE(3, 64, 128, 72, 1, 1) == a
+    b = bytes(ig.NormShape(3, 64, 72, 80, 88, 96, 104, 1, 1, 1, 1e-5, 0.5))
+    packed = ig._NORM_SHAPE(3, 64, 72, 80, 88, 96, 104, 1, 1, 1, 1e-5, 0.5)
+    assert packed == b[:len(packed)]
