@@ -74,6 +74,8 @@ int ig_mx4_dequantize(int64_t rows, int64_t K, const void* codes, const void* sc
   p.K = K;
   p.ldo = ld_out;
   p.kt = mx4_ktiles(K);
+  const int64_t pitch = ld_out * (out_type == IG_TYPE_F32 ? 4 : 2);
+  p.wide = (reinterpret_cast<uintptr_t>(out) % 32 == 0) && (rows == 1 || pitch % 32 == 0);
   return cuda_status(launch_mx4_dequantize(p, out_type == IG_TYPE_F32,
                                            static_cast<cudaStream_t>(stream)));
 }

@@ -43,6 +43,7 @@ struct Mx4DequantParams {
   const uint8_t* scales;
   void* out;
   int64_t rows, K, ldo, kt;
+  bool wide;           // every row of out starts at a multiple of 32 bytes
 };
 
 struct Mx4GemmParams {

@@ -7,7 +7,7 @@
 // too; all of a thread's loads are in flight before the first is used. The
 // lanes of four blocks hold the 4 bytes of a word of the scale tile, and one
 // of them stores it. 8192 x 28672: bf16 88 us (6.8 TB/s), FP32 150 us (7.1 TB/s),
-// back to bf16 98 us (6.0 TB/s).
+// back to bf16 90 us (6.6 TB/s).
 #include "mx4.cuh"
 
 namespace ig {
@@ -115,34 +115,52 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(Mx4QuantParams p) {
   }
 }
 
+// 32 bytes to a 32-byte boundary in one store, or to a 16-byte boundary in two
+// (which leaves each sector half written in between: 8192 x 28672 90 us against
+// 97). `wide` is the same for the whole grid.
+__device__ __forceinline__ void store32(void* at, const uint4& a, const uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(at), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z),
+                   "r"(b.w) : "memory");
+  } else {
+    static_cast<uint4*>(at)[0] = a;
+    static_cast<uint4*>(at)[1] = b;
+  }
+}
+
 template <typename T, int U>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(Mx4DequantParams p) {
-  const Walk<U, 8> start(p.kt);
-  const uint32_t groups = (uint32_t)(p.K / 8);
+  constexpr int G = Raw<T>::kValues, kLanes = kMx4Block / G;
+  const Walk<U, G> start(p.kt);
+  const uint32_t groups = (uint32_t)(p.K / G);
   griddep_wait();
-  uint32_t codes[U], byte[U];
-  Walk<U, 8> w = start;
+  uint2 codes[U];              // .y for bf16 only
+  uint32_t byte[U];
+  Walk<U, G> w = start;
 #pragma unroll
   for (int j = 0; j < U; ++j, w.next()) {
-    codes[j] = byte[j] = 0;
+    codes[j] = make_uint2(0, 0);
+    byte[j] = 0;
     if (w.row >= p.rows || w.c >= groups) continue;
-    codes[j] = __ldcs(reinterpret_cast<const uint32_t*>(p.codes) + w.row * groups + w.c);
-    byte[j] = p.scales[mx4_scale_at(w.row, w.c / 4, p.kt)];
+    const uint8_t* at = p.codes + (w.row * groups + w.c) * (G / 2);
+    if constexpr (G == 16) codes[j] = __ldcs(reinterpret_cast<const uint2*>(at));
+    else codes[j].x = __ldcs(reinterpret_cast<const uint32_t*>(at));
+    byte[j] = p.scales[mx4_scale_at(w.row, w.c / kLanes, p.kt)];
   }
   w = start;
 #pragma unroll
   for (int j = 0; j < U; ++j, w.next()) {
     if (w.row >= p.rows || w.c >= groups) continue;
-    const uint4 v = mx4_decode8(codes[j], byte[j]);
-    T* o = static_cast<T*>(p.out) + w.row * p.ldo + (int64_t)w.c * 8;
-    if constexpr (sizeof(T) == 4) {
-      float f[8];
-      unpack8(v, f);
-      reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    T* o = static_cast<T*>(p.out) + w.row * p.ldo + (int64_t)w.c * G;
+    uint4 a = mx4_decode8(codes[j].x, byte[j]), b;
+    if constexpr (G == 16) {
+      b = mx4_decode8(codes[j].y, byte[j]);
     } else {
-      *reinterpret_cast<uint4*>(o) = v;
+      b = make_uint4(a.z << 16, a.z & 0xffff0000u, a.w << 16, a.w & 0xffff0000u);
+      a = make_uint4(a.x << 16, a.x & 0xffff0000u, a.y << 16, a.y & 0xffff0000u);
     }
+    store32(o, a, b, p.wide);
   }
 }
 
@@ -159,15 +177,15 @@ cudaError_t launch(void (*several)(P), void (*one)(P), const P& p, cudaStream_t 
   return launch_pdl(many ? several : one, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
 }
 
-// Two groups (of 16 bf16 values) there, four (of 8) back: 4095 x 11008 19.5 us
-// with two, 20.7 with four; back 22.6 and 21.2.
+// Two groups a thread: 4095 x 11008 19.5 us with two, 20.7 with four; back 19.2
+// and 19.5.
 template <typename T>
 cudaError_t quantize(const Mx4QuantParams& p, cudaStream_t st) {
   return launch<2, Raw<T>::kValues>(quantize_kernel<T, 2>, quantize_kernel<T, 1>, p, st);
 }
 template <typename T>
 cudaError_t dequantize(const Mx4DequantParams& p, cudaStream_t st) {
-  return launch<4, 8>(dequantize_kernel<T, 4>, dequantize_kernel<T, 1>, p, st);
+  return launch<2, Raw<T>::kValues>(dequantize_kernel<T, 2>, dequantize_kernel<T, 1>, p, st);
 }
 
 }  // namespace
