@@ -18,8 +18,9 @@
 // per SM and less work per row; few rows are over sooner with W = 1
 // (launch_block_norm has the figures). Copying rows ahead through shared memory by
 // blocks that stay (cp.async, 3 rows deep) was slower than fresh blocks: 107
-// against 87 us at 8192 x 8192 (bf16, 537 MB: 6.1 TB/s; FP32 rows 121 us, 6.7
-// TB/s; 1001 x 11008 FP32 with a gate for each value 28 us, 5.5 TB/s).
+// against 87 us at 8192 x 8192, which now takes 82 us (bf16, 537 MB: 6.5 TB/s);
+// 1001 x 11008 FP32 with a gate for each value 30 us (5.1 TB/s), 4000 of those
+// rows 96 us (6.4 TB/s).
 //
 // The next kernel on the stream starts when this one is complete (no early
 // release): it may be one that reads n before its own wait, as the fused LoRA
@@ -321,10 +322,10 @@ cudaError_t launch(const NormParams& p, int threads, cudaStream_t st) {
 
 // V = 2 up to H = 16384, V = 4 to 32768 (always 1024 threads at most). Two sums
 // a thread from where the rows at one a thread would not all be at work at
-// once (1024 threads an SM): rows of 8192, bf16: 256 of them 5.6 us with one,
-// 7.5 with two; 600 of them 10.7 and 9.2; 8192 of them 113 and 87. Short rows
-// (T < 256: 8192 x 1024 17.1 against 19.0 us) and V = 4 (1000 x 32768: 59.8
-// against 66.6 us) keep one.
+// once (1024 threads an SM). bf16 rows of 8192: 304 of them 6.2 us with one, 7.3
+// with two; 608 of them 10.8 and 10.0; FP32 rows of 11008: 152 of them 7.6 and
+// 7.6, 608 of them 25.1 and 18.4. Short rows (T < 256) keep one: 608 of 2048
+// 4.6 and 6.0; so do those of V = 4, whose two sums would not fit the registers.
 template <bool F32>
 cudaError_t launch_rows(const NormParams& p, cudaStream_t st) {
   const int V = p.H <= 16384 ? 2 : 4;
