@@ -21,9 +21,9 @@
 // bytes.
 //
 // Warps: 0-3 take the sums out of tensor memory, 4 copies the weights, 6 the
-// tokens, 5 issues the MMAs. Two warps copy because a
-// thread takes about 60 cycles to issue a copy or an expected count: one alone
-// took 640 over a stage, which held a block at 46 GB/s.
+// tokens, 5 issues the MMAs. Two warps copy because the tokens wait for the
+// kernel before and static weights do not: with both after that wait M = 1, N =
+// K = 4096 takes 4.7 us.
 #include <algorithm>
 #include <atomic>
 

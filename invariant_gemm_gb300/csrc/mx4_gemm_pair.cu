@@ -8,10 +8,9 @@
 // products. Both blocks keep 128 x 256 sums in tensor memory.
 //
 // Warps: 0-15 take the sums out of tensor memory (32 lanes and a quarter of
-// the columns each), 16 copies codes, 17 scales, 18 (of the first block) issues
-// the MMAs. The sums of a part of K go to registers at once (64 a thread) and
-// tensor memory is free again: the stores of a tile run beside the products of
-// the next.
+// the columns each), 16 copies, 17 (of the first block) issues the MMAs. The
+// sums of a part of K go to registers at once (64 a thread) and tensor memory is
+// free again: the stores of a tile run beside the products of the next.
 //
 // Bound by the tensor cores, and they by the board's power: M = N = 8192, K =
 // 28672 509 us (7.6 PFLOP/s), 98% of the cycles in MMAs at 128 cycles each (K =
@@ -35,8 +34,8 @@ constexpr int kStage = 2 * kHalf + 6 * kMx4TileBytes;   // w, x, w scales (2 til
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 16;
 constexpr int kCols = kBT / (kEpiWarps / 4);   // token columns per warp
-constexpr int kCopyWarp = kEpiWarps, kCopySfWarp = kEpiWarps + 1, kMmaWarp = kEpiWarps + 2;
-constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr int kCopyWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr uint32_t kSfCol = 256;         // tensor memory: sums 0-255, then scales
 constexpr uint32_t kSfCols = 8 + 16;     // per stage: w 2 x 4, x 2 x 8
 constexpr uint32_t kTmemCols = 512;
@@ -152,7 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&ctl->full[i], 2);
+      mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->sums_full, 1);
@@ -177,34 +176,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t first = blockIdx.x / 2;
   const int64_t total = first < tiles ? (int64_t)((tiles - first - 1) / pairs + 1) * nkb : 0;
 
-  // Copies: one warp for the codes, one for the scales, since a thread takes
-  // about 60 cycles to issue a copy or an expected count, and one alone would
-  // take longer over a stage than its MMAs do. Whole warps go through the
-  // loops and one lane issues.
+  // Copies. The whole warp goes through the loops and one lane issues: code
+  // that the compiler knows to be uniform issues a copy in a few cycles, and a
+  // second warp for the scales would gain nothing.
   if (warp == kCopyWarp) {
-    const bool leader = elect_one();
-    const uint32_t bar0 = map_rank(ctl->full, 0);
-    bool ok = true;
-    Slot at;
-    for (uint32_t i = first; i < tiles && ok; i += pairs) {
-      const Tile t = tile_at(i, nt, mt);
-      const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
-      for (int kb = 0; kb < nkb; ++kb, at.next()) {
-        // a stage's first use finds its barrier in the phase before: parity 1 passes
-        if (!warp_wait(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
-          ok = false;
-          break;
-        }
-        if (leader) {
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 4 * kHalf);
-          uint8_t* st = ring + at.s * kStage;
-          tma_load_pair(st, &p.tm_w, kb * 64, wr, bar0 + 8 * at.s);
-          tma_load_pair(st + kHalf, &p.tm_x, kb * 64, xr, bar0 + 8 * at.s);
-        }
-      }
-    }
-    if (!ok && leader) ctl->fail = 1;
-  } else if (warp == kCopySfWarp) {
     const bool leader = elect_one();
     const uint32_t bar0 = map_rank(ctl->full, 0);
     const int kt = (int)p.kt;
@@ -212,20 +187,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Slot at;
     for (uint32_t i = first; i < tiles && ok; i += pairs) {
       const Tile t = tile_at(i, nt, mt);
+      const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
       // scale tiles, as rows of the maps; rows past the last one (of rows of
       // the operands that do not exist) are filled with zeros
       int wrow = ((t.n0 >> 7) + (int)rank) * kt, xrow = (t.m0 >> 7) * kt;
       for (int kb = 0; kb < nkb; ++kb, at.next(), wrow += 2, xrow += 2) {
+        // a stage's first use finds its barrier in the phase before: parity 1 passes
         if (!warp_wait(&ctl->empty[at.s], at.parity ^ 1, p.status)) {
           ok = false;
           break;
         }
         if (leader) {
-          uint8_t* sf = ring + at.s * kStage + 2 * kHalf;
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 12 * kMx4TileBytes);
-          tma_load_pair(sf, &p.tm_ws, 0, wrow, bar0 + 8 * at.s);
-          tma_load_pair(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, bar0 + 8 * at.s);
-          tma_load_pair(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, bar0 + 8 * at.s);
+          const uint32_t full = bar0 + 8 * at.s;
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 2 * kStage);
+          uint8_t* st = ring + at.s * kStage;
+          uint8_t* sf = st + 2 * kHalf;
+          tma_load_pair(st, &p.tm_w, kb * 64, wr, full);
+          tma_load_pair(st + kHalf, &p.tm_x, kb * 64, xr, full);
+          tma_load_pair(sf, &p.tm_ws, 0, wrow, full);
+          tma_load_pair(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, full);
+          tma_load_pair(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, full);
         }
       }
     }
