@@ -48,7 +48,7 @@ struct Mx4DequantParams {
 
 struct Mx4GemmParams {
   CUtensorMap tm_w;    // codes as [N][K / 4] 2-byte words, box 64 x 128, 128-byte swizzle
-  CUtensorMap tm_x;    // codes as [M][K / 4] 2-byte words, box 64 x BN (pairs: 128), 128-byte swizzle
+  CUtensorMap tm_x;    // codes as [M][K / 4] 2-byte words, box 64 x BN (pairs: 64), 128-byte swizzle
   CUtensorMap tm_ws, tm_xs;   // scale tiles as rows of 256 2-byte words, box 256 x 2 (pairs)
   const uint8_t* xc;
   const uint8_t* xs;

@@ -13,10 +13,10 @@
 // free again: the stores of a tile run beside the products of the next.
 //
 // Bound by the tensor cores, and they by the board's power: M = N = 8192, K =
-// 28672 509 us (7.6 PFLOP/s), 98% of the cycles in MMAs at 128 cycles each (K =
-// 64), at a clock of about 1.5 GHz; M = 4096, K = 4096, N = 12288 65 us, 84% of the
-// cycles (about 900 from a tile's last MMA to the next tile's first, and 11
-// rounds of tiles for 10.1 of work).
+// 28672 498 us (7.7 PFLOP/s), 98% of the cycles in MMAs at 128 cycles each (K =
+// 64), at a clock of about 1.5 GHz; M = 4096, K = 4096, N = 12288 64 us, 84% of the
+// cycles (about 900 from a tile's last MMA to the next tile's first, and 10.1
+// rounds of tiles).
 #include <atomic>
 
 #include "mx4.cuh"
@@ -31,6 +31,7 @@ constexpr int kBT = 256;                 // tokens per tile (128 rows of codes p
 constexpr int kBK = 256;                 // k per stage
 constexpr int kHalf = 128 * kBK / 2;     // codes of 128 rows
 constexpr int kStage = 2 * kHalf + 6 * kMx4TileBytes;   // w, x, w scales (2 tiles), x scales (4)
+constexpr int kHalfStage = kStage - kHalf / 2 - 2 * kMx4TileBytes;      // with 128 tokens
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 16;
 constexpr int kCols = kBT / (kEpiWarps / 4);   // token columns per warp
@@ -122,17 +123,21 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 
 struct Tile {
   int n0, m0;
+  int rows;        // of its token rows, those that each block copies: 128 or 64
 };
 
-// Tile i: token tiles in groups of kGroup; within a group all column tiles,
-// each with the group's token tiles, so that the pairs at work at a time share
-// both operands in L2.
-__device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t nt, uint32_t mt) {
+// Piece i: tile i, and from `whole` on half a tile, 128 tokens. Token tiles in
+// groups of kGroup; within a group all column tiles, each with the group's
+// token tiles, so that the pairs at work at a time share both operands in L2.
+__device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t whole, uint32_t nt, uint32_t mt) {
+  const uint32_t half = i < whole ? 0 : (i - whole) & 1;
+  const int rows = i < whole ? kBT / 2 : kBT / 4;
+  if (i >= whole) i = whole + (i - whole) / 2;
   const uint32_t per = kGroup * nt;
   const uint32_t g = i / per, r = i - g * per;
   const uint32_t gm = min((uint32_t)kGroup, mt - g * kGroup);
   const uint32_t n = r / gm;
-  return {(int)(n * kBN), (int)((g * kGroup + (r - n * gm)) * kBT)};
+  return {(int)(n * kBN), (int)((g * kGroup + (r - n * gm)) * kBT + half * (kBT / 2)), rows};
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -145,7 +150,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   const uint32_t rank = uniform(cluster_rank());
   const uint32_t nt = (uint32_t)((p.N + kBN - 1) / kBN), mt = (uint32_t)((p.M + kBT - 1) / kBT);
-  const uint32_t tiles = nt * mt, pairs = gridDim.x / 2;
+  // The last round of tiles, if it would give work to no more than half the
+  // pairs, is cut into half tiles, which take three quarters of the time (us
+  // before -> after: M = 384, K = 11008, N = 4096, 32 tiles 19.1 -> 16.4; M = N =
+  // K = 4096, 256 tiles 28.9 -> 28.4; M = N = 8192, K = 28672 504 -> 498). The
+  // bits stay: a sum's order is that of k alone.
+  const uint32_t pairs = gridDim.x / 2, rest = nt * mt % pairs;
+  const uint32_t whole = nt * mt - (2 * rest <= pairs ? rest : 0);
+  const uint32_t pieces = whole + 2 * (nt * mt - whole);
   // k-blocks (stages) of a tile and of a part of K
   const int nkb = (int)((p.K + kBK - 1) / kBK), per_part = (int)(p.k_part / kBK);
 
@@ -172,9 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch();
 
-  // this pair's tiles, and their stages one after the other
+  // this pair's pieces, and their stages one after the other
   const uint32_t first = blockIdx.x / 2;
-  const int64_t total = first < tiles ? (int64_t)((tiles - first - 1) / pairs + 1) * nkb : 0;
+  const int64_t total = first < pieces ? (int64_t)((pieces - first - 1) / pairs + 1) * nkb : 0;
 
   // Copies. The whole warp goes through the loops and one lane issues: code
   // that the compiler knows to be uniform issues a copy in a few cycles, and a
@@ -185,9 +197,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int kt = (int)p.kt;
     bool ok = true;
     Slot at;
-    for (uint32_t i = first; i < tiles && ok; i += pairs) {
-      const Tile t = tile_at(i, nt, mt);
-      const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + 128 * (int)rank;
+    for (uint32_t i = first; i < pieces && ok; i += pairs) {
+      const Tile t = tile_at(i, whole, nt, mt);
+      const int wr = t.n0 + 128 * (int)rank, xr = t.m0 + t.rows * (int)rank;
+      const bool full_tile = t.rows == 128;
       // scale tiles, as rows of the maps; rows past the last one (of rows of
       // the operands that do not exist) are filled with zeros
       int wrow = ((t.n0 >> 7) + (int)rank) * kt, xrow = (t.m0 >> 7) * kt;
@@ -199,28 +212,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (leader) {
           const uint32_t full = bar0 + 8 * at.s;
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[at.s], 2 * kStage);
+          if (rank == 0)
+            mbar_arrive_expect_tx(&ctl->full[at.s], 2 * (full_tile ? kStage : kHalfStage));
           uint8_t* st = ring + at.s * kStage;
           uint8_t* sf = st + 2 * kHalf;
           tma_load_pair(st, &p.tm_w, kb * 64, wr, full);
           tma_load_pair(st + kHalf, &p.tm_x, kb * 64, xr, full);
+          if (full_tile) tma_load_pair(st + kHalf + kHalf / 2, &p.tm_x, kb * 64, xr + 64, full);
           tma_load_pair(sf, &p.tm_ws, 0, wrow, full);
           tma_load_pair(sf + 2 * kMx4TileBytes, &p.tm_xs, 0, xrow, full);
-          tma_load_pair(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, full);
+          if (full_tile) tma_load_pair(sf + 4 * kMx4TileBytes, &p.tm_xs, 0, xrow + kt, full);
         }
       }
     }
     if (!ok && leader) ctl->fail = 1;
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
-      constexpr uint32_t idesc0 = umma_idesc_mx4(256, kBT), idesc1 = umma_idesc_sf(idesc0, 2);
+      constexpr uint32_t of_tile = umma_idesc_mx4(256, kBT), of_half = umma_idesc_mx4(256, kBT / 2);
       const uint64_t wd = umma_desc_sw128(smem_u32(ring)),
                      xd = umma_desc_sw128(smem_u32(ring) + kHalf),
                      sfd = sf_tile_desc(smem_u32(ring) + 2 * kHalf);
       const bool leader = elect_one();
       Slot at;
       int kb = 0, part_end = 0;
-      uint32_t part = 0;
+      uint32_t part = 0, i = first;
       bool ok = true;
       for (int64_t it = 0; it < total; ++it, at.next()) {
         const bool begin = kb == part_end || kb == 0;
@@ -235,18 +250,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t w = wd + at.s * (kStage >> 4), x = xd + at.s * (kStage >> 4);
         const uint32_t sfa = tmem + kSfCol + at.s * kSfCols, sfb = sfa + 8;
         const int rem = (int)min((int64_t)kBK, p.K - (int64_t)kb * kBK);
-        const bool end = kb + 1 == part_end;
+        const bool end = kb + 1 == part_end, full_tile = i < whole;
+        const uint32_t idesc0 = full_tile ? of_tile : of_half, idesc1 = umma_idesc_sf(idesc0, 2);
         const uint64_t sf = sfd + at.s * (kStage >> 4);      // tiles w0 w1 x0 x0' x1 x1'
         if (leader) {
           sf_tile_to_tmem_pair(sfa, sf);
           sf_tile_to_tmem_pair(sfb, sf + 64);
-          sf_tile_to_tmem_pair(sfb + 4, sf + 128);
+          if (full_tile) sf_tile_to_tmem_pair(sfb + 4, sf + 128);
           umma_mx4_pair(tmem, w, x, idesc0, sfa, sfb, !begin);
           if (rem > 64) umma_mx4_pair(tmem, w + 2, x + 2, idesc1, sfa, sfb, true);
           if (rem > 128) {
             sf_tile_to_tmem_pair(sfa + 4, sf + 32);
             sf_tile_to_tmem_pair(sfb + 8, sf + 96);
-            sf_tile_to_tmem_pair(sfb + 12, sf + 160);
+            if (full_tile) sf_tile_to_tmem_pair(sfb + 12, sf + 160);
             umma_mx4_pair(tmem, w + 4, x + 4, idesc0, sfa + 4, sfb + 8, true);
           }
           if (rem > 192) umma_mx4_pair(tmem, w + 6, x + 6, idesc1, sfa + 4, sfb + 8, true);
@@ -257,7 +273,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++kb;
         if (end) {
           ++part;
-          if (kb == nkb) kb = 0;
+          if (kb == nkb) {
+            kb = 0;
+            i += pairs;
+          }
         }
       }
       if (!ok && leader) ctl->fail = 1;
@@ -268,8 +287,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
     uint32_t part = 0;
     bool ok = true;
-    for (uint32_t i = first; i < tiles && ok; i += pairs) {
-      const Tile t = tile_at(i, nt, mt);
+    for (uint32_t i = first; i < pieces && ok; i += pairs) {
+      const Tile t = tile_at(i, whole, nt, mt);
+      const bool mine = c0 < 2 * t.rows;       // the upper columns are not there in half a tile
       float acc[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
@@ -281,6 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kCols / 8; ++c) {
+          if (!mine) break;
           float v[8];
           tmem_ld8(src + 8 * c, v);
 #pragma unroll
@@ -297,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // over tiles would cost the registers that hold the sums
       int64_t ld = p.ldy;
       asm volatile("" : "+l"(ld));
-      const int left = (int)min((int64_t)kCols, p.M - m);    // tokens of these columns
+      const int left = mine ? (int)min((int64_t)kCols, p.M - m) : 0;   // tokens of these columns
       if (p.y_f32) {
         float* y = static_cast<float*>(p.y) + m * ld + n + lane;
         if (n + lane < p.N) {
@@ -340,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st) {
   const uint64_t words = (uint64_t)p.K / 4, row = (uint64_t)p.K / 2;
   const uint64_t wt = (uint64_t)((p.N + 127) / 128 * p.kt), xt = (uint64_t)((p.M + 127) / 128 * p.kt);
-  if (encode_map_2d(&p.tm_x, p.xc, (uint64_t)p.M, words, row, 64, 128,
+  if (encode_map_2d(&p.tm_x, p.xc, (uint64_t)p.M, words, row, 64, 64,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK ||
       encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, words, row, 64, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK ||
@@ -354,7 +375,8 @@ cudaError_t launch_mx4_gemm_pair(Mx4GemmParams& p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = (p.N + kBN - 1) / kBN * ((p.M + kBT - 1) / kBT);
   if (tiles > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
-  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  const int64_t pieces = 2 * tiles <= sms / 2 ? 2 * tiles : tiles;   // half tiles, if they all fit
+  const int64_t pairs = pieces < sms / 2 ? pieces : sms / 2;
   return launch_pdl(gemm_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, st, p);
 }
 
