@@ -344,6 +344,32 @@ cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Which kernel is through soonest with more than 64 tokens, by a start and so
+// much for each stage of K in hundredths of a microsecond (fitted to the times
+// of 35 sizes, M 192-10000, N 128-12288, K 288-28672, within 20%). Here, the
+// blocks of an SM count one by one, which has two at a time: tiles of 64 tokens
+// only while all are at work at once; of 128 in waves (a last tile of up to 64
+// tokens counts half). Pairs: rounds of tiles, 24 a stage for a last round of
+// half tiles. us with 64 / 128 / pairs: M = 256, N = K = 4096 7.8 / 8.5 / 9.2; M
+// = 192, K = 28672, N = 12288 43.5 / - / 40.1; 128 / pairs: M = 384, K = 4096, N =
+// 2560 7.6 / 9.0; M = 512 11.0 / 9.3; M = 400, K = 11008 13.6 / 15.5; M = 512 19.8 /
+// 15.8; M = 900, K = 28672, N = 520 19.5 / 31.2.
+enum class Kind { k64, k128, kPairs };
+Kind soonest(const Mx4GemmParams& p, int64_t stages, int64_t per) {
+  const int64_t sms = sm_count(), pairs = sms / 2, halves = (p.M + 63) / 64;
+  auto deep = [&](int64_t blocks) {
+    return blocks > sms ? (blocks + 2 * sms - 1) / (2 * sms) * 2 : 1;
+  };
+  const int64_t b64 = halves * p.ntiles * p.S, b128 = (b64 + 1) / 2;
+  const int64_t tiles = (p.N + 255) / 256 * ((p.M + 255) / 256), rest = tiles % pairs;
+  const int64_t t64 = 420 + 18 * deep(b64) * per;
+  const int64_t t128 = 300 + deep(b128) * (130 + 35 * per);
+  const int64_t tpair =
+      540 + (33 * (tiles / pairs) + (rest == 0 ? 0 : 2 * rest <= pairs ? 24 : 33)) * stages;
+  if (b64 <= 2 * sms && t64 <= std::min(t128, tpair)) return Kind::k64;
+  return t128 <= tpair ? Kind::k128 : Kind::kPairs;
+}
+
 }  // namespace
 
 cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
@@ -359,21 +385,14 @@ cudaError_t launch_mx4_gemm(Mx4GemmParams& p, cudaStream_t st) {
   const int64_t per = (stages + S - 1) / S;
   p.k_part = per * kBK;
   p.S = (int32_t)((stages + per - 1) / per);   // no part is empty
-  // Blocks of 64 tokens here while all of them are at work at once, two to an
-  // SM: M = 256, N = K = 4096 (256 blocks) 7.8 us against 8.5 with 128 tokens and
-  // 10.7 in pairs; M = 333, N = 4104, K = 1056, FP32 (198) 6.0, 7.2, 8.0. Else
-  // pairs if their tiles of 256 x 256 come to 24, a third of the pairs: M = 512,
-  // N = K = 4096 (32 tiles) 10.9 us against 12.2 with 128 tokens here; M = 256, N
-  // = 4096, K = 11008 (16) 19.0 against 13.3.
-  const bool fit = (p.M + 63) / 64 * p.ntiles * p.S <= 2 * sm_count();
-  if (p.M > 64 && !fit && (p.N + 255) / 256 * ((p.M + 255) / 256) >= 24)
-    return launch_mx4_gemm_pair(p, sm_count(), st);
+  const Kind kind = p.M > 64 ? soonest(p, stages, per) : Kind::k64;
+  if (kind == Kind::kPairs) return launch_mx4_gemm_pair(p, sm_count(), st);
   if (encode_map_2d(&p.tm_w, p.wc, (uint64_t)p.N, (uint64_t)p.K / 4, (uint64_t)p.K / 2, 64, kBM,
                     CU_TENSOR_MAP_SWIZZLE_128B) != IG_OK)
     return cudaErrorInvalidValue;
   if (p.M <= 16) return launch_bn<16>(p, st);
   if (p.M <= 32) return launch_bn<32>(p, st);
-  if (p.M <= 64 || fit) return launch_bn<64>(p, st);
+  if (kind == Kind::k64) return launch_bn<64>(p, st);
   return launch_bn<128>(p, st);
 }
 
