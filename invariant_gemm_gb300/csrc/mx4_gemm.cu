@@ -11,7 +11,9 @@
 // part is a block here, the S blocks of a tile a cluster: each sends its sums,
 // four tokens at a time, to the block that owns those tokens (the groups of
 // four go round the blocks) through distributed shared memory, and the owner
-// adds and stores them.
+// adds and stores them. A warp whose sums never came says so to the owners and
+// counts its bytes as sent, so an owner's wait ends on every path, and never
+// while sums are on their way to it.
 //
 // With few tokens the weights' bytes bound it: nearly all of shared memory is
 // a ring of copies (17 KB of weights to a stage), and with
@@ -49,6 +51,7 @@ struct Ctl {
   uint32_t tmem;
   int32_t issued[2];   // stages filled: weights, tokens
   int32_t consumed;    // stages whose copies the MMA thread saw arrive
+  uint32_t missing;    // some sums of this owner's tokens never came
 };
 
 // Stage: W codes, x codes, W scales (2 tiles), x scales (2 tiles). A token tile
@@ -98,6 +101,17 @@ __device__ __forceinline__ void store4(T* y, int64_t ld, int n, bool in, int t0,
   }
 }
 
+// Takes `bytes` off what a barrier of the cluster waits for, after setting the
+// word at `flag` of the same block: a thread that sees the barrier's phase end
+// sees the word.
+__device__ __forceinline__ void give_up(uint32_t flag, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "st.shared::cluster.u32 [%0], 1;\n\t"
+      "fence.acq_rel.cluster;\n\t"
+      "mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%1], %2;"
+      ::"r"(flag), "r"(bar), "r"(bytes) : "memory");
+}
+
 template <int BN>
 __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ Mx4GemmParams p) {
   constexpr int kStage = stage_bytes(BN);
@@ -121,7 +135,8 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
   const int tok = (int)min((int64_t)BN, p.M - m0);         // tokens of the tile
   const int share = share_of(BN, S);
   const int quads = (tok + 3) / 4;                         // groups of four tokens
-  const int owned = quads > part ? (quads - part - 1) / S + 1 : 0;
+  auto owned_by = [&](int q) { return quads > q ? (quads - q - 1) / S + 1 : 0; };
+  const int owned = owned_by(part);
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -131,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     mbar_init(&ctl->done, 2);
     mbar_init(&ctl->parts, 1);
     ctl->issued[0] = ctl->issued[1] = ctl->consumed = 0;
+    ctl->missing = 0;
     fence_mbar_init();
     if (S > 1) mbar_arrive_expect_tx(&ctl->parts, (uint32_t)(S * owned * kBM * 16));
   }
@@ -268,18 +284,25 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       }
     }
     tc_fence_before();
+  } else if (S > 1 && warp < 4 && lane < min(S, quads)) {
+    give_up(map_rank(&ctl->missing, lane), map_rank(&ctl->parts, lane), owned_by(lane) * 32 * 16);
   }
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, p.tmem_cols);
   if (ctl->issued[0] != nk || ctl->issued[1] != nk || ctl->consumed != nk) {
-    // a copy never came: wait for those in flight, store nothing
+    // a copy never came: wait for those in flight (the last to each stage),
+    // store nothing
     ok = false;
+    const int last = max(ctl->issued[0], ctl->issued[1]);
     if (tid == 0)
-      for (int b = 0; b < 2 * NST; ++b)
-        mbar_wait_bounded(&ctl->full[b % NST], b / NST, p.status, 1ll << 28);
+      for (int b = max(0, last - NST); b < last; ++b)
+        mbar_wait_bounded(&ctl->full[b % NST], (b / NST) & 1, p.status, 1ll << 28);
     __syncthreads();
   }
-  if (S > 1) ok = mbar_wait_bounded(&ctl->parts, 0, p.status) && ok;
+  // The wait outlasts any sender's own bounded waits.
+  if (S > 1)
+    ok = mbar_wait_bounded(&ctl->parts, 0, p.status, 1ll << 36) && ok &&
+         *static_cast<volatile uint32_t*>(&ctl->missing) == 0;
 
   // The owner of four tokens adds their sums up in order and stores them: a
   // lane two neighbouring columns, a warp 64, a line of 128 bytes in bf16.
