@@ -181,6 +181,9 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     int b = 0, s = 0;
     uint32_t parity = 1;      // a stage's first use finds its barrier in the phase before
     for (; b < nk; ++b) {
+      // No bounded wait spans the kernel before: a stage is free again only
+      // after it, since no MMA starts without tokens.
+      if (early && b == NST) griddep_wait();
       if (!warp_wait(&ctl->empty[s], parity, p.status)) break;
       if (leader) {
         const uint32_t sfb = (2 * b + 1 < ntile ? 2 : 1) * kMx4TileBytes;
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     const bool leader = elect_one();
     int b = 0, s = 0;
     uint32_t parity = 0;
+    griddep_wait();           // as the tokens' copies do: the bounded waits start here
     for (; b < nk; ++b) {
       const bool expire = b == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT) != 0;
       if (!warp_wait(&ctl->full[s], parity, p.status, expire ? 0 : 1ll << 31)) break;
@@ -244,7 +248,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       umma_commit(&ctl->done);
     }
     __syncwarp();
-    griddep_wait();
   } else {
     griddep_wait();
     ok = warp_wait(&ctl->done, 0, p.status) && ctl->consumed == nk;
