@@ -331,9 +331,9 @@ int lora_shrink_noalloc(const ig_shape* shape, const void* x, const void* A_stac
  *           below and must be finite; those of rows past the last are
  *           neither written nor of any effect.
  * These calls keep the conventions above (device pointers, 16-byte alignment,
- * enqueue only, argument errors before anything is enqueued); row strides
- * (ld_*) are in elements and multiples of 8. An operator with no rows is a
- * no-op.
+ * enqueue only, argument errors before anything is enqueued); pointers and
+ * stream belong to the current GPU; row strides (ld_*) are in elements and
+ * multiples of 8. An operator with no rows is a no-op.
  * ------------------------------------------------------------------------ */
 typedef enum ig_type { IG_TYPE_BF16 = 0, IG_TYPE_F32 = 1 } ig_type;
 

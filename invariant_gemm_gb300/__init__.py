@@ -270,7 +270,8 @@ def check_status(ws, stream=None) -> int:
 #
 # Sizes and strides come from the tensors. A tensor of another type, size,
 # device or inner stride than its place asks for raises IGError (IG_ERR_ARG or
-# IG_ERR_SHAPE) before the library is called; the library checks the rest.
+# IG_ERR_SHAPE) before the library is called, and so do operands on a GPU that
+# is not the current one; the library checks the rest.
 
 # The checks of a call take longer than its launch. So each call tests all that
 # is usual (right types, one device, contiguous) in expressions of its own, and
@@ -323,7 +324,12 @@ def _values(what, name, t, torch):
     return shape, dev, int(dtype is torch.float32), ld
 
 
-def _stream_of(dev, stream, torch):
+def _stream_of(what, dev, stream, torch):
+    """The stream's handle for a launch on GPU `dev`, which has to be the current
+    one: the library launches there."""
+    now = torch._C._cuda_getDevice()
+    if now != dev:
+        raise IGError(-1, f"{what}: operands are on GPU {dev}, the current one is GPU {now}")
     # the current stream's handle without the Stream object around it, whose
     # construction costs 2 us a call
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -341,23 +347,26 @@ def mx4_quantize(x, codes, scales, stream=None):
     """x [rows][K] (bf16 or FP32, rows may be strided) -> MX4: codes uint8
     [rows][K/2] and scales, uint8 of mx4_scale_bytes(rows, K) elements."""
     import torch
-    (rows, K), dev, t, ld = _values("mx4_quantize", "x", x, torch)
-    _packed("mx4_quantize", "x", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
+    what = "mx4_quantize"
+    (rows, K), dev, t, ld = _values(what, "x", x, torch)
+    _packed(what, "x", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
     rc = (_LIB or lib()).ig_mx4_quantize(rows, K, x.data_ptr(), ld, t, codes.data_ptr(),
-                                         scales.data_ptr(), _stream_of(dev, stream, torch))
+                                         scales.data_ptr(), _stream_of(what, dev, stream, torch))
     if rc:
-        raise IGError(rc, "mx4_quantize")
+        raise IGError(rc, what)
 
 
 def mx4_dequantize(codes, scales, out, stream=None):
     """The values of an MX4 matrix into out [rows][K] (bf16 or FP32)."""
     import torch
-    (rows, K), dev, t, ld = _values("mx4_dequantize", "out", out, torch)
-    _packed("mx4_dequantize", "input", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
+    what = "mx4_dequantize"
+    (rows, K), dev, t, ld = _values(what, "out", out, torch)
+    _packed(what, "input", codes, scales, dev, torch.uint8, rows, (K + 1) >> 1)
     rc = (_LIB or lib()).ig_mx4_dequantize(rows, K, codes.data_ptr(), scales.data_ptr(),
-                                           out.data_ptr(), ld, t, _stream_of(dev, stream, torch))
+                                           out.data_ptr(), ld, t,
+                                           _stream_of(what, dev, stream, torch))
     if rc:
-        raise IGError(rc, "mx4_dequantize")
+        raise IGError(rc, what)
 
 
 def mx4_workspace(device="cuda"):
@@ -381,7 +390,7 @@ def mx4_gemm(x_codes, x_scales, w_codes, w_scales, y, ws, flags=0, stream=None):
     rc = (_LIB or lib()).ig_mx4_gemm(_MX4_SHAPE(M, N, 2 * half, ld, t, flags), x_codes.data_ptr(),
                                      x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                                      y.data_ptr(), ws.data_ptr(), ws.numel(),
-                                     _stream_of(dev, stream, torch))
+                                     _stream_of(what, dev, stream, torch))
     if rc:
         raise IGError(rc, what)
 
@@ -459,6 +468,6 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
         pc, ps = codes.data_ptr(), scales.data_ptr()
     rc = (_LIB or lib()).ig_block_norm(
         _NORM_SHAPE(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale), ph, py, pg,
-        p_post, p_pre, pho, pn, pc, ps, _stream_of(dev, stream, torch))
+        p_post, p_pre, pho, pn, pc, ps, _stream_of(what, dev, stream, torch))
     if rc:
         raise IGError(rc, what)
