@@ -295,6 +295,14 @@ def _flat(what, name, t, dev, dtype, count):
         _why(what, name, t, dev, dtype, (count,))
 
 
+def _vector(what, name, t, dev, dtype, count):
+    """Checks a contiguous operand of `count` elements; returns its address."""
+    if not (t.dtype is dtype and t.numel() == count and t.is_contiguous() and
+            t.get_device() == dev >= 0):
+        _why(what, name, t, dev, dtype, (count,))
+    return t.data_ptr()
+
+
 def _packed(what, name, codes, scales, dev, u8, rows, half):
     """Checks the two tensors of a [rows][2 half] MX4 matrix."""
     count = ((rows + 127) >> 7) * ((half + 63) >> 6) * 512
@@ -453,11 +461,9 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
             ld_n = _rows(what, "n_out", n_out, dev, b16, shape)
         pn = n_out.data_ptr()
     if w_post is not None:
-        _flat(what, "w_post", w_post, dev, b16, H)
-        p_post = w_post.data_ptr()
+        p_post = _vector(what, "w_post", w_post, dev, b16, H)
     if w_pre is not None:
-        _flat(what, "w_pre", w_pre, dev, b16, H)
-        p_pre = w_pre.data_ptr()
+        p_pre = _vector(what, "w_pre", w_pre, dev, b16, H)
     if gate is not None:
         grs, gcs = _gate(what, gate, dev, b16, M, H)
         pg = gate.data_ptr()

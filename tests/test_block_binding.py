@@ -71,3 +71,14 @@ def test_operands_on_a_gpu_that_is_not_current(library, name, stream):
         CALLS[name](operands(), stream=stream)
     assert e.value.code == -1 and "GPU 1" in str(e.value) and "GPU 0" in str(e.value)
     assert library.calls == ["ig_" + name]
+
+
+@pytest.mark.parametrize("post,pre", [(128, 64), (64, 128), (32, 64), (64, 72)])
+def test_norm_weights_of_another_size(library, post, pre):
+    """A weight of more than H values is not one of H: its first row may be
+    another layer's."""
+    o = operands()
+    w = {n: on(torch.ones(n, dtype=B16)) for n in (post, pre)}
+    with pytest.raises(ig.IGError) as e:
+        ig.block_norm(o["x"], o["x"], w[post], w[pre], n_out=o["x"])
+    assert e.value.code == -2 and library.calls == []
