@@ -387,7 +387,8 @@ typedef struct ig_norm_shape {
   int64_t ld_h, ld_y, ld_h_out, ld_n; /* row strides of what is given */
   int64_t gate_row_stride; /* 0: the same gate for every row */
   int32_t gate_col_stride; /* 1, or 0: one gate value per row (then
-                              gate_row_stride may be any) */
+                              gate_row_stride may be any, and gate any
+                              address of a bf16 value) */
   int32_t h_type;          /* ig_type of h and h_out */
   int32_t flags;           /* 0 or IG_NORM_WEIGHT_PLUS_ONE */
   float eps;               /* >= 0 */
