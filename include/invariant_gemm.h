@@ -43,7 +43,7 @@
  *     8 (so rows are whole 16-byte vectors).
  *   - Return value: IG_OK, or a negative ig_status. Argument errors are
  *     detected on the host before anything is enqueued. IG_ERR_CUDA reports
- *     a failed launch (cudaGetLastError).
+ *     a failed launch of this call.
  *   - Overlap: shrink and expand kernels are launched with programmatic
  *     dependent launch. A kernel may start while the previous kernel on the
  *     stream finishes, but it reads activations, z, y and the workspace

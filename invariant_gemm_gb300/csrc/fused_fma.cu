@@ -323,9 +323,7 @@ cudaError_t launch_fused_fma(const FusedParams& p, int bn, int64_t tiles_max, cu
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace ig

@@ -184,7 +184,8 @@ struct TreeParams {
   float scale;
 };
 
-// Launchers (defined in the .cu files); they return cudaGetLastError().
+// Launchers (defined in the .cu files). They return the launch's own result:
+// cudaGetLastError() may hold the failure of an earlier call.
 cudaError_t launch_map_tokens(const MapParams& p, cudaStream_t st);
 cudaError_t launch_shrink_warp(const ShrinkParams& p, int mode, int bn,
                               int64_t tiles_max, cudaStream_t st);
@@ -222,9 +223,7 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 #ifdef __CUDACC__

@@ -199,8 +199,12 @@ cudaError_t launch_map_tokens(const MapParams& p, cudaStream_t st) {
                                          (int)smem);
     if (e != cudaSuccess) return e;
   }
-  map_tokens_kernel<<<1, kMapThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, map_tokens_kernel, p);
 }
 
 }  // namespace ig

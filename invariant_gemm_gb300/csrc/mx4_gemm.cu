@@ -365,9 +365,7 @@ cudaError_t launch_bn(Mx4GemmParams& p, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // Which kernel is through soonest with more than 64 tokens, by a start and so

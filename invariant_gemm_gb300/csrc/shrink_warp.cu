@@ -276,9 +276,7 @@ cudaError_t launch_cluster(const ShrinkParams& p, int64_t tiles_max, cudaStream_
     if (!it->second) return cudaErrorNotSupported;
   }
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int BN>
