@@ -39,6 +39,24 @@ def test_blocks_that_failed_do_not_keep_the_others_waiting(M):
     assert torch.equal(gemm(x, w, N, "f32", ws=ws), ref)
 
 
+@gpu
+@pytest.mark.parametrize("y_t", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(4, 264, 256), (16, 264, 8192), (48, 520, 4096),
+                                   (100, 512, 2048), (300, 136, 2048), (600, 4096, 1024),
+                                   (257, 12288, 512)])
+def test_expired_blocks_store_their_result_or_nothing(M, N, K, y_t):
+    """Each element is as it was or, bit for bit, that of an undisturbed call."""
+    need_gpu()
+    x, w = held(values(M, K, 3)), held(values(N, K, 4))
+    ref = gemm(x, w, N, y_t)
+    ws = ig.mx4_workspace()
+    y = torch.full_like(ref, 5.0)
+    ig.mx4_gemm(x[0], x[1], w[0], w[1], y, ws, flags=ig.FLAG_TEST_COPY_TIMEOUT)
+    assert ig.check_status(ws) == IG_ERR_TIMEOUT
+    assert ((y == 5) | (y == ref)).all() and (y == 5).any()
+    assert torch.equal(gemm(x, w, N, y_t, ws=ws), ref)
+
+
 # A kernel that lets the next one on the stream start and then runs on for
 # `clocks` (at most 2^32) of its SM's clock: two seconds or so.
 DELAY = r"""
