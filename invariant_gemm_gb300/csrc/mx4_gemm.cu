@@ -18,7 +18,7 @@
 // With few tokens the weights' bytes bound it: nearly all of shared memory is
 // a ring of copies (17 KB of weights to a stage), and with
 // IG_FLAG_STATIC_WEIGHTS the ring is filled while the kernel before ends. M = 16,
-// K = 28672, N = 8192: 21.4 us, 5.9 TB/s. Small weights are over in the time from
+// K = 28672, N = 8192: 21.5 us, 5.8 TB/s. Small weights are over in the time from
 // the first copy to the last store: M = 1, N = K = 4096 3.9 us, for 1.3 us of
 // bytes.
 //
@@ -181,9 +181,6 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     int b = 0, s = 0;
     uint32_t parity = 1;      // a stage's first use finds its barrier in the phase before
     for (; b < nk; ++b) {
-      // No bounded wait spans the kernel before: a stage is free again only
-      // after it, since no MMA starts without tokens.
-      if (early && b == NST) griddep_wait();
       if (!warp_wait(&ctl->empty[s], parity, p.status)) break;
       if (leader) {
         const uint32_t sfb = (2 * b + 1 < ntile ? 2 : 1) * kMx4TileBytes;
@@ -197,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
       if (++s == NST) {
         s = 0;
         parity ^= 1;
+        griddep_wait();         // no bounded wait for a free stage spans the kernel before
       }
     }
     if (leader) ctl->issued[w ? 0 : 1] = b;
