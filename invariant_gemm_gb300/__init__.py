@@ -332,12 +332,23 @@ def _values(what, name, t, torch):
     return shape, dev, int(dtype is torch.float32), ld
 
 
-def _stream_of(what, dev, stream, torch):
-    """The stream's handle for a launch on GPU `dev`, which has to be the current
-    one: the library launches there."""
+_ONE_GPU = False    # the process sees one GPU, which is then the current one
+
+
+def _check_current(what, dev, torch):
+    """The library launches on the current GPU: operands have to be there."""
+    global _ONE_GPU
+    _ONE_GPU = torch.cuda.device_count() == 1
     now = torch._C._cuda_getDevice()
     if now != dev:
         raise IGError(-1, f"{what}: operands are on GPU {dev}, the current one is GPU {now}")
+
+
+def _stream_of(what, dev, stream, torch):
+    """The stream's handle for a launch on GPU `dev`, checked to be current (with
+    one GPU once: the look costs a call 0.3 us)."""
+    if not _ONE_GPU:
+        _check_current(what, dev, torch)
     # the current stream's handle without the Stream object around it, whose
     # construction costs 2 us a call
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)

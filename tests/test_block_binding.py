@@ -39,6 +39,8 @@ def library(monkeypatch):
     rec.ig_status_string = ig.lib().ig_status_string
     rec.current = 1
     monkeypatch.setattr(ig, "_LIB", rec)
+    monkeypatch.setattr(ig, "_ONE_GPU", False)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: rec.current, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
     return rec
