@@ -360,7 +360,9 @@ typedef struct ig_mx4_shape {
   int64_t K;      /* reduction length (a multiple of 32) */
   int64_t ld_y;   /* row stride of y */
   int32_t y_type; /* ig_type */
-  int32_t flags;  /* 0, IG_FLAG_STATIC_WEIGHTS (of w_codes and w_scales) and, for
+  int32_t flags;  /* 0, IG_FLAG_STATIC_WEIGHTS (w_codes and w_scales may be read
+                     before earlier work on the stream has ended; products of
+                     many tokens do not make use of it) and, for
                      tests only, IG_FLAG_TEST_COPY_TIMEOUT: the first wait for a
                      copy expires in every block, nothing is stored for its
                      tile and the status becomes IG_ERR_TIMEOUT */

@@ -3,7 +3,10 @@
 //   n = h' rsqrt(mean(h'^2) + eps) w_pre, and n in MX4.
 //
 // One row per thread block, one pass: a thread holds its vectors of 8 values
-// of the row in registers from the load to the last store.
+// of the row from the load to the last store, in registers but for a few words
+// that go to local memory (stored + loaded bytes a thread by V and W, below:
+// bf16 rows 0 for V = 2, W = 1, 36 + 36 for W = 2, 84 + 60 for V = 4; FP32 rows
+// 12 + 8, 0 and 124 + 108).
 //
 // The order of the sums is fixed by H: a row has `slots` places for vectors,
 // cut into V runs of T places; the values of the vectors at places t, t + T,
@@ -18,9 +21,17 @@
 // per SM and less work per row; few rows are over sooner with W = 1
 // (launch_block_norm has the figures). Copying rows ahead through shared memory by
 // blocks that stay (cp.async, 3 rows deep) was slower than fresh blocks: 107
-// against 87 us at 8192 x 8192, which now takes 82 us (bf16, 537 MB: 6.5 TB/s);
-// 1001 x 11008 FP32 with a gate for each value 30 us (5.1 TB/s), 4000 of those
-// rows 96 us (6.4 TB/s).
+// against 87 us at 8192 x 8192, which now takes 82-84 us (bf16, 537 MB: 6.5 TB/s);
+// 1001 x 11008 FP32 with a gate for each value 28-30 us (5.1-5.6 TB/s), 4000 of
+// those rows 96 us (6.4 TB/s). With n in MX4 alone 8192 x 8192 takes 88 us (5.0
+// TB/s, instructions issued in 77% of the cycles), the norm of h alone 49 us
+// (268 MB: 5.5 TB/s) and with MX4 out 62 us (2.8 TB/s).
+//
+// Far from memory's rate: short rows, where a block has 64 threads for as few as
+// 8 vectors (8192 rows of 64 to 256 values 9 us, of 512 10 us); FP32 rows above
+// 12288 and all rows above 16384, whose blocks leave room for no other on their
+// SM (4000 x 16384 FP32 168 us, 4.7 TB/s, where 12288 reach 6.5; 4000 x 32768 bf16
+// 178 us, 5.9 TB/s, FP32 371 us, 4.2 TB/s).
 //
 // The next kernel on the stream starts when this one is complete (no early
 // release): it may be one that reads n before its own wait, as the fused LoRA

@@ -18,7 +18,7 @@ namespace ig {
 constexpr int kMx4Block = 32;           // values per scale
 constexpr int kMx4TileBytes = 512;      // scale bytes of 128 rows x 128 k
 
-constexpr int64_t kNormMaxH = 32768;    // a row of the block norm stays in registers
+constexpr int64_t kNormMaxH = 32768;    // block norm: 1024 threads with 4 vectors of 8 values each
 
 __host__ __device__ inline int64_t mx4_ktiles(int64_t K) { return (K + 127) / 128; }
 

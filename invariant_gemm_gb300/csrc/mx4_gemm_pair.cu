@@ -16,7 +16,8 @@
 // 28672 498 us (7.7 PFLOP/s), 98% of the cycles in MMAs at 128 cycles each (K =
 // 64), at a clock of about 1.5 GHz; M = 4096, K = 4096, N = 12288 64 us, 84% of the
 // cycles (about 900 from a tile's last MMA to the next tile's first, and 10.1
-// rounds of tiles).
+// rounds of tiles), 76 us with an FP32 result. With K up to 512 by the stores, a
+// tile's 5200 cycles in 64-byte pieces: M = N = 8192, K = 64 40 us (3.3 TB/s).
 #include <atomic>
 
 #include "mx4.cuh"
