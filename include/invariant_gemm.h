@@ -81,7 +81,9 @@ typedef enum ig_status {
   IG_ERR_WS_CORRUPT = -6,    /* device: a completion counter held a value >= S */
   IG_ERR_ADAPTER_RANGE = -7, /* device: an adapter index outside [-1, L) */
   IG_ERR_TIMEOUT = -8,       /* device: a bounded wait expired */
-  IG_ERR_UNSUPPORTED = -9    /* valid request outside this build's limits */
+  IG_ERR_UNSUPPORTED = -9,   /* valid request outside this build's limits */
+  IG_ERR_INDEX_RANGE = -10   /* device: a position, page number or length of
+                                the attention calls outside its range */
 } ig_status;
 
 /* Reduction variant of the shrink (sec. 4.1-4.3). */
@@ -413,9 +415,150 @@ int ig_block_norm(const ig_norm_shape* shape, const void* h, const void* y, cons
                   const void* w_post, const void* w_pre, void* h_out, void* n_out, void* codes,
                   void* scales, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention of a served layer: head norms with the position rotation, a
+ * paged key/value cache held in 8 bits, and attention over it. These calls
+ * take the q, k and v that the stacked projections (slices = 3) leave and make
+ * the input of the output projection.
+ *
+ * Tokens of a batch are stacked; sequence b has the rows cu[b] .. cu[b+1] - 1
+ * and they are its last ones: positions kv_len[b] - rows .. kv_len[b] - 1.
+ * Rows that belong to no sequence are neither read nor written. Token j of
+ * sequence b is in row j % page of the page page_table[b][j / page].
+ *
+ * Cache, for each page, side (0 keys, 1 values) and kv head:
+ *   codes   uint8 [pages][2][heads][page][head_dim], e4m3: sign, 4 exponent and
+ *           3 mantissa bits, largest 448, 0x7f and 0xff NaN, no infinities
+ *   scales  uint8 [pages][2][heads][page / 16]: 16 tokens of a head (a block)
+ *           share the scale 2^(byte - 127); 255 = NaN
+ * Pages may lie further apart than they are long (page_stride, scale_stride);
+ * what is inside a page is dense.
+ *
+ * These calls keep the conventions above; pointers and stream belong to the
+ * current GPU. q, k, v and their outputs are bf16 [T][heads][head_dim] with a
+ * stride of ld_* elements (a multiple of 8) between tokens, so they may be
+ * columns of one buffer. head_dim is 64 or 128. A sequence whose cu, kv_len or
+ * page count is out of range (rows outside [0, T), more than max_q of them
+ * where the call has one, kv_len beyond ld_table pages) is left out of the
+ * call, tokens on pages outside [0, pages) are taken as absent, and the status
+ * word of ws records IG_ERR_INDEX_RANGE. ws is any initialised workspace of the
+ * library (ig_mx4_workspace_bytes() zeroed bytes will do), but for
+ * ig_paged_attention, which says how much it needs.
+ *
+ * The bits of a row of q, k, v and of the attention's output depend on that
+ * row, its sequence (kv_len, number of new tokens, cache content) and the sizes
+ * of heads and pages only: never on the other sequences, the sequence's place
+ * in the batch, the pages it is on or the run.
+ * ------------------------------------------------------------------------ */
+#define IG_ROPE_INTERLEAVED 2 /* rotated pairs are neighbours (x[2i], x[2i+1]);
+                                 otherwise (x[i], x[i + rot_dim / 2]) */
+
+typedef struct ig_rope_shape {
+  int64_t T;               /* tokens */
+  int64_t table_rows;      /* positions that cos_sin holds */
+  int64_t ld_q, ld_k, ld_q_out, ld_k_out; /* strides of what is given */
+  int32_t heads_q, heads_k;
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t rot_dim;         /* values rotated, the first of each head: a multiple
+                              of 16, at most head_dim */
+  int32_t flags;           /* 0, IG_NORM_WEIGHT_PLUS_ONE, IG_ROPE_INTERLEAVED */
+  float eps;               /* >= 0 */
+} ig_rope_shape;
+
+typedef struct ig_kv_cache {
+  void* codes;
+  void* scales;
+  int64_t pages;
+  int64_t page_stride;     /* bytes between pages of codes (a multiple of 16) */
+  int64_t scale_stride;    /* bytes between pages of scales */
+  int32_t page;            /* tokens to a page: 16, 32, 64, 128 or 256 */
+  int32_t heads;           /* kv heads */
+  int32_t head_dim;
+  int32_t reserved;        /* 0 */
+} ig_kv_cache;
+
+typedef struct ig_batch {
+  const int32_t* cu;         /* [batch + 1], not falling */
+  const int32_t* kv_len;     /* [batch] tokens in all, the new ones among them */
+  const int32_t* page_table; /* [batch][ld_table] */
+  int64_t ld_table;          /* pages that a row of page_table can name */
+  int32_t batch;
+  int32_t max_q;             /* no sequence has more new tokens than this */
+} ig_batch;
+
+/* Norms of queries and keys for each head and the position rotation, in one
+ * pass, in FP32 with one rounding:
+ *   n = x * rsqrt(mean(x^2) + eps) * w               (w NULL: n = x)
+ *   (n1, n2) -> (n1 cos - n2 sin, n2 cos + n1 sin)    (cos_sin NULL: as it is)
+ * for the rot_dim / 2 pairs, with the cosines cos_sin[p][0 .. rot_dim/2) and the
+ * sines cos_sin[p][rot_dim/2 .. rot_dim) of the token's position p
+ * (cos_sin FP32 [table_rows][rot_dim], positions int32 [T]). q or k may be NULL,
+ * with their outputs. q_out may be q and k_out may be k (same strides). A token whose position is
+ * outside the table gets NaN, and ws records IG_ERR_INDEX_RANGE. w_q and w_k
+ * are bf16 [head_dim]. */
+int ig_qk_norm_rope(const ig_rope_shape* shape, const void* q, const void* k, const void* w_q,
+                    const void* w_k, const float* cos_sin, const int32_t* positions, void* q_out,
+                    void* k_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Keys and values of the new tokens into the cache, keys (and q, where given,
+ * into q_out) normed and rotated as by ig_qk_norm_rope; positions NULL: the
+ * token's place in its sequence. Quantised from FP32: a block's scale is the
+ * smallest 2^e, e >= -120, with max|value| <= 448 2^e over the finite values of
+ * its new tokens; where older tokens of the sequence are in the block it is at
+ * least their scale, and where it grew they are divided by as much. Values are
+ * rounded to nearest, ties to even; what is not finite is held as NaN. Rows of
+ * the block behind the last token keep their bytes.
+ * Two sequences of a call must not share a block that one of them writes.
+ * Tokens appended one by one and together get the same scales, and the same
+ * codes but for values under 2^-6 scale, which a growing scale rounds again.
+ * k and v have batch->cu's rows of shape->T; ld_k is the stride of k. */
+int ig_kv_append(const ig_rope_shape* shape, const ig_kv_cache* cache, const ig_batch* batch,
+                 const void* k, const void* v, int64_t ld_v, const void* q, const void* w_q,
+                 const void* w_k, const float* cos_sin, const int32_t* positions, void* q_out,
+                 void* ws, size_t ws_bytes, void* stream);
+
+/* What the cache holds, as bf16 (exact but for what bf16 cannot hold: values
+ * under 2^-126): row cu[b] + i of k_out and v_out [T][heads][head_dim] is token
+ * kv_len[b] - rows + i of sequence b. max_q is not looked at. Rows of tokens
+ * before the sequence's first (more rows than kv_len) are written as 0, of
+ * absent tokens as NaN. */
+int ig_kv_gather(const ig_kv_cache* cache, const ig_batch* batch, int64_t T, void* k_out,
+                 int64_t ld_k_out, void* v_out, int64_t ld_v_out, void* ws, size_t ws_bytes,
+                 void* stream);
+
+typedef struct ig_attn_shape {
+  int64_t T;               /* rows of q and out */
+  int64_t ld_q, ld_out;
+  int32_t heads_q;         /* a multiple of the cache's heads: query head h reads
+                              kv head h / (heads_q / heads) */
+  int32_t flags;           /* 0 or, for tests only, IG_FLAG_TEST_COPY_TIMEOUT: every
+                              block acts as if its first wait for a copy had
+                              expired; out is then unspecified and the status
+                              IG_ERR_TIMEOUT */
+  float scale;             /* of the products, usually 1 / sqrt(head_dim) */
+  int32_t reserved;        /* 0 */
+} ig_attn_shape;
+
+/* Bytes of workspace of ig_paged_attention for these sizes (of batch: batch,
+ * max_q and ld_table; of cache: page, heads and head_dim); 0 for invalid ones.
+ * Zeroed once after it is allocated; calls that may overlap need one each. */
+size_t ig_attention_workspace_bytes(const ig_attn_shape* shape, const ig_kv_cache* cache,
+                                    const ig_batch* batch);
+
+/* Attention of the new tokens over the cache, causal at the sequence's end:
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j),
+ * over the tokens j <= kv_len - rows + i for row i of a sequence's `rows`. Rows
+ * that see no token (rows > kv_len) are 0. Products of the held values in
+ * the tensor cores with FP32 sums, softmax in FP32; p is rounded to 11 bits for
+ * the product with v. out may not be q. */
+int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
+                       const ig_batch* batch, const void* q, void* out, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read and clear the workspace status word, and return
  * the most severe device-side error recorded since the last check
- * (IG_ERR_TIMEOUT, IG_ERR_WS_CORRUPT, IG_ERR_ADAPTER_RANGE) or IG_OK. After
+ * (IG_ERR_TIMEOUT, IG_ERR_WS_CORRUPT, IG_ERR_ADAPTER_RANGE,
+ * IG_ERR_INDEX_RANGE) or IG_OK. After
  * IG_ERR_WS_CORRUPT or IG_ERR_TIMEOUT the completion counters are zeroed
  * again, so the workspace is usable for the next call. After IG_ERR_TIMEOUT
  * the z and y written by the calls since the last check are unspecified

@@ -13,7 +13,8 @@ their data pointers are handed to the library unchanged. Layouts:
   y        bf16  [M][slices*N]   (updated in place)
   idx      int32 [M]             (-1 = no adapter)
 The calls around the adapters (mx4_quantize, mx4_dequantize, mx4_gemm,
-block_norm) take their sizes and strides from the tensors and check them.
+block_norm) and those of the attention (qk_norm_rope, kv_append, kv_gather,
+paged_attention) take their sizes and strides from the tensors and check them.
 """
 from __future__ import annotations
 
@@ -31,6 +32,8 @@ __all__ = [
     "EXPORTS",
     "NORM_WEIGHT_PLUS_ONE", "Mx4Shape", "NormShape", "mx4_scale_bytes", "mx4_quantize",
     "mx4_dequantize", "mx4_workspace", "mx4_gemm", "block_norm",
+    "ROPE_INTERLEAVED", "qk_norm_rope", "kv_append", "kv_gather", "attention_workspace",
+    "paged_attention",
 ]
 
 MODE_DET, MODE_ATOMIC, MODE_UNSPLIT, MODE_DET_TREE = 0, 1, 2, 3
@@ -40,12 +43,14 @@ FLAG_Z_FP32 = 4
 FLAG_TEST_COPY_TIMEOUT = 8   # testing only: the first A-copy wait of each block expires
 FLAG_INPUT_READY = 16        # x not written by work still running on the stream
 PATH_AUTO, PATH_WARP, PATH_MMA, PATH_FMA = 0, 1, 2, 3
-NORM_WEIGHT_PLUS_ONE = 1     # block_norm: norm weights are stored as w - 1
+NORM_WEIGHT_PLUS_ONE = 1     # block_norm, head norms: norm weights are stored as w - 1
+ROPE_INTERLEAVED = 2         # rotated pairs are neighbours, not halves
 
 STATUS = {
     0: "IG_OK", -1: "IG_ERR_ARG", -2: "IG_ERR_SHAPE", -3: "IG_ERR_ALIGN",
     -4: "IG_ERR_WS_SMALL", -5: "IG_ERR_CUDA", -6: "IG_ERR_WS_CORRUPT",
     -7: "IG_ERR_ADAPTER_RANGE", -8: "IG_ERR_TIMEOUT", -9: "IG_ERR_UNSUPPORTED",
+    -10: "IG_ERR_INDEX_RANGE",
 }
 
 # every function declared in include/invariant_gemm.h
@@ -54,6 +59,8 @@ EXPORTS = [
     "ig_workspace_init", "ig_map_tokens", "lora_shrink", "lora_expand", "lora_apply",
     "ig_check_status", "lora_shrink_noalloc", "ig_mx4_scale_bytes", "ig_mx4_workspace_bytes",
     "ig_mx4_quantize", "ig_mx4_dequantize", "ig_mx4_gemm", "ig_block_norm",
+    "ig_qk_norm_rope", "ig_kv_append", "ig_kv_gather", "ig_attention_workspace_bytes",
+    "ig_paged_attention",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +116,11 @@ class NormShape(ctypes.Structure):
 # The same structs as bytes: half the time of a ctypes.Structure.
 _MX4_SHAPE = struct.Struct("qqqqii").pack
 _NORM_SHAPE = struct.Struct("qqqqqqqiiiff").pack
+# ig_rope_shape, ig_kv_cache, ig_batch and ig_attn_shape of the header
+_ROPE_SHAPE = struct.Struct("qqqqqqiiiiif").pack
+_KV_CACHE = struct.Struct("PPqqqiiii").pack
+_BATCH = struct.Struct("PPPqii").pack
+_ATTN_SHAPE = struct.Struct("qqqiifi").pack
 
 _LIB = None
 _P = ctypes.c_void_p
@@ -161,6 +173,17 @@ def lib() -> ctypes.CDLL:
         L.ig_mx4_gemm.argtypes = [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.ig_block_norm.restype = ctypes.c_int
         L.ig_block_norm.argtypes = [_P] * 11
+        n = ctypes.c_size_t
+        L.ig_qk_norm_rope.restype = ctypes.c_int
+        L.ig_qk_norm_rope.argtypes = [_P] * 10 + [n, _P]
+        L.ig_kv_append.restype = ctypes.c_int
+        L.ig_kv_append.argtypes = [_P] * 5 + [i64] + [_P] * 7 + [n, _P]
+        L.ig_kv_gather.restype = ctypes.c_int
+        L.ig_kv_gather.argtypes = [_P, _P, i64, _P, i64, _P, i64, _P, n, _P]
+        L.ig_attention_workspace_bytes.restype = n
+        L.ig_attention_workspace_bytes.argtypes = [_P] * 3
+        L.ig_paged_attention.restype = ctypes.c_int
+        L.ig_paged_attention.argtypes = [_P] * 6 + [n, _P]
         _LIB = L
     return _LIB
 
@@ -486,5 +509,234 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
     rc = (_LIB or lib()).ig_block_norm(
         _NORM_SHAPE(M, H, ld_h, ld_y, ld_ho, ld_n, grs, gcs, t, flags, eps, scale), ph, py, pg,
         p_post, p_pre, pho, pn, pc, ps, _stream_of(what, dev, stream, torch))
+    if rc:
+        raise IGError(rc, what)
+
+
+# --- the attention of a served layer -------------------------------------------
+#
+# Heads: bf16 [T][heads][D], dense but for the stride between tokens (so q, k
+# and v may be columns of one buffer). Cache: codes uint8 [pages][2][heads][page]
+# [D] and scales uint8 [pages][2][heads][page / 16], dense but for the stride
+# between pages. Batch: cu int32 [B + 1], kv_len int32 [B], page_table int32
+# [B][pages of the longest]; sequence b has the rows cu[b] .. cu[b + 1] - 1, its
+# last tokens.
+
+def _heads(what, name, t, dev, b16):
+    """(T, heads, D, stride between tokens) of an operand of heads."""
+    shape = t.shape
+    if t.dtype is b16 and len(shape) == 3 and t.get_device() == dev >= 0:
+        T, heads, D = shape
+        if t.is_contiguous():
+            return T, heads, D, heads * D
+        ld, hs, inner = t.stride()
+        if (inner == 1 or D == 1) and (hs == D or heads == 1):
+            return T, heads, D, (ld if T > 1 else heads * D)
+    _why(what, name, t, dev, b16, shape)
+
+
+def _like(what, name, t, dev, b16, T, heads, D):
+    """Checks an operand of T tokens of these heads; returns its stride."""
+    got = _heads(what, name, t, dev, b16)
+    if got[:3] != (T, heads, D):
+        _why(what, name, t, dev, b16, (T, heads, D))
+    return got[3]
+
+
+def _cache_of(what, cache, scales, dev, u8):
+    """The cache's struct and its (heads, head_dim)."""
+    shape = cache.shape
+    if not (cache.dtype is u8 and len(shape) == 5 and shape[1] == 2 and cache.get_device() == dev):
+        _why(what, "cache", cache, dev, u8, shape)
+    pages, _, heads, page, D = shape
+    inner, blocks = 2 * heads * page * D, page >> 4
+    ps, ss = inner, 2 * heads * blocks
+    if not (scales.dtype is u8 and scales.shape == (pages, 2, heads, blocks) and
+            scales.get_device() == dev):
+        _why(what, "scales", scales, dev, u8, (pages, 2, heads, blocks))
+    if not cache.is_contiguous():
+        if pages > 1:
+            ps = cache.stride(0)
+        if pages and not cache[0].is_contiguous():
+            _why(what, "cache", cache, dev, u8, shape)
+    if not scales.is_contiguous():
+        if pages > 1:
+            ss = scales.stride(0)
+        if pages and not scales[0].is_contiguous():
+            _why(what, "scales", scales, dev, u8, (pages, 2, heads, blocks))
+    return (_KV_CACHE(cache.data_ptr(), scales.data_ptr(), pages, ps, ss, page, heads, D, 0),
+            heads, D)
+
+
+def _batch_of(what, cu, kv_len, page_table, dev, i32, max_q):
+    B = kv_len.numel()
+    if not (cu.dtype is i32 and kv_len.dtype is i32 and page_table.dtype is i32 and
+            cu.numel() == B + 1 and cu.is_contiguous() and kv_len.is_contiguous() and
+            page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_contiguous() and
+            cu.get_device() == kv_len.get_device() == page_table.get_device() == dev):
+        _vector(what, "cu", cu, dev, i32, B + 1)
+        _vector(what, "kv_len", kv_len, dev, i32, B)
+        _why(what, "page_table", page_table, dev, i32, (B, page_table.shape[-1]))
+    return _BATCH(cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], B,
+                  max_q)
+
+
+def _angles(what, cos_sin, positions, dev, T, torch):
+    """(rows, rotated values, addresses) of the rotation's operands."""
+    rows = rot = 0
+    pc = pp = None
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            _why(what, "cos_sin", cos_sin, dev, torch.float32, cos_sin.shape)
+        rows, rot = cos_sin.shape
+        pc = _vector(what, "cos_sin", cos_sin, dev, torch.float32, rows * rot)
+    if positions is not None:
+        pp = _vector(what, "positions", positions, dev, torch.int32, T)
+    return rows, rot, pc, pp
+
+
+def _status_ws(what, ws, dev, u8):
+    if not (ws.dtype is u8 and ws.is_contiguous() and ws.get_device() == dev):
+        _flat(what, "ws", ws, dev, u8, 0)
+
+
+def qk_norm_rope(q, k, q_out, k_out, ws, *, w_q=None, w_k=None, cos_sin=None, positions=None,
+                 eps=1e-6, flags=0, stream=None):
+    """Norm of each head of q and k (w_q, w_k bf16 [D]; None: no norm) and the
+    rotation of its first values by the angles of the token's position (cos_sin
+    FP32 [positions][rotated values]: the cosines, then the sines; positions int32
+    [T]; None: no rotation). q or k may be None, with their outputs; q_out may be
+    q, k_out may be k. flags: NORM_WEIGHT_PLUS_ONE, ROPE_INTERLEAVED. ws: any
+    workspace; a position outside the table is NaN there and in check_status."""
+    import torch
+    what, b16 = "qk_norm_rope", torch.bfloat16
+    lead = q if q is not None else k
+    if lead is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise IGError(-1, "qk_norm_rope: q and q_out, k and k_out go together, one pair at least")
+    dev = lead.get_device()
+    T, hq, D, ld_q = _heads(what, "q" if q is not None else "k", lead, dev, b16)
+    hk = ld_k = ld_qo = ld_ko = 0
+    pq = pk = pqo = pko = pwq = pwk = None
+    if q is not None:
+        ld_qo = _like(what, "q_out", q_out, dev, b16, T, hq, D)
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    else:
+        hq = ld_q = 0
+    if k is not None:
+        Tk, hk, Dk, ld_k = _heads(what, "k", k, dev, b16)
+        if Tk != T or Dk != D:
+            _why(what, "k", k, dev, b16, (T, hk, D))
+        ld_ko = _like(what, "k_out", k_out, dev, b16, T, hk, D)
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    if w_q is not None:
+        pwq = _vector(what, "w_q", w_q, dev, b16, D)
+    if w_k is not None:
+        pwk = _vector(what, "w_k", w_k, dev, b16, D)
+    rows, rot, pc, pp = _angles(what, cos_sin, positions, dev, T, torch)
+    _status_ws(what, ws, dev, torch.uint8)
+    rc = (_LIB or lib()).ig_qk_norm_rope(
+        _ROPE_SHAPE(T, rows, ld_q, ld_k, ld_qo, ld_ko, hq, hk, D, rot, flags, eps), pq, pk, pwq,
+        pwk, pc, pp, pqo, pko, ws.data_ptr(), ws.numel(), _stream_of(what, dev, stream, torch))
+    if rc:
+        raise IGError(rc, what)
+
+
+def kv_append(k, v, cache, scales, cu, kv_len, page_table, ws, *, w_k=None, cos_sin=None,
+              positions=None, q=None, q_out=None, w_q=None, eps=1e-6, max_q=None, flags=0,
+              stream=None):
+    """k (normed and rotated as by qk_norm_rope) and v of the new tokens into the
+    cache; q likewise into q_out (may be q) where given. positions None: the
+    token's place in its sequence. max_q: no sequence has more new tokens (None:
+    as many as there are)."""
+    import torch
+    what, b16 = "kv_append", torch.bfloat16
+    dev = k.get_device()
+    T, hk, D, ld_k = _heads(what, "k", k, dev, b16)
+    ld_v = _like(what, "v", v, dev, b16, T, hk, D)
+    c, heads, Dc = _cache_of(what, cache, scales, dev, torch.uint8)
+    if heads != hk or Dc != D:
+        _why(what, "k", k, dev, b16, (T, heads, Dc))
+    b = _batch_of(what, cu, kv_len, page_table, dev, torch.int32, T if max_q is None else max_q)
+    hq = ld_q = ld_qo = 0
+    pq = pqo = pwq = pwk = None
+    if (q is None) != (q_out is None):
+        raise IGError(-1, "kv_append: q and q_out go together")
+    if q is not None:
+        Tq, hq, Dq, ld_q = _heads(what, "q", q, dev, b16)
+        if Tq != T or Dq != D:
+            _why(what, "q", q, dev, b16, (T, hq, D))
+        ld_qo = _like(what, "q_out", q_out, dev, b16, T, hq, D)
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    if w_q is not None:
+        pwq = _vector(what, "w_q", w_q, dev, b16, D)
+    if w_k is not None:
+        pwk = _vector(what, "w_k", w_k, dev, b16, D)
+    rows, rot, pc, pp = _angles(what, cos_sin, positions, dev, T, torch)
+    _status_ws(what, ws, dev, torch.uint8)
+    rc = (_LIB or lib()).ig_kv_append(
+        _ROPE_SHAPE(T, rows, ld_q, ld_k, ld_qo, 0, hq, hk, D, rot, flags, eps), c, b, k.data_ptr(),
+        v.data_ptr(), ld_v, pq, pwq, pwk, pc, pp, pqo, ws.data_ptr(), ws.numel(),
+        _stream_of(what, dev, stream, torch))
+    if rc:
+        raise IGError(rc, what)
+
+
+def kv_gather(cache, scales, cu, kv_len, page_table, k_out, v_out, ws, *, stream=None):
+    """What the cache holds, in bf16: rows cu[b] .. cu[b + 1] - 1 of k_out and
+    v_out [T][heads][D] are the last tokens of sequence b."""
+    import torch
+    what, b16 = "kv_gather", torch.bfloat16
+    dev = cache.get_device()
+    c, heads, D = _cache_of(what, cache, scales, dev, torch.uint8)
+    T, hk, Dk, ld_k = _heads(what, "k_out", k_out, dev, b16)
+    if hk != heads or Dk != D:
+        _why(what, "k_out", k_out, dev, b16, (T, heads, D))
+    ld_v = _like(what, "v_out", v_out, dev, b16, T, heads, D)
+    b = _batch_of(what, cu, kv_len, page_table, dev, torch.int32, 0)
+    _status_ws(what, ws, dev, torch.uint8)
+    rc = (_LIB or lib()).ig_kv_gather(c, b, T, k_out.data_ptr(), ld_k, v_out.data_ptr(), ld_v,
+                                      ws.data_ptr(), ws.numel(),
+                                      _stream_of(what, dev, stream, torch))
+    if rc:
+        raise IGError(rc, what)
+
+
+def attention_workspace(q, cache, page_table, max_q=None):
+    """Allocate (with torch) a workspace for paged_attention over up to the rows
+    of q, the sequences and pages of page_table and max_q new tokens of one
+    sequence (None: as many as q has). It serves the other calls as well."""
+    import torch
+    T, hq, D = q.shape
+    _, _, heads, page, Dc = cache.shape
+    B, cols = page_table.shape
+    n = int(lib().ig_attention_workspace_bytes(
+        _ATTN_SHAPE(T, hq * D, hq * D, hq, 0, 1.0, 0),
+        _KV_CACHE(0, 0, 0, 0, 0, page, heads, Dc, 0),
+        _BATCH(0, 0, 0, cols, B, T if max_q is None else max_q)))
+    if n == 0 or Dc != D:
+        raise IGError(-2, "ig_attention_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(q, cache, scales, cu, kv_len, page_table, out, ws, *, max_q=None, scale=None,
+                    flags=0, stream=None):
+    """Attention of the new tokens (q [T][heads][D]) over the cache, causal at the
+    end of each sequence, into out (not q). scale None: 1 / sqrt(D). max_q: no
+    sequence has more new tokens (None: as many as there are); it and the number
+    of sequences and pages decide how large ws has to be (attention_workspace)."""
+    import torch
+    what, b16 = "paged_attention", torch.bfloat16
+    dev = q.get_device()
+    T, hq, D, ld_q = _heads(what, "q", q, dev, b16)
+    ld_o = _like(what, "out", out, dev, b16, T, hq, D)
+    c, heads, Dc = _cache_of(what, cache, scales, dev, torch.uint8)
+    if Dc != D:
+        _why(what, "q", q, dev, b16, (T, hq, Dc))
+    b = _batch_of(what, cu, kv_len, page_table, dev, torch.int32, T if max_q is None else max_q)
+    _status_ws(what, ws, dev, torch.uint8)
+    rc = (_LIB or lib()).ig_paged_attention(
+        _ATTN_SHAPE(T, ld_q, ld_o, hq, flags, D ** -0.5 if scale is None else scale, 0), c, b,
+        q.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_of(what, dev, stream, torch))
     if rc:
         raise IGError(rc, what)

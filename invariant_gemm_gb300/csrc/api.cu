@@ -446,6 +446,7 @@ const char* ig_status_string(int s) {
     case IG_ERR_ADAPTER_RANGE: return "adapter index out of range";
     case IG_ERR_TIMEOUT: return "bounded device wait expired";
     case IG_ERR_UNSUPPORTED: return "unsupported by this build";
+    case IG_ERR_INDEX_RANGE: return "position, page number or length out of range";
     default: return "unknown status";
   }
 }
@@ -570,7 +571,7 @@ int ig_check_status(void* ws, size_t ws_bytes, void* stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return IG_ERR_CUDA;
   if (status & kStatusTimeout) return IG_ERR_TIMEOUT;
   if (status & kStatusCorrupt) return IG_ERR_WS_CORRUPT;
-  return IG_ERR_ADAPTER_RANGE;
+  return status & kStatusAdapterRange ? IG_ERR_ADAPTER_RANGE : IG_ERR_INDEX_RANGE;
 }
 
 }  // extern "C"

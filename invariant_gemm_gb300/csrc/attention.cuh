@@ -1,0 +1,150 @@
+// What the calls of a served layer's attention share: the batch and cache as
+// the kernels see them, the head norm's launch parameters, the e4m3 format.
+//
+// Cache: codes [pages][2][heads][page][D] (e4m3), scales [pages][2][heads]
+// [page / 16] (E8M0). Scales are powers of two, so a code times its scale is
+// exact in every format with e4m3's three mantissa bits and the range, and the
+// kernels may apply a scale to codes, products or sums alike.
+#pragma once
+
+#include "mx4.cuh"
+
+namespace ig {
+
+constexpr int kKvBlock = 16;            // tokens that share a scale
+constexpr int kKvMinExp = -120;         // least scale that the append writes: 2^-120
+
+// Batch and cache.
+struct KvParams {
+  uint8_t* codes;
+  uint8_t* scales;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  uint32_t* status;
+  int64_t pages, page_stride, scale_stride, ld_table;
+  int64_t T;
+  int32_t batch, max_q, heads, page_shift;
+};
+
+struct RopeParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* w_q;
+  const __nv_bfloat16* w_k;
+  const float* cos_sin;
+  const int32_t* positions;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  uint32_t* status;
+  int64_t T, table_rows, ld_q, ld_k, ld_qo, ld_ko;
+  int32_t heads_q, heads_k, rot, interleaved, plus_one;
+  float eps;
+};
+
+struct AppendParams {
+  RopeParams r;
+  KvParams c;
+  const __nv_bfloat16* v;
+  int64_t ld_v;
+  int32_t nblocks;      // blocks of a sequence that max_q tokens can touch
+};
+
+struct GatherParams {
+  KvParams c;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int64_t ld_k, ld_v;
+};
+
+struct AttnParams {
+  CUtensorMap tm;       // codes as {D, 2 heads page, pages} bytes, box {D, 16, 1}, swizzled by rows
+  KvParams c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  uint32_t* counters;
+  float* parts;         // partial results [item][rows][D]
+  float* part_ml;       // [item][rows][kPartWords]
+  int64_t ld_q, ld_out;
+  int32_t heads_q, group;   // query heads, and of one kv head
+  int32_t few_rows;     // sequences with at most this many rows a kv head are the split kernel's
+  int32_t max_tiles;    // 16-row tiles of such a sequence
+  int32_t part_rows;
+  int32_t flags;
+  float scale_log2;     // scale * log2(e)
+};
+
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_kv_append(const AppendParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_kv_gather(const GatherParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st);
+
+// {D, rows of a page, pages} of codes; box {D, 16, 1}, rows of 128 or 64 bytes
+// swizzled by as much. IG_OK or IG_ERR_CUDA.
+int encode_map_codes(CUtensorMap* map, const void* base, int head_dim, uint64_t rows,
+                     uint64_t pages, uint64_t page_stride);
+
+// --- splitting a sequence ---------------------------------------------------
+// A sequence's tokens are cut into parts of a length that kv_len alone fixes
+// (so that a row's bits do not depend on the batch): whole 512s, at most 32 of
+// them.
+constexpr int kSplitTokens = 512;
+constexpr int kMaxSplits = 32;
+constexpr int kPartWords = 4;           // of a row of a part: maximum, sum, exponent, unused
+__host__ __device__ inline int split_tokens(int kv) {
+  return kSplitTokens * ((kv + kSplitTokens * kMaxSplits - 1) / (kSplitTokens * kMaxSplits));
+}
+
+#ifdef __CUDACC__
+// New tokens of sequence b: rows row0 .. row0 + n - 1, the last of kv tokens.
+// False (and the status word says so) where they are out of range.
+__device__ __forceinline__ bool sequence_of(const KvParams& c, int b, int& row0, int& n, int& kv) {
+  row0 = __ldg(c.cu + b);
+  n = __ldg(c.cu + b + 1) - row0;
+  kv = __ldg(c.kv_len + b);
+  return row0 >= 0 && n >= 0 && n <= c.max_q && (int64_t)row0 + n <= c.T && kv >= 0 &&
+         (int64_t)kv <= (c.ld_table << c.page_shift);
+}
+
+// 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+// 2^e for e from -126 to 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Two e4m3 codes (the low one in bits 0-7) -> two FP16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+// Two FP32 values -> two e4m3 codes, to nearest, ties to even; NaN is NaN.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t v) {
+  float lo, hi;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(v));
+  return make_float2(lo, hi);
+}
+// Eight values of eight codes.
+__device__ __forceinline__ void e4m3_decode8(uint2 c, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? c.x : c.y;
+    const float2 t = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(i & 1 ? w >> 16 : w & 0xffffu)));
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ uint2 e4m3_encode8(const float (&f)[8]) {
+  return make_uint2(f32x2_to_e4m3x2(f[0], f[1]) | f32x2_to_e4m3x2(f[2], f[3]) << 16,
+                    f32x2_to_e4m3x2(f[4], f[5]) | f32x2_to_e4m3x2(f[6], f[7]) << 16);
+}
+#endif  // __CUDACC__
+
+}  // namespace ig

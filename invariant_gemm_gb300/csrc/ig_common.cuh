@@ -37,6 +37,7 @@ constexpr int kMaxAdapters = 1023;  // token-map groups G = L + 1 <= 1024
 constexpr uint32_t kStatusAdapterRange = 1u << 0;
 constexpr uint32_t kStatusCorrupt = 1u << 1;
 constexpr uint32_t kStatusTimeout = 1u << 2;
+constexpr uint32_t kStatusIndexRange = 1u << 3;
 
 __host__ __device__ constexpr size_t align_up(size_t v, size_t a) {
   return (v + a - 1) / a * a;

@@ -4,7 +4,7 @@
 #include <cudaTypedefs.h>
 #include <mutex>
 
-#include "ig_common.cuh"
+#include "attention.cuh"
 
 namespace ig {
 
@@ -50,6 +50,20 @@ int encode_map_a3(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? IG_OK : IG_ERR_CUDA;
+}
+
+int encode_map_codes(CUtensorMap* map, const void* base, int head_dim, uint64_t rows,
+                     uint64_t pages, uint64_t page_stride) {
+  if (!encoder()) return IG_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, rows, pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim, page_stride};
+  const cuuint32_t box[3] = {(cuuint32_t)head_dim, (cuuint32_t)kKvBlock, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IG_OK : IG_ERR_CUDA;
 }
 
