@@ -78,11 +78,16 @@ cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t 
 cudaError_t launch_kv_append(const AppendParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_kv_gather(const GatherParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attention_prompt(const AttnParams& p, int head_dim, cudaStream_t st);
 
 // {D, rows of a page, pages} of codes; box {D, 16, 1}, rows of 128 or 64 bytes
 // swizzled by as much. IG_OK or IG_ERR_CUDA.
 int encode_map_codes(CUtensorMap* map, const void* base, int head_dim, uint64_t rows,
                      uint64_t pages, uint64_t page_stride);
+
+// Sequences of at most this many rows a kv head are the split kernel's, the
+// others the prompt kernel's.
+constexpr int kFewRows = 64;
 
 // --- splitting a sequence ---------------------------------------------------
 // A sequence's tokens are cut into parts of a length that kv_len alone fixes

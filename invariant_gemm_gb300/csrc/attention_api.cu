@@ -160,7 +160,7 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
   pl->group = s->heads_q / c->heads;
   const int64_t rows = (int64_t)pl->group * b->max_q;
   if (rows > (1 << 28)) return IG_ERR_UNSUPPORTED;
-  pl->max_tiles = (int)((rows + 15) / 16);
+  pl->max_tiles = (int)(((rows < kFewRows ? rows : kFewRows) + 15) / 16);
   if ((int64_t)b->batch * pl->max_tiles * c->heads > kMaxCounters) return IG_ERR_UNSUPPORTED;
   pl->part_rows = (int)(rows < 16 ? rows : 16);
   const int64_t cap = b->ld_table * c->page;
@@ -295,12 +295,17 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.ld_out = shape->ld_out;
   p.heads_q = shape->heads_q;
   p.group = pl.group;
-  p.few_rows = 0x7fffffff;
+  p.few_rows = kFewRows;
   p.max_tiles = pl.max_tiles;
   p.part_rows = pl.part_rows;
   p.flags = shape->flags;
   p.scale_log2 = shape->scale * 1.4426950408889634f;
-  return cuda_status(launch_attention_split(p, cache->head_dim, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((int64_t)batch->max_q * pl.group > kFewRows && shape->T * pl.group > kFewRows) {
+    const cudaError_t e = launch_attention_prompt(p, cache->head_dim, st);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return cuda_status(launch_attention_split(p, cache->head_dim, st));
 }
 
 }  // extern "C"

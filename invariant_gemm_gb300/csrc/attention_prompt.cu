@@ -1,0 +1,642 @@
+// Attention of many query rows over the 8-bit paged cache: prompts and chunks of
+// them, on the tcgen05 tensor cores.
+//
+// A block takes 256 rows of one kv head (`group` query heads for each new
+// token), two tiles of 128 (the MMA's M), and walks the tokens that they see 128
+// at a time:
+//   S = Q K^T   kind::f8f6f4. The keys' codes are the B operand as TMA leaves
+//               them. A query row, scaled by a power of two to a maximum of 128
+//               to 256, is the sum of two e4m3 numbers: 8 significant bits are 4
+//               and, of what is left, 4 more (values under 2^-9 of the row's
+//               maximum are off by at most 2^-17 of it). Two MMAs at twice the
+//               rate of one in FP16, and no conversion of the keys.
+//   O += P V    kind::f16. P goes back to tensor memory over S, as FP16; the
+//               values' codes are FP16 numbers too, converted by a warpgroup of
+//               their own into the MMA's order (tokens along K, so V as it lies:
+//               the MN-major operand).
+// Softmax as in the split kernel: base 2, whole exponents, a row's maximum raised
+// only past m + 7, value scales folded into P, key scales into the logits.
+//
+// Warps: 0-3 and 4-7 the softmax of a tile each, a row to a thread; 8-11 the
+// values; 12 the copies; 13 the MMAs. The two tiles take turns: while one is in
+// the softmax the tensor cores work on the other.
+#include "attention.cuh"
+#include "umma_mx4.cuh"
+
+namespace ig {
+
+namespace {
+
+constexpr int kTile = 128;              // rows of a tile, tokens of a step
+constexpr int kThreads = 512;
+constexpr float kHeadroom = 7.0f;
+constexpr float kBias = 8.0f;
+constexpr int kMinShift = -40;
+constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
+constexpr int kNoBlock = 2000;          // tokens that no row sees, or an absent page
+constexpr int kInfo = 4;                // steps whose scales are held
+
+template <int D>
+struct Smem {
+  static constexpr int kPart = kTile * D;               // bytes of 128 rows of codes
+  static constexpr int kQ = 0;                          // [tile][hi, lo]
+  static constexpr int kK = kQ + 4 * kPart;             // [2]
+  static constexpr int kV8 = kK + 2 * kPart;            // [2]
+  static constexpr int kV16 = kV8 + 2 * kPart;          // [2]
+  static constexpr int kEnd = kV16 + 4 * kPart;
+  uint64_t k_full[2], k_empty[2], v8_full[2], v8_empty[2], v16_full[2], v16_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t info_full[kInfo], info_empty[kInfo], drain;
+  float ks[kInfo][8];
+  int ve[kInfo][8];
+  int partly[kInfo];                    // some block of the step is not there
+  int nan_at[D];
+  uint32_t tmem;
+  int dead;
+  int item[8];
+};
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+__device__ __forceinline__ float qnan() { return __uint_as_float(0x7fc00000u); }
+__device__ __forceinline__ float pow2_down(float d) {
+  if (d != d) return d;
+  return d < -126.0f ? 0.0f : pow2((int)d);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// D[m][n] = sum_k A[m][k] B[n][k], FP32: e4m3 operands along K; FP16 with B in
+// rows of n.
+__host__ __device__ constexpr uint32_t idesc_f8(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_f16_nt(int m, int n) {
+  return (1u << 4) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// Rows of D bytes, swizzled by as much, 8-row groups 8 D bytes apart.
+template <int D>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)((8 * D) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(D == 128 ? 2 : 4) << 61;             // SWIZZLE_128B, SWIZZLE_64B
+  return d;
+}
+// FP16 rows along n: atoms of 64 n (128 bytes) x 8 tokens, 1024 bytes, one after
+// the other along the tokens; the next 64 n 128 tokens further.
+__device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((kTile * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void mma_f16_tm(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+#define IG_ST32(taddr, r)                                                                        \
+  asm volatile(                                                                                  \
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "  \
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "    \
+      "%28, %29, %30, %31, %32};" ::"r"(taddr), "r"((r)[0]), "r"((r)[1]), "r"((r)[2]),           \
+      "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]), "r"((r)[7]), "r"((r)[8]),              \
+      "r"((r)[9]), "r"((r)[10]), "r"((r)[11]), "r"((r)[12]), "r"((r)[13]), "r"((r)[14]),         \
+      "r"((r)[15]), "r"((r)[16]), "r"((r)[17]), "r"((r)[18]), "r"((r)[19]), "r"((r)[20]),        \
+      "r"((r)[21]), "r"((r)[22]), "r"((r)[23]), "r"((r)[24]), "r"((r)[25]), "r"((r)[26]),        \
+      "r"((r)[27]), "r"((r)[28]), "r"((r)[29]), "r"((r)[30]), "r"((r)[31]) : "memory")
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Bounded wait that also ends when any other wait of the block gave up.
+template <typename S>
+__device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&s.dead)) return false;
+    if (clock64() - t0 > (1ll << 31)) {
+      *reinterpret_cast<volatile int*>(&s.dead) = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ AttnParams p) {
+  using S = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  S& s = *reinterpret_cast<S*>(raw + S::kEnd);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+      mbar_init(&s.v8_full[i], 1);
+      mbar_init(&s.v8_empty[i], 4);
+      mbar_init(&s.v16_full[i], 4);
+      mbar_init(&s.v16_empty[i], 1);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 4);
+    }
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(&s.info_full[i], 1);
+      mbar_init(&s.info_empty[i], 12);
+    }
+    mbar_init(&s.drain, 1);
+    s.dead = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tm);
+  }
+  if (tid < D) s.nan_at[tid] = 0x7fffffff;
+  griddep_wait();
+
+  // the block's rows: sequences in order, a sequence's last rows first
+  if (warp == 0) {
+    int at = blockIdx.x, found = -1;
+    for (int b0 = 0; b0 < p.c.batch && found < 0; b0 += 32) {
+      int row0, n, kv, count = 0;
+      if (b0 + lane < p.c.batch && sequence_of(p.c, b0 + lane, row0, n, kv) &&
+          n * p.group > p.few_rows)
+        count = (n * p.group + 2 * kTile - 1) / (2 * kTile) * p.c.heads;
+      int sum = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, at < sum);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        if (lane == l) {
+          const int v = at - (sum - count);
+          s.item[0] = b0 + l;
+          s.item[1] = v % p.c.heads;
+          s.item[2] = count / p.c.heads - 1 - v / p.c.heads;
+          s.item[3] = row0;
+          s.item[4] = n;
+          s.item[5] = kv;
+        }
+        found = b0 + l;
+      }
+      at -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) s.item[6] = found;
+    __syncwarp();
+    if (found >= 0) {
+      tmem_alloc(&s.tmem, 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s.item[6] < 0) return;
+  const int b = s.item[0], h = s.item[1], row_first = s.item[2] * 2 * kTile;
+  const int row0 = s.item[3], n = s.item[4], kv = s.item[5];
+  const int all_rows = n * p.group;
+  const int rows = min(2 * kTile, all_rows - row_first);
+  const int tiles = rows > kTile ? 2 : 1;
+  const int low = kv - n + row_first / p.group;                  // last token its first row sees
+  const int high = kv - n + (row_first + rows - 1) / p.group;    // and its last row
+  const int steps = high >= 0 ? high / kTile + 1 : 0;
+  const uint32_t tmem = s.tmem;
+
+  // ---- queries: a row to a thread of the first two warpgroups
+  float f = 0.0f;                       // logit of a product, base 2
+  int lim = 0x7fffffff;                 // last token that the row sees
+  if (warp < 8) {
+    const int r = tid, gr = row_first + r;
+    const bool in = r < rows;
+    const int tok = gr / p.group, head = h * p.group + gr % p.group;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(row0 + tok) * p.ld_q +
+                                                      (int64_t)head * D);
+    if (in) lim = kv - n + tok;
+    uint32_t top = 0;
+    uint4 w[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+    }
+    const int e = (int)(top >> 7);      // the largest value is below 2^(e - 126)
+    float up = e == 255 ? qnan() : pow2(134 - max(e, 20));
+    f = fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
+    if (p.scale_log2 < 0.0f) up = -up;
+    uint8_t* hi = raw + S::kQ + (r >> 7) * 2 * S::kPart + (r & 127) * D;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {  // 16 values: 16 bytes of each part
+      uint32_t a[4], c[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x[8], y[8];
+        unpack8(w[2 * i + j], x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= up;
+        const uint2 q = e4m3_encode8(x);
+        e4m3_decode8(q, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
+        const uint2 t = e4m3_encode8(y);
+        a[2 * j] = q.x; a[2 * j + 1] = q.y;
+        c[2 * j] = t.x; c[2 * j + 1] = t.y;
+      }
+      const int at = (D == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) * 16;
+      *reinterpret_cast<uint4*>(hi + at) = make_uint4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<uint4*>(hi + S::kPart + at) = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+    fence_proxy_async_smem();
+  }
+  if (tid == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT)) {      // as if a wait had expired
+    s.dead = 1;
+    atomicOr(p.c.status, kStatusTimeout);
+  }
+  __syncthreads();
+
+  if (warp < 4 * tiles) {
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * D + lanes;
+    const int tile_low = kv - n + (row_first + t * kTile) / p.group;
+    float m = neg_inf(), l = 0.0f;
+    int expo = -1000;
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      const int in = j % kInfo;
+      ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
+           wait(s, &s.s_full[t], j & 1, p.c.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const int t0 = j * kTile;
+      const bool masks = t0 + kTile - 1 > tile_low || s.partly[in];
+      // the row's largest logit
+      float x = neg_inf();
+      int et = -1000;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld32(ts + 32 * c, v);
+        if (masks) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (t0 + 32 * c + i > lim || s.ve[in][2 * c + i / 16] == kNoBlock) v[i] = neg_inf();
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float y = v[16 * q];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) y = fmaxf(y, v[16 * q + i]);
+          y = y == neg_inf() ? y : y * (f * s.ks[in][2 * c + q]);
+          x = fmaxf(x, y);
+          const int e = s.ve[in][2 * c + q];
+          if (e < kNaNExp) et = max(et, e);
+        }
+      }
+      float down = 1.0f;
+      if (x > m + kHeadroom) {
+        const float up = ceilf(x);
+        down = m == neg_inf() ? 0.0f : pow2_down(m - up);
+        m = up;
+      }
+      l *= down;
+      if (et > expo) {
+        if (expo > -1000) down *= pow2(max(expo - et, -126));
+        expo = et;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tmem_ld32(to + 32 * c, v);
+          uint32_t u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * down);
+          IG_ST32(to + 32 * c, u);
+        }
+      }
+      const float base = m == neg_inf() ? 0.0f : m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld32(ts + 32 * c, v);
+        uint32_t u[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int e = s.ve[in][2 * c + q];
+          const int shift = e < kNaNExp ? max(e - expo, kMinShift) : 0;
+          const float k = f * s.ks[in][2 * c + q], off = base - (kBias + (float)shift);
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float a = ex2(fmaf(v[16 * q + i], k, -off));
+            float d = ex2(fmaf(v[16 * q + i + 1], k, -off));
+            if (masks) {
+              const int at = t0 + 32 * c + 16 * q + i;
+              if (at > lim || e == kNoBlock) a = 0.0f;
+              if (at + 1 > lim || e == kNoBlock) d = 0.0f;
+            }
+            sum += a + d;
+            u[8 * q + i / 2] = f16x2_of(a, d);
+          }
+          l = fmaf(sum, pow2(-shift), l);
+        }
+        tmem_st16(ts + 16 * c, u);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s.info_empty[in]);
+        mbar_arrive(&s.p_full[t]);
+      }
+    }
+    // ---- the rows' results
+    if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(s, &s.s_full[t], steps & 1, p.c.status));
+    tc_fence_after();
+    if (ok) {
+      const int r = tid, gr = row_first + r;
+      const bool in = r < rows;
+      const int tok = gr / p.group, head = h * p.group + gr % p.group;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(row0 + tok) * p.ld_out +
+                                            (int64_t)head * D);
+      const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        if (steps > 0) {
+          tmem_ld32(to + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[i] = l == 0.0f ? 0.0f : v[i] * inv;
+          if (lim >= s.nan_at[32 * c + i]) v[i] = qnan();
+        }
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[4 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
+                                        f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
+                                        f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
+                                        f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // the second tile has no rows: only its share of the scales' barrier
+    for (int j = 0; j < steps; ++j) {
+      const int in = j % kInfo;
+      if (!wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.info_empty[in]);
+    }
+  } else if (warp < 12) {
+    // ----------------------------------------------------------------- values
+    const int r = tid - 256;            // token of the step
+    for (int j = 0; j < steps; ++j) {
+      const int in = j % kInfo, st = j & 1;
+      bool ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
+                wait(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
+                wait(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int at = j * kTile + r, e = s.ve[in][r >> 4];
+      const uint8_t* src = raw + S::kV8 + st * S::kPart + r * D;
+      uint8_t* dst = raw + S::kV16 + st * 2 * S::kPart + r * 128;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint4 w = *reinterpret_cast<const uint4*>(
+            src + (D == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) * 16);
+        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if (e == kNaNExp) u[0] = u[1] = u[2] = u[3] = 0x7f7f7f7fu;
+        if (at > high || e == kNoBlock) {
+          u[0] = u[1] = u[2] = u[3] = 0;               // p is 0, but 0 times NaN is not
+        } else if (at > low) {
+          // seen by some rows: a NaN is kept for those
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            if (bad) {
+              for (int q = 0; q < 4; ++q)
+                if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[16 * i + 4 * k + q], at);
+              u[k] &= ~((bad >> 7) * 0xffu);
+            }
+          }
+        }
+        // values 16 i .. 16 i + 15: two chunks of 16 bytes of a row of 64 values
+        uint8_t* row = dst + (i >> 2) * (kTile * 128);
+        const int c = 2 * (i & 3);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a = u[2 * k], d = u[2 * k + 1];
+          *reinterpret_cast<uint4*>(row + ((c + k) ^ (r & 7)) * 16) =
+              make_uint4(e4m3x2_to_f16x2((uint16_t)a), e4m3x2_to_f16x2((uint16_t)(a >> 16)),
+                         e4m3x2_to_f16x2((uint16_t)d), e4m3x2_to_f16x2((uint16_t)(d >> 16)));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s.info_empty[in]);
+        mbar_arrive(&s.v8_empty[st]);
+        mbar_arrive(&s.v16_full[st]);
+      }
+    }
+  } else if (warp == 12) {
+    // ----------------------------------------------------------------- copies
+    const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
+    const int blocks = 1 << (p.c.page_shift - 4);
+    int asked = 0;
+    for (int j = 0; j < steps; ++j) {
+      const int in = j % kInfo, st = j & 1;
+      // lane l looks up block l of the step
+      const int tok = j * kTile + lane * kKvBlock;
+      bool there = lane < 8 && tok <= high;
+      int32_t page = 0;
+      uint32_t kb = 127, vb = 0;
+      const int row = tok & ((1 << p.c.page_shift) - 1);
+      if (there) {
+        page = __ldg(table + (tok >> p.c.page_shift));
+        there = page >= 0 && page < p.c.pages;
+        if (!there) atomicOr(p.c.status, kStatusIndexRange);
+      }
+      if (there) {
+        const uint8_t* sc = p.c.scales + page * p.c.scale_stride + h * blocks + row / kKvBlock;
+        kb = __ldg(sc);
+        vb = __ldg(sc + p.c.heads * blocks);
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, there);
+      bool ok = wait(s, &s.info_empty[in], ((j / kInfo) & 1) ^ 1, p.c.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane < 8) {
+        s.ks[in][lane] = e8m0_value(kb);
+        s.ve[in][lane] = !there ? kNoBlock : vb == 255 ? kNaNExp : (int)vb - 127;
+      }
+      if (lane == 0) s.partly[in] = have != 0xffu;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.info_full[in]);
+      ok = wait(s, &s.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t bytes = __popc(have) * (kKvBlock * D);
+      if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], bytes);
+      __syncwarp();
+      if (there)
+        tma_load_3d(raw + S::kK + st * S::kPart + lane * (kKvBlock * D), &p.tm, 0,
+                    (h << p.c.page_shift) + row, page, &s.k_full[st]);
+      ok = wait(s, &s.v8_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        // the keys' copy of this step is in flight, the values' is not
+        mbar_wait_bounded(&s.k_full[st], (j >> 1) & 1, p.c.status);
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&s.v8_full[st], bytes);
+      __syncwarp();
+      if (there)
+        tma_load_3d(raw + S::kV8 + st * S::kPart + lane * (kKvBlock * D), &p.tm, 0,
+                    ((p.c.heads + h) << p.c.page_shift) + row, page, &s.v8_full[st]);
+      asked = j + 1;
+    }
+    if (*reinterpret_cast<volatile int*>(&s.dead)) {
+      // copies still in flight land before the block leaves
+      for (int j = max(asked - 2, 0); j < asked; ++j) {
+        mbar_wait_bounded(&s.k_full[j & 1], (j >> 1) & 1, p.c.status);
+        mbar_wait_bounded(&s.v8_full[j & 1], (j >> 1) & 1, p.c.status);
+      }
+    }
+  } else if (warp == 13 && steps > 0) {
+    // ------------------------------------------------------------------- MMAs
+    constexpr uint32_t iqk = idesc_f8(kTile, kTile), ipv = idesc_f16_nt(kTile, D);
+    const uint32_t base = smem_u32(raw);
+    auto qk = [&](int t, int j) {
+      const uint32_t q = base + S::kQ + t * 2 * S::kPart, k = base + S::kK + (j & 1) * S::kPart;
+      if (elect_one()) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            mma_f8(tmem + t * kTile, desc_rows<D>(q + part * S::kPart + 32 * i),
+                   desc_rows<D>(k + 32 * i), iqk, part + i > 0);
+        umma_commit(&s.s_full[t]);
+      }
+      __syncwarp();
+    };
+    bool ok = wait(s, &s.k_full[0], 0, p.c.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      for (int t = 0; t < tiles; ++t) qk(t, 0);
+      if (elect_one()) umma_commit(&s.k_empty[0]);
+      __syncwarp();
+    }
+    for (int j = 0; ok && j < steps; ++j) {
+      ok = wait(s, &s.v16_full[j & 1], (j >> 1) & 1, p.c.status);
+      if (ok && j + 1 < steps)
+        ok = wait(s, &s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.c.status);
+      for (int t = 0; t < tiles; ++t) {
+        ok = ok && wait(s, &s.p_full[t], j & 1, p.c.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v = base + S::kV16 + (j & 1) * 2 * S::kPart;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_f16_tm(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * i,
+                       desc_values(v + 2048 * i), ipv, j > 0 || i > 0);
+          if (j + 1 == steps) umma_commit(&s.s_full[t]);
+        }
+        __syncwarp();
+        if (j + 1 < steps) qk(t, j + 1);
+      }
+      if (!ok) break;
+      if (elect_one()) {
+        umma_commit(&s.v16_empty[j & 1]);
+        if (j + 1 < steps) umma_commit(&s.k_empty[(j + 1) & 1]);
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (s.dead && warp == 13) {
+    // MMAs still at work end before the tensor memory is given back
+    tc_fence_after();
+    if (elect_one()) umma_commit(&s.drain);
+    __syncwarp();
+    mbar_wait_bounded(&s.drain, 0, p.c.status);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnParams& p, cudaStream_t st) {
+  const size_t smem = Smem<D>::kEnd + sizeof(Smem<D>);
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  // at most so many tiles: whole ones, and one more for each sequence that can
+  // have more rows than the split kernel takes
+  const int64_t rows = p.c.T * p.group;
+  const int64_t seqs = rows / (p.few_rows + 1);
+  const int64_t tiles = rows / (2 * kTile) + (seqs < p.c.batch ? seqs : p.c.batch);
+  return launch_pdl(prompt_kernel<D>, dim3((unsigned)(tiles * p.c.heads)), dim3(kThreads), smem, st,
+                    p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prompt(const AttnParams& p, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
+}
+
+}  // namespace ig

@@ -85,8 +85,11 @@ class Batch:
         FP32 one. A logit of products that sum to A in
         magnitude is off by 2^-16 A at most: D / 16 tensor-core sums of 16 exact
         products into FP32 (each within 2^-20 of the magnitudes added), two FP32
-        products and the rounding of the exponential's argument. Both count
-        twice, in p and in the sum of p, over sum p |v|."""
+        products and the rounding of the exponential's argument. Where a sequence
+        has more than 64 rows a kv head, a query is two e4m3 numbers: exact but for
+        values under 2^-9 of the row's largest, off by at most 2^-17 of it (steps of
+        2^-9 where the largest is 2^7 at least). These count twice, in p and in the
+        sum of p, over sum p |v|."""
         scale = self.D ** -0.5 if scale is None else scale
         q = f64(q)
         out, tol = np.zeros(q.shape), np.zeros(q.shape)
@@ -97,7 +100,12 @@ class Batch:
             absent = (bad < 0) | (bad >= self.pages)
             o, size, big = ref.attention(q[r], k, v, scale, absent)
             out[r] = o
-            tol[r] = 2.0 ** -8 * np.abs(o) + 2 * (2.0 ** -11 + 2.0 ** -16 * big) * size
+            logit = 2.0 ** -16 * big
+            if n * self.hq // self.hkv > 64 and kv:
+                kk = np.nan_to_num(np.abs(k)).sum(-1).max()
+                logit = logit + 2.0 ** -17 * abs(scale) * kk * np.nan_to_num(
+                    np.abs(q[r])).max(-1, keepdims=True)
+            tol[r] = 2.0 ** -8 * np.abs(o) + 2 * (2.0 ** -11 + logit) * size
             top = np.abs(np.where(np.isfinite(v), v, 0)).max(initial=0.0)
             tol[r] += kv * 2.0 ** -31 * top
         return out, tol

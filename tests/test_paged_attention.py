@@ -102,6 +102,18 @@ def test_sizes_of_the_queries():
     b.check(q, b.attend(q))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_sizes_of_the_queries_of_a_prompt(D):
+    need_gpu()
+    b = Batch([(120, 150)], 4, 1, D, 32, seed=21).fill()
+    q = b.rows(4).float()
+    q *= torch.from_numpy(2.0 ** b.rng.integers(-60, 3, (b.T, 4, 1))).float()
+    q[50:] *= torch.from_numpy(2.0 ** b.rng.integers(-14, 1, (b.T - 50, 4, D))).float()
+    q[7] = 0
+    q = q.to(B16)
+    b.check(q, b.attend(q))
+
+
 def test_a_sharp_maximum_late_and_early():
     """One token outweighs the others by more than p's range, at the first, a middle
     and the last place."""
