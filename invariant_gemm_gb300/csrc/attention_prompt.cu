@@ -117,16 +117,76 @@ __device__ __forceinline__ void mma_f16_tm(uint32_t d, uint32_t a, uint64_t b, u
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
-#define IG_ST32(taddr, r)                                                                        \
-  asm volatile(                                                                                  \
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "  \
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "    \
-      "%28, %29, %30, %31, %32};" ::"r"(taddr), "r"((r)[0]), "r"((r)[1]), "r"((r)[2]),           \
-      "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]), "r"((r)[7]), "r"((r)[8]),              \
-      "r"((r)[9]), "r"((r)[10]), "r"((r)[11]), "r"((r)[12]), "r"((r)[13]), "r"((r)[14]),         \
-      "r"((r)[15]), "r"((r)[16]), "r"((r)[17]), "r"((r)[18]), "r"((r)[19]), "r"((r)[20]),        \
-      "r"((r)[21]), "r"((r)[22]), "r"((r)[23]), "r"((r)[24]), "r"((r)[25]), "r"((r)[26]),        \
-      "r"((r)[27]), "r"((r)[28]), "r"((r)[29]), "r"((r)[30]), "r"((r)[31]) : "memory")
+// 32 columns of this thread's lane, on their way until tmem_wait_ld; loaded32
+// keeps their uses behind it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void loaded32(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                    "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                    "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+  asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                    "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                    "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Pairs of FP32 values: one instruction for both.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A warpgroup's share of the block's registers (512 threads launched with 128).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -296,8 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
+  // 256 threads with 192 registers and 256 with 64: the 65536 of the launch
   if (warp < 4 * tiles) {
     // ---------------------------------------------------------------- softmax
+    more_registers<192>();
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * D + lanes;
@@ -313,29 +375,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int t0 = j * kTile;
-      const bool masks = t0 + kTile - 1 > tile_low || s.partly[in];
-      // the row's largest logit
+      // the row's products, all in registers; columns that it does not see are
+      // -inf: in few steps, so the others have no look at them
+      float v[kTile];
+      tmem_ld32_async(ts, v);
+      tmem_ld32_async(ts + 32, v + 32);
+      tmem_ld32_async(ts + 64, v + 64);
+      tmem_ld32_async(ts + 96, v + 96);
+      int ve[8];
+      float k[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        ve[q] = s.ve[in][q];
+        k[q] = f * s.ks[in][q];         // not 0: times -inf it would be no number
+        if (k[q] < 1.18e-38f) k[q] = 1.18e-38f;
+      }
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) loaded32(v + 32 * c);
+      if (t0 + kTile - 1 > tile_low || s.partly[in]) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i)
+          if (t0 + i > lim || ve[i / 16] == kNoBlock) v[i] = neg_inf();
+      }
       float x = neg_inf();
       int et = -1000;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld32(ts + 32 * c, v);
-        if (masks) {
+      for (int q = 0; q < 8; ++q) {
+        float y = max3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (t0 + 32 * c + i > lim || s.ve[in][2 * c + i / 16] == kNoBlock) v[i] = neg_inf();
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float y = v[16 * q];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) y = fmaxf(y, v[16 * q + i]);
-          y = y == neg_inf() ? y : y * (f * s.ks[in][2 * c + q]);
-          x = fmaxf(x, y);
-          const int e = s.ve[in][2 * c + q];
-          if (e < kNaNExp) et = max(et, e);
-        }
+        for (int i = 3; i < 15; i += 2) y = max3(y, v[16 * q + i], v[16 * q + i + 1]);
+        y = fmaxf(y, v[16 * q + 15]);
+        x = fmaxf(x, y * k[q]);
+        if (ve[q] < kNaNExp) et = max(et, ve[q]);
       }
       float down = 1.0f;
       if (x > m + kHeadroom) {
@@ -350,40 +422,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float v[32];
-          tmem_ld32(to + 32 * c, v);
-          uint32_t u[32];
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16];
+          tmem_ld16(to + 16 * c, o);
+          uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * down);
-          IG_ST32(to + 32 * c, u);
+          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * down);
+          tmem_st16(to + 16 * c, u);
         }
       }
       const float base = m == neg_inf() ? 0.0f : m;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld32(ts + 32 * c, v);
         uint32_t u[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int e = s.ve[in][2 * c + q];
+          const int e = ve[2 * c + q];
           const int shift = e < kNaNExp ? max(e - expo, kMinShift) : 0;
-          const float k = f * s.ks[in][2 * c + q], off = base - (kBias + (float)shift);
-          float sum = 0.0f;
+          const float off = (kBias + (float)shift) - base;
+          const uint64_t kk = pair2(k[2 * c + q], k[2 * c + q]), oo = pair2(off, off);
+          uint64_t sum = 0;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            float a = ex2(fmaf(v[16 * q + i], k, -off));
-            float d = ex2(fmaf(v[16 * q + i + 1], k, -off));
-            if (masks) {
-              const int at = t0 + 32 * c + 16 * q + i;
-              if (at > lim || e == kNoBlock) a = 0.0f;
-              if (at + 1 > lim || e == kNoBlock) d = 0.0f;
-            }
-            sum += a + d;
+            const float* at = v + 32 * c + 16 * q + i;
+            const float2 y = split2(fma2(pair2(at[0], at[1]), kk, oo));
+            const float a = ex2(y.x), d = ex2(y.y);
+            sum = add2(sum, pair2(a, d));
             u[8 * q + i / 2] = f16x2_of(a, d);
           }
-          l = fmaf(sum, pow2(-shift), l);
+          const float2 both = split2(sum);
+          l = fmaf(both.x + both.y, pow2(-shift), l);
         }
         tmem_st16(ts + 16 * c, u);
       }
@@ -431,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {
     // the second tile has no rows: only its share of the scales' barrier
+    more_registers<192>();
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo;
       if (!wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
@@ -439,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 12) {
     // ----------------------------------------------------------------- values
+    fewer_registers<64>();
     const int r = tid - 256;            // token of the step
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
@@ -488,7 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&s.v16_full[st]);
       }
     }
-  } else if (warp == 12) {
+  } else {
+   fewer_registers<64>();
+   if (warp == 12) {
     // ----------------------------------------------------------------- copies
     const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
     const int blocks = 1 << (p.c.page_shift - 4);
@@ -549,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&s.v8_full[j & 1], (j >> 1) & 1, p.c.status);
       }
     }
-  } else if (warp == 13 && steps > 0) {
+   } else if (warp == 13 && steps > 0) {
     // ------------------------------------------------------------------- MMAs
     constexpr uint32_t iqk = idesc_f8(kTile, kTile), ipv = idesc_f16_nt(kTile, D);
     const uint32_t base = smem_u32(raw);
@@ -600,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
+   }
   }
 
   tc_fence_before();
