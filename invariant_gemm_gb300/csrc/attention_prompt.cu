@@ -34,7 +34,7 @@ constexpr float kBias = 8.0f;
 constexpr int kMinShift = -40;
 constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
 constexpr int kNoBlock = 2000;          // tokens that no row sees, or an absent page
-constexpr int kInfo = 4;                // steps whose scales are held
+constexpr int kInfo = 8;                // steps whose pages and scales are held
 
 template <int D>
 struct Smem {
@@ -47,9 +47,13 @@ struct Smem {
   uint64_t k_full[2], k_empty[2], v8_full[2], v8_empty[2], v16_full[2], v16_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t info_full[kInfo], info_empty[kInfo], drain;
-  float ks[kInfo][8];
+  // of a step's 8 blocks: scale of the keys; kBias + e - E and 2^(E - e) for p; e
+  alignas(16) float ks[kInfo][8], bias[kInfo][8], back[kInfo][8];
   int ve[kInfo][8];
+  int page[kInfo][8];
   int partly[kInfo];                    // some block of the step is not there
+  float less[kInfo];                    // 2^(E before - E) of the step
+  int top;                              // E in the end
   int nan_at[D];
   uint32_t tmem;
   int dead;
@@ -157,6 +161,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Row's factor times a block's scale; not 0, which times -inf were no number.
+__device__ __forceinline__ float factor(float f, float ks) {
+  const float k = f * ks;
+  return k < 1.18e-38f ? 1.18e-38f : k;
+}
 // Pairs of FP32 values: one instruction for both.
 __device__ __forceinline__ uint64_t pair2(float lo, float hi) {
   uint64_t r;
@@ -202,12 +211,22 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Bounded wait that also ends when any other wait of the block gave up.
+// Bounded wait that also ends when any other wait of the block gave up; a look
+// may sleep for 20 us.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(20000) : "memory");
+  return ok != 0;
+}
 template <typename S>
 __device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!try_wait_long(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&s.dead)) return false;
     if (clock64() - t0 > (1ll << 31)) {
       *reinterpret_cast<volatile int*>(&s.dead) = 1;
@@ -239,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&s.info_full[i], 1);
-      mbar_init(&s.info_empty[i], 12);
+      mbar_init(&s.info_empty[i], 13);
     }
     mbar_init(&s.drain, 1);
     s.dead = 0;
@@ -365,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * D + lanes;
     const int tile_low = kv - n + (row_first + t * kTile) / p.group;
     float m = neg_inf(), l = 0.0f;
-    int expo = -1000;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo;
@@ -382,32 +400,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32_async(ts + 32, v + 32);
       tmem_ld32_async(ts + 64, v + 64);
       tmem_ld32_async(ts + 96, v + 96);
-      int ve[8];
-      float k[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        ve[q] = s.ve[in][q];
-        k[q] = f * s.ks[in][q];         // not 0: times -inf it would be no number
-        if (k[q] < 1.18e-38f) k[q] = 1.18e-38f;
-      }
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) loaded32(v + 32 * c);
-      if (t0 + kTile - 1 > tile_low || s.partly[in]) {
+      if (t0 + kTile - 1 > tile_low) {
+        const int seen = lim - t0;
 #pragma unroll
         for (int i = 0; i < kTile; ++i)
-          if (t0 + i > lim || ve[i / 16] == kNoBlock) v[i] = neg_inf();
+          if (i > seen) v[i] = neg_inf();
+      }
+      if (s.partly[in]) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i)
+          if (s.ve[in][i / 16] == kNoBlock) v[i] = neg_inf();
       }
       float x = neg_inf();
-      int et = -1000;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         float y = max3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
 #pragma unroll
         for (int i = 3; i < 15; i += 2) y = max3(y, v[16 * q + i], v[16 * q + i + 1]);
         y = fmaxf(y, v[16 * q + 15]);
-        x = fmaxf(x, y * k[q]);
-        if (ve[q] < kNaNExp) et = max(et, ve[q]);
+        x = fmaxf(x, y * factor(f, s.ks[in][q]));
       }
       float down = 1.0f;
       if (x > m + kHeadroom) {
@@ -416,12 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = up;
       }
       l *= down;
-      if (et > expo) {
-        if (expo > -1000) down *= pow2(max(expo - et, -126));
-        expo = et;
-      }
+      down *= s.less[in];
       if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           float o[16];
           tmem_ld16(to + 16 * c, o);
@@ -437,10 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int e = ve[2 * c + q];
-          const int shift = e < kNaNExp ? max(e - expo, kMinShift) : 0;
-          const float off = (kBias + (float)shift) - base;
-          const uint64_t kk = pair2(k[2 * c + q], k[2 * c + q]), oo = pair2(off, off);
+          const float off = s.bias[in][2 * c + q] - base, k = factor(f, s.ks[in][2 * c + q]);
+          const uint64_t kk = pair2(k, k), oo = pair2(off, off);
           uint64_t sum = 0;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[8 * q + i / 2] = f16x2_of(a, d);
           }
           const float2 both = split2(sum);
-          l = fmaf(both.x + both.y, pow2(-shift), l);
+          l = fmaf(both.x + both.y, s.back[in][2 * c + q], l);
         }
         tmem_st16(ts + 16 * c, u);
       }
@@ -472,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = gr / p.group, head = h * p.group + gr % p.group;
       uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(row0 + tok) * p.ld_out +
                                             (int64_t)head * D);
+      const int expo = s.top;
       const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -519,37 +529,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = j * kTile + r, e = s.ve[in][r >> 4];
       const uint8_t* src = raw + S::kV8 + st * S::kPart + r * D;
       uint8_t* dst = raw + S::kV16 + st * 2 * S::kPart + r * 128;
+      uint32_t u[D / 4];
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        uint4 w = *reinterpret_cast<const uint4*>(
+        const uint4 w = *reinterpret_cast<const uint4*>(
             src + (D == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) * 16);
-        uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if (e == kNaNExp) u[0] = u[1] = u[2] = u[3] = 0x7f7f7f7fu;
+        u[4 * i] = w.x; u[4 * i + 1] = w.y; u[4 * i + 2] = w.z; u[4 * i + 3] = w.w;
+      }
+      if (at > low || e >= kNaNExp) {
         if (at > high || e == kNoBlock) {
-          u[0] = u[1] = u[2] = u[3] = 0;               // p is 0, but 0 times NaN is not
-        } else if (at > low) {
-          // seen by some rows: a NaN is kept for those
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bad = ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            if (bad) {
+          for (int i = 0; i < D / 4; ++i) u[i] = 0;    // p is 0, but 0 times NaN is not
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            if (e == kNaNExp) u[i] = 0x7f7f7f7fu;
+            // seen by some rows only: a NaN is kept for those
+            const uint32_t bad = ((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            if (at > low && bad) {
               for (int q = 0; q < 4; ++q)
-                if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[16 * i + 4 * k + q], at);
-              u[k] &= ~((bad >> 7) * 0xffu);
+                if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[4 * i + q], at);
+              u[i] &= ~((bad >> 7) * 0xffu);
             }
           }
         }
-        // values 16 i .. 16 i + 15: two chunks of 16 bytes of a row of 64 values
-        uint8_t* row = dst + (i >> 2) * (kTile * 128);
-        const int c = 2 * (i & 3);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t a = u[2 * k], d = u[2 * k + 1];
-          *reinterpret_cast<uint4*>(row + ((c + k) ^ (r & 7)) * 16) =
-              make_uint4(e4m3x2_to_f16x2((uint16_t)a), e4m3x2_to_f16x2((uint16_t)(a >> 16)),
-                         e4m3x2_to_f16x2((uint16_t)d), e4m3x2_to_f16x2((uint16_t)(d >> 16)));
-        }
       }
+      // values 16 i .. 16 i + 15: two chunks of 16 bytes of a row of 64 values
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * (kTile * 128) + ((i & 7) ^ (r & 7)) * 16) =
+            make_uint4(e4m3x2_to_f16x2((uint16_t)u[2 * i]),
+                       e4m3x2_to_f16x2((uint16_t)(u[2 * i] >> 16)),
+                       e4m3x2_to_f16x2((uint16_t)u[2 * i + 1]),
+                       e4m3x2_to_f16x2((uint16_t)(u[2 * i + 1] >> 16)));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -562,37 +574,16 @@ __global__ void __launch_bounds__(kThreads, 1)
    fewer_registers<64>();
    if (warp == 12) {
     // ----------------------------------------------------------------- copies
-    const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
-    const int blocks = 1 << (p.c.page_shift - 4);
     int asked = 0;
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
-      // lane l looks up block l of the step
-      const int tok = j * kTile + lane * kKvBlock;
-      bool there = lane < 8 && tok <= high;
-      int32_t page = 0;
-      uint32_t kb = 127, vb = 0;
-      const int row = tok & ((1 << p.c.page_shift) - 1);
-      if (there) {
-        page = __ldg(table + (tok >> p.c.page_shift));
-        there = page >= 0 && page < p.c.pages;
-        if (!there) atomicOr(p.c.status, kStatusIndexRange);
-      }
-      if (there) {
-        const uint8_t* sc = p.c.scales + page * p.c.scale_stride + h * blocks + row / kKvBlock;
-        kb = __ldg(sc);
-        vb = __ldg(sc + p.c.heads * blocks);
-      }
-      const uint32_t have = __ballot_sync(0xffffffffu, there);
-      bool ok = wait(s, &s.info_empty[in], ((j / kInfo) & 1) ^ 1, p.c.status);
+      bool ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane < 8) {
-        s.ks[in][lane] = e8m0_value(kb);
-        s.ve[in][lane] = !there ? kNoBlock : vb == 255 ? kNaNExp : (int)vb - 127;
-      }
-      if (lane == 0) s.partly[in] = have != 0xffu;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.info_full[in]);
+      const bool there = lane < 8 && s.ve[in][lane & 7] != kNoBlock;
+      const int32_t page = s.page[in][lane & 7];
+      const int row = (j * kTile + (lane & 7) * kKvBlock) & ((1 << p.c.page_shift) - 1);
+      const uint32_t have = __ballot_sync(0xffffffffu, there);
+      if (lane == 0) mbar_arrive(&s.info_empty[in]);
       ok = wait(s, &s.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t bytes = __popc(have) * (kKvBlock * D);
@@ -619,6 +610,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = max(asked - 2, 0); j < asked; ++j) {
         mbar_wait_bounded(&s.k_full[j & 1], (j >> 1) & 1, p.c.status);
         mbar_wait_bounded(&s.v8_full[j & 1], (j >> 1) & 1, p.c.status);
+      }
+    }
+   } else if (warp == 14) {
+    // ------------------------------------------------------- pages and scales
+    // a block to a lane, four steps at a time, ahead of the copies
+    const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
+    const int blocks = 1 << (p.c.page_shift - 4);
+    bool ok = true;
+    int expo = -1000;                   // E, the largest value scale so far
+    if (lane == 0) s.top = expo;
+    for (int j0 = 0; ok && j0 < steps; j0 += 4) {
+      const int tok = j0 * kTile + lane * kKvBlock;
+      bool there = tok <= high;
+      int32_t page = 0;
+      uint32_t kb = 127, vb = 0;
+      if (there) {
+        page = __ldg(table + (tok >> p.c.page_shift));
+        there = page >= 0 && page < p.c.pages;
+        if (!there) atomicOr(p.c.status, kStatusIndexRange);
+      }
+      if (there) {
+        const uint8_t* sc = p.c.scales + page * p.c.scale_stride + h * blocks +
+                            (tok & ((1 << p.c.page_shift) - 1)) / kKvBlock;
+        kb = __ldg(sc);
+        vb = __ldg(sc + p.c.heads * blocks);
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, there);
+      for (int i = 0; i < 4 && j0 + i < steps; ++i) {
+        const int in = (j0 + i) % kInfo;
+        ok = wait(s, &s.info_empty[in], (((j0 + i) / kInfo) & 1) ^ 1, p.c.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool mine = lane >> 3 == i, scaled = there && vb != 255;
+        const int e = (int)vb - 127;
+        const int to = max(expo, __reduce_max_sync(0xffffffffu, mine && scaled ? e : -1000));
+        if (mine) {
+          const int shift = scaled ? max(e - to, kMinShift) : 0;
+          s.ks[in][lane & 7] = e8m0_value(kb);
+          s.bias[in][lane & 7] = kBias + (float)shift;
+          s.back[in][lane & 7] = pow2(-shift);
+          s.ve[in][lane & 7] = !there ? kNoBlock : vb == 255 ? kNaNExp : e;
+          s.page[in][lane & 7] = page;
+        }
+        if (lane == 0) {
+          s.partly[in] = (have >> (8 * i) & 0xffu) != 0xffu;
+          s.less[in] = expo > -1000 ? pow2(max(expo - to, -126)) : 1.0f;
+          s.top = to;
+        }
+        expo = to;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.info_full[in]);
       }
     }
    } else if (warp == 13 && steps > 0) {
