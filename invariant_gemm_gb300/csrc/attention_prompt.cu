@@ -17,9 +17,9 @@
 // Softmax as in the split kernel: base 2, whole exponents, a row's maximum raised
 // only past m + 7, value scales folded into P, key scales into the logits.
 //
-// Warps: 0-3 and 4-7 the softmax of a tile each, a row to a thread; 8-11 the
-// values; 12 the copies; 13 the MMAs. The two tiles take turns: while one is in
-// the softmax the tensor cores work on the other.
+// Warps: 0-7 and 8-15 the softmax of a tile each, half a row to a thread; 16-19
+// the values; 20 the copies; 21 the MMAs; 22 the pages and scales. The two tiles
+// take turns: while one is in the softmax the tensor cores work on the other.
 #include "attention.cuh"
 #include "umma_mx4.cuh"
 
@@ -28,7 +28,8 @@ namespace ig {
 namespace {
 
 constexpr int kTile = 128;              // rows of a tile, tokens of a step
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
+constexpr int kHalf = kTile / 2;        // columns of a thread
 constexpr float kHeadroom = 7.0f;
 constexpr float kBias = 8.0f;
 constexpr int kMinShift = -40;
@@ -55,6 +56,7 @@ struct Smem {
   float less[kInfo];                    // 2^(E before - E) of the step
   int top;                              // E in the end
   int nan_at[D];
+  float most[2][2][2 * kTile];          // [step % 2][half][row]: largest logit, sum
   uint32_t tmem;
   int dead;
   int item[8];
@@ -187,7 +189,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// A warpgroup's share of the block's registers (512 threads launched with 128).
+// A warpgroup's share of the block's registers (768 threads launched with 80).
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -211,8 +213,9 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Bounded wait that also ends when any other wait of the block gave up; a look
-// may sleep for 20 us.
+// Bounded wait that also ends when any other wait of the block gave up; with
+// SLEEP a look may take 20 us, and the warp wakes up later than without (250
+// clocks against 90) but issues nothing meanwhile.
 __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -222,11 +225,13 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
       : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(20000) : "memory");
   return ok != 0;
 }
-template <typename S>
+template <bool SLEEP = false, typename S>
 __device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (try_wait_long(bar, parity)) return true;
+  auto look = [&] { return SLEEP ? try_wait_long(bar, parity) : mbar_try_wait(bar, parity); };
+  if (look()) return true;
   const long long t0 = clock64();
-  while (!try_wait_long(bar, parity)) {
+  while (!look()) {
+    __nanosleep(20);
     if (*reinterpret_cast<volatile int*>(&s.dead)) return false;
     if (clock64() - t0 > (1ll << 31)) {
       *reinterpret_cast<volatile int*>(&s.dead) = 1;
@@ -235,6 +240,16 @@ __device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint3
     }
   }
   return true;
+}
+
+// Barrier of a tile's eight warps; whether all came with true.
+__device__ __forceinline__ bool all_of(int bar, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, %2, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all) : "r"((uint32_t)mine), "r"(bar) : "memory");
+  return all != 0;
 }
 
 template <int D>
@@ -254,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.v16_full[i], 4);
       mbar_init(&s.v16_empty[i], 1);
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.p_full[i], 8);
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&s.info_full[i], 1);
-      mbar_init(&s.info_empty[i], 13);
+      mbar_init(&s.info_empty[i], 21);
     }
     mbar_init(&s.drain, 1);
     s.dead = 0;
@@ -319,35 +334,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int steps = high >= 0 ? high / kTile + 1 : 0;
   const uint32_t tmem = s.tmem;
 
-  // ---- queries: a row to a thread of the first two warpgroups
+  // ---- queries: half a row to a thread
+  const int half = (warp >> 2) & 1;
+  const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;      // of warps 0-15
   float f = 0.0f;                       // logit of a product, base 2
   int lim = 0x7fffffff;                 // last token that the row sees
-  if (warp < 8) {
-    const int r = tid, gr = row_first + r;
-    const bool in = r < rows;
+  uint4 w[D / 16];
+  if (warp < 16) {
+    const int gr = row_first + my_row;
+    const bool in = my_row < rows;
     const int tok = gr / p.group, head = h * p.group + gr % p.group;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(row0 + tok) * p.ld_q +
-                                                      (int64_t)head * D);
+                                                      (int64_t)head * D + half * (D / 2));
     if (in) lim = kv - n + tok;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
     uint32_t top = 0;
-    uint4 w[D / 8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
+    for (int i = 0; i < D / 16; ++i) {
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
     }
+    s.most[0][half][my_row] = __uint_as_float(top);
+  }
+  __syncthreads();
+  if (warp < 16) {
+    const uint32_t top = max(__float_as_uint(s.most[0][0][my_row]),
+                             __float_as_uint(s.most[0][1][my_row]));
     const int e = (int)(top >> 7);      // the largest value is below 2^(e - 126)
     float up = e == 255 ? qnan() : pow2(134 - max(e, 20));
     f = fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
     if (p.scale_log2 < 0.0f) up = -up;
+    const int r = my_row;
     uint8_t* hi = raw + S::kQ + (r >> 7) * 2 * S::kPart + (r & 127) * D;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {  // 16 values: 16 bytes of each part
+    for (int i = 0; i < D / 32; ++i) {  // 16 values: 16 bytes of each part
       uint32_t a[4], c[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -363,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         a[2 * j] = q.x; a[2 * j + 1] = q.y;
         c[2 * j] = t.x; c[2 * j + 1] = t.y;
       }
-      const int at = (D == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) * 16;
+      const int ch = half * (D / 32) + i;
+      const int at = (D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) * 16;
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(a[0], a[1], a[2], a[3]);
       *reinterpret_cast<uint4*>(hi + S::kPart + at) = make_uint4(c[0], c[1], c[2], c[3]);
     }
@@ -375,94 +398,120 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  // 256 threads with 192 registers and 256 with 64: the 65536 of the launch
-  if (warp < 4 * tiles) {
+  // 512 threads with 96 registers and 256 with 48: the 61440 of the launch
+  if (warp < 8 * tiles) {
     // ---------------------------------------------------------------- softmax
-    more_registers<192>();
-    const int t = warp >> 2;
+    more_registers<96>();
+    const int t = warp >> 3;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * D + lanes;
+    const uint32_t ts = tmem + t * kTile + lanes;
+    const uint32_t to = tmem + 2 * kTile + t * D + half * (D / 2) + lanes;
     const int tile_low = kv - n + (row_first + t * kTile) / p.group;
+    const int pair_bar = 1 + t * 4 + (warp & 3);        // the two warps of these rows
     float m = neg_inf(), l = 0.0f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo;
-      ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
-           wait(s, &s.s_full[t], j & 1, p.c.status);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
+      // what the scales have to say is here before the products are
+      const float4 ks = *reinterpret_cast<const float4*>(&s.ks[in][4 * half]);
+      const float4 bias = *reinterpret_cast<const float4*>(&s.bias[in][4 * half]);
+      const float4 back = *reinterpret_cast<const float4*>(&s.back[in][4 * half]);
+      const float k[4] = {factor(f, ks.x), factor(f, ks.y), factor(f, ks.z), factor(f, ks.w)};
+      const bool partly = s.partly[in];
+      float down = s.less[in];
+      // one warp of the tile looks for the products, the others wait for it: looks
+      // share a queue with the exponentials
+      if ((warp & 7) == 0) ok = ok && wait(s, &s.s_full[t], j & 1, p.c.status);
+      ok = all_of(9 + t, ok);
       if (!ok) break;
       tc_fence_after();
-      const int t0 = j * kTile;
-      // the row's products, all in registers; columns that it does not see are
-      // -inf: in few steps, so the others have no look at them
-      float v[kTile];
-      tmem_ld32_async(ts, v);
-      tmem_ld32_async(ts + 32, v + 32);
-      tmem_ld32_async(ts + 64, v + 64);
-      tmem_ld32_async(ts + 96, v + 96);
+      const int t0 = j * kTile + half * kHalf;
+      // half a row's products, all in registers; columns that the row does not
+      // see are -inf: in few steps, so the others have no look at them
+      float v[kHalf];
+      tmem_ld32_async(ts + half * kHalf, v);
+      tmem_ld32_async(ts + half * kHalf + 32, v + 32);
       tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) loaded32(v + 32 * c);
-      if (t0 + kTile - 1 > tile_low) {
+      loaded32(v);
+      loaded32(v + 32);
+      if (t0 + kHalf - 1 > tile_low || partly) {
         const int seen = lim - t0;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
+        for (int i = 0; i < kHalf; ++i)
           if (i > seen) v[i] = neg_inf();
-      }
-      if (s.partly[in]) {
+        if (partly) {
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          if (s.ve[in][i / 16] == kNoBlock) v[i] = neg_inf();
-      }
-      float x = neg_inf();
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float y = max3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
-#pragma unroll
-        for (int i = 3; i < 15; i += 2) y = max3(y, v[16 * q + i], v[16 * q + i + 1]);
-        y = fmaxf(y, v[16 * q + 15]);
-        x = fmaxf(x, y * factor(f, s.ks[in][q]));
-      }
-      float down = 1.0f;
-      if (x > m + kHeadroom) {
-        const float up = ceilf(x);
-        down = m == neg_inf() ? 0.0f : pow2_down(m - up);
-        m = up;
-      }
-      l *= down;
-      down *= s.less[in];
-      if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          float o[16];
-          tmem_ld16(to + 16 * c, o);
-          uint32_t u[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * down);
-          tmem_st16(to + 16 * c, u);
+          for (int i = 0; i < kHalf; ++i)
+            if (s.ve[in][4 * half + i / 16] == kNoBlock) v[i] = neg_inf();
         }
       }
-      const float base = m == neg_inf() ? 0.0f : m;
+      float y[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int q = 0; q < 4; ++q) y[q] = max3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
+#pragma unroll
+      for (int i = 3; i < 15; i += 2)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = max3(y[q], v[16 * q + i], v[16 * q + i + 1]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = fmaxf(y[q], v[16 * q + 15]) * k[q];
+      float x = fmaxf(max3(y[0], y[1], y[2]), y[3]);
+      // the other half's; both have their products in registers from here on, so
+      // P may take the place of S
+      s.most[j & 1][half][my_row] = x;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      x = fmaxf(x, s.most[j & 1][half ^ 1][my_row]);
+      if (x > m + kHeadroom) {
+        const float up = ceilf(x), d = m == neg_inf() ? 0.0f : pow2_down(m - up);
+        m = up;
+        l *= d;
+        down *= d;
+      }
+      const float base = m == neg_inf() ? 0.0f : m;
+      const float off[4] = {bias.x - base, bias.y - base, bias.z - base, bias.w - base};
+      float sums[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t u[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float off = s.bias[in][2 * c + q] - base, k = factor(f, s.ks[in][2 * c + q]);
-          const uint64_t kk = pair2(k, k), oo = pair2(off, off);
+          const int blk = 2 * c + q;
+          const uint64_t kk = pair2(k[blk], k[blk]), oo = pair2(off[blk], off[blk]);
           uint64_t sum = 0;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float* at = v + 32 * c + 16 * q + i;
-            const float2 y = split2(fma2(pair2(at[0], at[1]), kk, oo));
-            const float a = ex2(y.x), d = ex2(y.y);
+            const float* at = v + 16 * blk + i;
+            const float2 z = split2(fma2(pair2(at[0], at[1]), kk, oo));
+            const float a = ex2(z.x), d = ex2(z.y);
             sum = add2(sum, pair2(a, d));
             u[8 * q + i / 2] = f16x2_of(a, d);
           }
           const float2 both = split2(sum);
-          l = fmaf(both.x + both.y, s.back[in][2 * c + q], l);
+          sums[blk] = both.x + both.y;
         }
-        tmem_st16(ts + 16 * c, u);
+        tmem_st16(ts + 32 * half + 16 * c, u);
+      }
+      l = fmaf(sums[0], back.x, l);
+      l = fmaf(sums[1], back.y, l);
+      l = fmaf(sums[2], back.z, l);
+      l = fmaf(sums[3], back.w, l);
+      // the sums so far by the new maximum and exponent
+      if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
+        constexpr int N = D / 2 < 32 ? D / 2 : 32;
+#pragma unroll
+        for (int c = 0; c < D / 2; c += N) {
+          float o[32];
+          tmem_ld32_async(to + c, o);
+          tmem_wait_ld();
+          loaded32(o);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t u[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(o[16 * i + q] * down);
+            tmem_st16(to + c + 16 * i, u);
+          }
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -473,95 +522,105 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ---- the rows' results
-    if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(s, &s.s_full[t], steps & 1, p.c.status));
+    if (ok && steps > 0) {
+      if ((warp & 7) == 0) ok = wait(s, &s.s_full[t], steps & 1, p.c.status);
+      ok = all_of(9 + t, ok);
+    }
     tc_fence_after();
     if (ok) {
-      const int r = tid, gr = row_first + r;
-      const bool in = r < rows;
+      s.most[steps & 1][half][my_row] = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      // (first half) + (second half), for both the same
+      l = s.most[steps & 1][0][my_row] + s.most[steps & 1][1][my_row];
+      const int gr = row_first + my_row;
+      const bool in = my_row < rows;
       const int tok = gr / p.group, head = h * p.group + gr % p.group;
       uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(row0 + tok) * p.ld_out +
-                                            (int64_t)head * D);
+                                            (int64_t)head * D + half * (D / 2));
       const int expo = s.top;
       const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        float v[32];
+        float v[16];
         if (steps > 0) {
-          tmem_ld32(to + 32 * c, v);
+          tmem_ld16(to + 16 * c, v);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           v[i] = l == 0.0f ? 0.0f : v[i] * inv;
-          if (lim >= s.nan_at[32 * c + i]) v[i] = qnan();
+          if (lim >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
         }
         if (in) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[4 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
+          for (int i = 0; i < 2; ++i)
+            dst[2 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
                                         f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
                                         f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
                                         f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
+    more_registers<96>();
     // the second tile has no rows: only its share of the scales' barrier
-    more_registers<192>();
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo;
-      if (!wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
+      if (!wait<true>(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.info_empty[in]);
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ----------------------------------------------------------------- values
-    fewer_registers<64>();
-    const int r = tid - 256;            // token of the step
+    fewer_registers<48>();
+    const int r = tid - 512;            // token of the step
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
       bool ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
-                wait(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
-                wait(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+                wait<true>(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
+                wait<true>(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const int at = j * kTile + r, e = s.ve[in][r >> 4];
       const uint8_t* src = raw + S::kV8 + st * S::kPart + r * D;
       uint8_t* dst = raw + S::kV16 + st * 2 * S::kPart + r * 128;
-      uint32_t u[D / 4];
+#pragma unroll 1
+      for (int d = 0; d < D / 64; ++d) {          // 64 values at a time
+        uint32_t u[16];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(
-            src + (D == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) * 16);
-        u[4 * i] = w.x; u[4 * i + 1] = w.y; u[4 * i + 2] = w.z; u[4 * i + 3] = w.w;
-      }
-      if (at > low || e >= kNaNExp) {
-        if (at > high || e == kNoBlock) {
+        for (int i = 0; i < 4; ++i) {
+          const int ch = 4 * d + i;
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              src + (D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) * 16);
+          u[4 * i] = x.x; u[4 * i + 1] = x.y; u[4 * i + 2] = x.z; u[4 * i + 3] = x.w;
+        }
+        if (at > low || e >= kNaNExp) {
+          if (at > high || e == kNoBlock) {
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) u[i] = 0;    // p is 0, but 0 times NaN is not
-        } else {
+            for (int i = 0; i < 16; ++i) u[i] = 0;     // p is 0, but 0 times NaN is not
+          } else {
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) {
-            if (e == kNaNExp) u[i] = 0x7f7f7f7fu;
-            // seen by some rows only: a NaN is kept for those
-            const uint32_t bad = ((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            if (at > low && bad) {
-              for (int q = 0; q < 4; ++q)
-                if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[4 * i + q], at);
-              u[i] &= ~((bad >> 7) * 0xffu);
+            for (int i = 0; i < 16; ++i) {
+              if (e == kNaNExp) u[i] = 0x7f7f7f7fu;
+              // seen by some rows only: a NaN is kept for those
+              const uint32_t bad = ((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (at > low && bad) {
+                for (int q = 0; q < 4; ++q)
+                  if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[64 * d + 4 * i + q], at);
+                u[i] &= ~((bad >> 7) * 0xffu);
+              }
             }
           }
         }
-      }
-      // values 16 i .. 16 i + 15: two chunks of 16 bytes of a row of 64 values
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * (kTile * 128) + ((i & 7) ^ (r & 7)) * 16) =
-            make_uint4(e4m3x2_to_f16x2((uint16_t)u[2 * i]),
-                       e4m3x2_to_f16x2((uint16_t)(u[2 * i] >> 16)),
-                       e4m3x2_to_f16x2((uint16_t)u[2 * i + 1]),
-                       e4m3x2_to_f16x2((uint16_t)(u[2 * i + 1] >> 16)));
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(dst + d * (kTile * 128) + (i ^ (r & 7)) * 16) =
+              make_uint4(e4m3x2_to_f16x2((uint16_t)u[2 * i]),
+                         e4m3x2_to_f16x2((uint16_t)(u[2 * i] >> 16)),
+                         e4m3x2_to_f16x2((uint16_t)u[2 * i + 1]),
+                         e4m3x2_to_f16x2((uint16_t)(u[2 * i + 1] >> 16)));
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -571,20 +630,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-   fewer_registers<64>();
-   if (warp == 12) {
+   fewer_registers<48>();
+   if (warp == 20) {
     // ----------------------------------------------------------------- copies
     int asked = 0;
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
-      bool ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
+      bool ok = wait<true>(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const bool there = lane < 8 && s.ve[in][lane & 7] != kNoBlock;
       const int32_t page = s.page[in][lane & 7];
       const int row = (j * kTile + (lane & 7) * kKvBlock) & ((1 << p.c.page_shift) - 1);
       const uint32_t have = __ballot_sync(0xffffffffu, there);
       if (lane == 0) mbar_arrive(&s.info_empty[in]);
-      ok = wait(s, &s.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+      ok = wait<true>(s, &s.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t bytes = __popc(have) * (kKvBlock * D);
       if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], bytes);
@@ -592,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (there)
         tma_load_3d(raw + S::kK + st * S::kPart + lane * (kKvBlock * D), &p.tm, 0,
                     (h << p.c.page_shift) + row, page, &s.k_full[st]);
-      ok = wait(s, &s.v8_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
+      ok = wait<true>(s, &s.v8_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) {
         // the keys' copy of this step is in flight, the values' is not
         mbar_wait_bounded(&s.k_full[st], (j >> 1) & 1, p.c.status);
@@ -612,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&s.v8_full[j & 1], (j >> 1) & 1, p.c.status);
       }
     }
-   } else if (warp == 14) {
+   } else if (warp == 22) {
     // ------------------------------------------------------- pages and scales
     // a block to a lane, four steps at a time, ahead of the copies
     const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
@@ -639,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t have = __ballot_sync(0xffffffffu, there);
       for (int i = 0; i < 4 && j0 + i < steps; ++i) {
         const int in = (j0 + i) % kInfo;
-        ok = wait(s, &s.info_empty[in], (((j0 + i) / kInfo) & 1) ^ 1, p.c.status);
+        ok = wait<true>(s, &s.info_empty[in], (((j0 + i) / kInfo) & 1) ^ 1, p.c.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const bool mine = lane >> 3 == i, scaled = there && vb != 255;
@@ -663,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&s.info_full[in]);
       }
     }
-   } else if (warp == 13 && steps > 0) {
+   } else if (warp == 21 && steps > 0) {
     // ------------------------------------------------------------------- MMAs
     constexpr uint32_t iqk = idesc_f8(kTile, kTile), ipv = idesc_f16_nt(kTile, D);
     const uint32_t base = smem_u32(raw);
@@ -719,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (s.dead && warp == 13) {
+  if (s.dead && warp == 21) {
     // MMAs still at work end before the tensor memory is given back
     tc_fence_after();
     if (elect_one()) umma_commit(&s.drain);
