@@ -62,16 +62,24 @@ struct AttnParams {
   KvParams c;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
-  uint32_t* counters;
-  float* parts;         // partial results [item][rows][D]
-  float* part_ml;       // [item][rows][kPartWords]
+  float* parts;         // results of parts [sequence][tile][kv head][part][row][D]
+  float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
   int64_t ld_q, ld_out;
   int32_t heads_q, group;   // query heads, and of one kv head
   int32_t few_rows;     // sequences with at most this many rows a kv head are the split kernel's
   int32_t max_tiles;    // 16-row tiles of such a sequence
-  int32_t part_rows;
+  int32_t max_parts, part_rows;
   int32_t flags;
   float scale_log2;     // scale * log2(e)
+};
+
+struct AttnJoinParams {
+  KvParams c;
+  __nv_bfloat16* out;
+  const float* parts;
+  const float* part_ml;
+  int64_t ld_out;
+  int32_t group, few_rows, tokens, max_tiles, max_parts, part_rows;
 };
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t st);
@@ -91,13 +99,12 @@ constexpr int kFewRows = 64;
 
 // --- splitting a sequence ---------------------------------------------------
 // A sequence's tokens are cut into parts of a length that kv_len alone fixes
-// (so that a row's bits do not depend on the batch): whole 512s, at most 32 of
-// them.
-constexpr int kSplitTokens = 512;
+// (so that a row's bits do not depend on the batch): 256 up to 4096 tokens, then
+// whole 512s, at most 32 of them.
 constexpr int kMaxSplits = 32;
 constexpr int kPartWords = 4;           // of a row of a part: maximum, sum, exponent, unused
 __host__ __device__ inline int split_tokens(int kv) {
-  return kSplitTokens * ((kv + kSplitTokens * kMaxSplits - 1) / (kSplitTokens * kMaxSplits));
+  return kv <= 4096 ? 256 : 512 * ((kv + 512 * kMaxSplits - 1) / (512 * kMaxSplits));
 }
 
 #ifdef __CUDACC__

@@ -137,10 +137,10 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
   return IG_OK;
 }
 
-// What the workspace of an attention call holds behind the status word and the
-// counters.
+// What the workspace of an attention call holds behind the status word and (not
+// used here) the counters.
 struct AttnPlan {
-  int group, max_tiles, part_rows;
+  int group, max_tiles, max_parts, part_rows;
   size_t ml_at, total;
 };
 
@@ -161,12 +161,10 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
   const int64_t rows = (int64_t)pl->group * b->max_q;
   if (rows > (1 << 28)) return IG_ERR_UNSUPPORTED;
   pl->max_tiles = (int)(((rows < kFewRows ? rows : kFewRows) + 15) / 16);
-  if ((int64_t)b->batch * pl->max_tiles * c->heads > kMaxCounters) return IG_ERR_UNSUPPORTED;
   pl->part_rows = (int)(rows < 16 ? rows : 16);
   const int64_t cap = b->ld_table * c->page;
-  int64_t parts = (cap + kSplitTokens - 1) / kSplitTokens;
-  if (parts > kMaxSplits) parts = kMaxSplits;
-  const int64_t items = (int64_t)b->batch * pl->max_tiles * c->heads * parts;
+  pl->max_parts = cap < 256 * kMaxSplits ? (int)((cap + 255) / 256) : kMaxSplits;
+  const int64_t items = (int64_t)b->batch * pl->max_tiles * c->heads * pl->max_parts;
   if (items > (1ll << 30)) return IG_ERR_UNSUPPORTED;
   pl->ml_at = align_up((size_t)items * pl->part_rows * c->head_dim * 4, 256);
   pl->total = kMapOffset + pl->ml_at + (size_t)items * pl->part_rows * kPartWords * 4;
@@ -288,7 +286,6 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.c = kv_params(cache, batch, shape->T, ws);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kCountersOffset);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.ml_at);
   p.ld_q = shape->ld_q;
@@ -297,6 +294,7 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.group = pl.group;
   p.few_rows = kFewRows;
   p.max_tiles = pl.max_tiles;
+  p.max_parts = pl.max_parts;
   p.part_rows = pl.part_rows;
   p.flags = shape->flags;
   p.scale_log2 = shape->scale * 1.4426950408889634f;

@@ -2,16 +2,25 @@
 // tokens, the ends of chunks.
 //
 // Rows are a kv head's: `group` query heads for each new token, 16 rows to a
-// tile (the M of mma.sync.m16n8k16). A work item is one tile, one kv head and
-// one part of the sequence's tokens (split_tokens); its four warps take the
-// part's steps of 16 tokens, one block of the cache each, in turn. Each warp
-// has a ring of its own: one TMA box for a step's keys and one for its values.
-// Items are dealt to blocks that stay; a warp asks for the next item's steps
-// while it computes this one's.
+// tile. A work item is one tile, one kv head and one part of the sequence's
+// tokens (split_tokens). Items are dealt to blocks that stay, three to an SM
+// where a tile has 8 rows at most, else two. In a block four warps compute, one
+// copies ahead and one joins:
+//   copies   pages and scales of the part, a step of 16 tokens (a block of the
+//            cache) to a lane, asked for while the part before is on its way;
+//            then one TMA box for a step's keys and one for its values, four
+//            steps to a stage of the ring; the item's queries
+//   compute  a step of each stage to a warp
+//   join     the four warps' sums, in their order, into the output or, where the
+//            rows see several parts, into the workspace
+// A second kernel joins the parts, in their order.
 //
-// FP16 tensor-core products: a code is exact in FP16, a query row too once it is
-// scaled by a power of two to a maximum below 2^15. Scales, being powers of two,
-// are applied outside the products: the keys' to the logits, the values' to p.
+// FP16 tensor-core products with the tokens as rows (M) and the query rows as
+// columns (N, 8 at a time): S^T = K Q^T and O^T = V^T P^T, so that 8 rows a kv
+// head leave no part of an MMA unused. A code is exact in FP16, a query row too
+// once it is scaled by a power of two to a maximum below 2^15. Scales, being
+// powers of two, are applied outside the products: the keys' to the logits, the
+// values' to p.
 //
 // Online softmax in base 2 with whole exponents: a row's m is raised only when a
 // logit passes m + 7, to the next whole number, so that every rescaling is by
@@ -19,10 +28,10 @@
 // the largest exponent of the value scales so far and e this step's, stays below
 // 2^15; as FP16 it has 11 bits down to 2^-14. The sum of p is FP32.
 //
-// The K order of both products is free, so the fragments are what lies together:
-// a lane's keys are 32 consecutive bytes of one token, its values 16 consecutive
-// bytes of four tokens; the box's swizzle makes both 128-bit loads free of bank
-// conflicts.
+// The K order of both products is free, and so is the M order of the second, so
+// the fragments are what lies together: a lane's keys are 32 consecutive bytes of
+// two tokens, its values 16 consecutive bytes of four tokens; the box's swizzle
+// makes both 128-bit loads free of bank conflicts.
 #include "attention.cuh"
 #include "warp_mma.cuh"
 
@@ -30,28 +39,45 @@ namespace ig {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kStages = 4;              // steps of a warp in flight
+constexpr int kTeam = 4;                // warps that compute
+constexpr int kThreads = 32 * (kTeam + 2);
 constexpr int kStep = kKvBlock;
-constexpr int kRows = 16;
+constexpr int kRows = 16;               // of a tile
+constexpr int kUnit = 32;               // steps looked up at a time
 constexpr float kHeadroom = 7.0f;       // a row's m is raised past m + this
 constexpr float kBias = 8.0f;           // p is 2^kBias at m
 constexpr int kMinShift = -40;          // value scales below 2^-40 of the largest: as 2^-40
-constexpr uint32_t kAbsent = 1u << 16;  // slot word: the step's page does not exist
+constexpr uint32_t kAbsent = 1u << 16;  // step's word: its page does not exist
+constexpr int kSeqs = 128;              // sequences that a block keeps beside their items
 
-template <int D>
+// A tile of a sequence, one kv head, one part.
+struct Item {
+  int b, h, tile, split, tiles, ns;
+  int row0, n, kv, rows;       // rows of the tile
+  int t0, t1;                  // tokens of the part that the tile's rows see: t0 .. t1 - 1
+  int low, high;               // last token that its first and its last row see
+  int parts;                   // parts that its rows see
+  int id;                      // -1: no more items
+};
+
+template <int D, int NT>
 struct Smem {
+  static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr int kBox = kStep * D;              // bytes of a step's keys (or values)
-  static constexpr int kRing = kWarps * kStages * 2 * kBox;
+  static constexpr int kStage = 2 * kTeam * kBox;     // keys of four steps, then values
+  static constexpr int kRing = kStages * kStage;
   static constexpr int kPitch = D + 4;                // floats of a row of sums
-  float o[kWarps][kRows][kPitch];
-  float ml[kWarps][kRows][2];
-  int expo[kWarps];
+  float o[kTeam][8 * NT][kPitch];
+  alignas(16) __nv_bfloat16 q[2][8 * NT][D];
+  float ml[kTeam][8 * NT][2];
+  int expo[kTeam];
   int nan_at[2][D];
-  uint64_t full[kWarps][kStages];
-  uint32_t slot[kWarps][kStages];
-  int scan[kWarps];
-  int last;
+  Item item[2];
+  uint64_t full[kStages], empty[kStages], item_full[2], item_empty[2], sums_full, sums_empty;
+  uint32_t info[kStages][kTeam];
+  int3 seq[kSeqs];                      // row0, n, kv of the first sequences
+  int scan[kTeam + 2];
+  int dead;
 };
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
@@ -80,43 +106,72 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t lo_f16(uint32_t v) { return e4m3x2_to_f16x2((uint16_t)v); }
-__device__ __forceinline__ uint32_t hi_f16(uint32_t v) {
-  return e4m3x2_to_f16x2((uint16_t)(v >> 16));
+// Four codes -> FP16 values of the low two and of the high two.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(v));
+}
+// 8 x 8 values of 16 bits over the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // 0x80 in each byte of w that is a NaN code
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
-
-// A tile of a sequence, one kv head, one part.
-struct Item {
-  int b, h, tile, split, tiles, ns;
-  int row0, n, kv, rows;       // rows of the tile
-  int t0, t1;                  // tokens of the part that the tile's rows see: t0 .. t1 - 1
-  int low, high;               // last token that its first and its last row see
-  int parts;                   // parts that its rows see
-  int first;                   // number of the sequence's first item
-};
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Bounded wait of a warp that also ends when any other wait of the block gave up.
+template <typename S>
+__device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint32_t* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      if (*reinterpret_cast<volatile int*>(&s.dead)) break;
+      if (clock64() - t0 > (1ll << 31)) {
+        *reinterpret_cast<volatile int*>(&s.dead) = 1;
+        atomicOr(status, kStatusTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
 
 __device__ __forceinline__ int seq_splits(int kv, int len) { return kv > 0 ? (kv + len - 1) / len : 1; }
-__device__ __forceinline__ int part_len(int kv) { return max(split_tokens(kv), kSplitTokens); }
+
+// Parts with tokens that a tile sees whose last row sees token `high`.
+__device__ __forceinline__ int tile_parts(int high, int len) {
+  return high < 0 ? 1 : high / len + 1;
+}
 
 // prefix[b]: items of the sequences before b.
-__device__ __forceinline__ Item item_of(const AttnParams& p, const int* prefix, int item) {
+__device__ __forceinline__ Item item_of(const AttnParams& p, const int* prefix, const int3* seq,
+                                        int item) {
   int lo = 0, hi = p.c.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (prefix[mid] <= item) lo = mid; else hi = mid;
   }
   Item it;
+  it.id = item;
   it.b = lo;
-  it.first = prefix[lo];
-  sequence_of(p.c, lo, it.row0, it.n, it.kv);
-  const int rows = it.n * p.group, len = part_len(it.kv);
+  if (lo < kSeqs) {
+    it.row0 = seq[lo].x;
+    it.n = seq[lo].y;
+    it.kv = seq[lo].z;
+  } else {
+    sequence_of(p.c, lo, it.row0, it.n, it.kv);
+  }
+  const int rows = it.n * p.group, len = split_tokens(it.kv);
   it.tiles = (rows + kRows - 1) / kRows;
   it.ns = seq_splits(it.kv, len);
-  uint32_t v = (uint32_t)(item - it.first);
+  uint32_t v = (uint32_t)(item - prefix[lo]);
   it.tile = (int)next_digit(v, it.tiles);
   it.split = (int)next_digit(v, it.ns);
   it.h = (int)v;
@@ -125,124 +180,612 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, const int* prefix, 
   it.low = it.kv - it.n + r / p.group;
   it.high = it.kv - it.n + (r + it.rows - 1) / p.group;
   const int end = max(it.high + 1, 0);
-  it.parts = max(1, (end + len - 1) / len);
+  it.parts = tile_parts(it.high, len);
   it.t0 = it.split * len;
   it.t1 = max(it.t0, min(end, it.t0 + len));
   return it;
 }
-__device__ __forceinline__ int warp_steps(const Item& it, int warp) {
-  const int steps = (it.t1 - it.t0 + kStep - 1) / kStep;
-  return (steps - warp + kWarps - 1) / kWarps;         // steps warp, warp + 4, ...
-}
 
-// Copies of one warp's steps, item after item.
-template <int D>
-struct Feed {
-  const AttnParams& p;
-  const int* prefix;
-  uint8_t* ring;               // of the warp
-  uint64_t* full;
-  uint32_t* slot;
-  int warp, lane, total, item, steps, i, batch_at, t0, h;
-  int32_t page;                // of the batch's step `lane`
+// The copying warp's look at 32 steps of an item, a step to a lane.
+struct Unit {
+  Item it;
+  int step;                    // first of the unit's steps
+  int32_t page;
   uint32_t info;
-  uint32_t made;               // stages asked for so far
-  const int32_t* table;
-  bool done;
-
-  __device__ __forceinline__ void open() {
-    // the next item of this block with steps of this warp
-    while (item < total) {
-      const Item it = item_of(p, prefix, item);
-      steps = it.split < it.parts ? warp_steps(it, warp) : 0;
-      if (steps > 0) {
-        t0 = it.t0;
-        h = it.h;
-        table = p.c.table + (int64_t)it.b * p.c.ld_table;
-        i = 0;
-        batch_at = -32;
-        return;
-      }
-      item += gridDim.x;
-    }
-    done = true;
-  }
-  // Pages and scales of 32 steps, one to a lane.
-  __device__ __forceinline__ void look() {
-    batch_at = i;
-    info = kAbsent;
-    page = 0;
-    if (i + lane < steps) {
-      const int tok = t0 + (warp + kWarps * (i + lane)) * kStep;
-      page = __ldg(table + (tok >> p.c.page_shift));
-      if (page >= 0 && page < p.c.pages) {
-        const int blocks = 1 << (p.c.page_shift - 4);
-        const uint8_t* s = p.c.scales + page * p.c.scale_stride + h * blocks +
-                           ((tok & ((1 << p.c.page_shift) - 1)) / kKvBlock);
-        info = __ldg(s) | (uint32_t)__ldg(s + p.c.heads * blocks) << 8;
-      } else {
-        atomicOr(p.c.status, kStatusIndexRange);
-      }
-    }
-  }
-  // Asks for one more step. Call with done == false.
-  __device__ __forceinline__ void push() {
-    if (i >= batch_at + 32) look();
-    const int32_t pg = __shfl_sync(0xffffffffu, page, i - batch_at);
-    const uint32_t in = __shfl_sync(0xffffffffu, info, i - batch_at);
-    const uint32_t st = made % kStages;
-    if (lane == 0) {
-      slot[st] = in;
-      if (in & kAbsent) {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(full + st))
-                     : "memory");
-      } else {
-        const int tok = t0 + (warp + kWarps * i) * kStep;
-        const int row = tok & ((1 << p.c.page_shift) - 1);
-        uint8_t* at = ring + st * 2 * Smem<D>::kBox;
-        mbar_arrive_expect_tx(full + st, 2 * Smem<D>::kBox);
-        tma_load_3d(at, &p.tm, 0, (h << p.c.page_shift) + row, pg, full + st);
-        tma_load_3d(at + Smem<D>::kBox, &p.tm, 0, ((p.c.heads + h) << p.c.page_shift) + row, pg,
-                    full + st);
-      }
-    }
-    ++made;
-    if (++i == steps) {
-      item += gridDim.x;
-      open();
-    }
-  }
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps, 2) split_kernel(const __grid_constant__ AttnParams p) {
-  using S = Smem<D>;
+// The unit after u: of the same item, else of the block's next item that has a
+// part its rows see (id -1: none). Pages only.
+__device__ __forceinline__ void next_unit(const AttnParams& p, const int* prefix, const int3* seq,
+                                          int total, int lane, Unit& u) {
+  u.step += kUnit;
+  if (u.it.id < 0 || u.it.t0 + u.step * kStep >= u.it.t1) {
+    int id = u.it.id < 0 ? (int)blockIdx.x : u.it.id + (int)gridDim.x;
+    u.step = 0;
+    while (true) {
+      if (id >= total) {
+        u.it.id = -1;
+        return;
+      }
+      u.it = item_of(p, prefix, seq, id);
+      if (u.it.split < u.it.parts) break;
+      id += gridDim.x;
+    }
+  }
+  u.info = kAbsent;
+  u.page = 0;
+  const int tok = u.it.t0 + (u.step + lane) * kStep;
+  if (tok < u.it.t1)
+    u.page = __ldg(p.c.table + (int64_t)u.it.b * p.c.ld_table + (tok >> p.c.page_shift));
+}
+// Its scales.
+__device__ __forceinline__ void unit_scales(const AttnParams& p, int lane, Unit& u) {
+  const int tok = u.it.t0 + (u.step + lane) * kStep;
+  if (u.it.id < 0 || tok >= u.it.t1) return;
+  if (u.page >= 0 && u.page < p.c.pages) {
+    const int blocks = 1 << (p.c.page_shift - 4);
+    const uint8_t* s = p.c.scales + u.page * p.c.scale_stride + u.it.h * blocks +
+                       ((tok & ((1 << p.c.page_shift) - 1)) / kKvBlock);
+    u.info = __ldg(s) | (uint32_t)__ldg(s + p.c.heads * blocks) << 8;
+  } else {
+    atomicOr(p.c.status, kStatusIndexRange);
+  }
+}
+
+template <int D, int NT>
+__device__ void copy_warp(const AttnParams& p, Smem<D, NT>& s, uint8_t* ring, const int* prefix,
+                          int total, int lane) {
+  using S = Smem<D, NT>;
+  Unit u;
+  u.it.id = -1;
+  u.step = 0;
+  next_unit(p, prefix, s.seq, total, lane, u);
+  unit_scales(p, lane, u);
+  uint32_t items = 0, made = 0;
+  bool ok = true;
+  while (ok) {
+    if (u.step == 0) {
+      // the item and its queries: the heads of one kv head lie together
+      const int buf = items & 1;
+      ok = wait(s, &s.item_empty[buf], ((items >> 1) & 1) ^ 1, p.c.status);
+      if (!ok) break;
+      ++items;
+      if (lane == 0) {
+        s.item[buf] = u.it;
+        const uint32_t bytes = u.it.id < 0 ? 0 : u.it.rows * D * 2;
+        mbar_arrive_expect_tx(&s.item_full[buf], bytes);
+      }
+      __syncwarp();
+      if (u.it.id < 0) break;
+      const int r = u.it.tile * kRows, last = r + u.it.rows;      // rows of the sequence
+      const int tok = r / p.group + lane;
+      const int from = max(r, tok * p.group), to = min(last, (tok + 1) * p.group);
+      if (from < to)
+        bulk_g2s(&s.q[buf][from - r][0],
+                 p.q + (int64_t)(u.it.row0 + tok) * p.ld_q +
+                     (int64_t)(u.it.h * p.group + from - tok * p.group) * D,
+                 (uint32_t)(to - from) * D * 2, &s.item_full[buf]);
+    }
+    const Unit now = u;
+    const int steps = min(kUnit, (now.it.t1 - now.it.t0 + kStep - 1) / kStep - now.step);
+    const int row0 = now.it.t0 + now.step * kStep;
+    for (int i = 0; i < steps || i == 0; i += kTeam) {
+      if (steps > 0) {
+        const uint32_t st = made % S::kStages;
+        ok = wait(s, &s.empty[st], ((made / S::kStages) & 1) ^ 1, p.c.status);
+        if (!ok) break;
+        ++made;
+        // lane l < 4: keys and values of step i + l; the scales may still be on
+        // their way
+        const int32_t page = __shfl_sync(0xffffffffu, now.page, (i + lane) & 31);
+        const bool there = lane < kTeam && i + lane < steps && page >= 0 && page < p.c.pages;
+        const uint32_t have = __popc(__ballot_sync(0xffffffffu, there));
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[st], have * 2 * S::kBox);
+        __syncwarp();
+        if (there) {
+          const int row = (row0 + (i + lane) * kStep) & ((1 << p.c.page_shift) - 1);
+          uint8_t* at = ring + st * S::kStage + lane * S::kBox;
+          tma_load_3d(at, &p.tm, 0, (now.it.h << p.c.page_shift) + row, page, &s.full[st]);
+          tma_load_3d(at + kTeam * S::kBox, &p.tm, 0,
+                      ((p.c.heads + now.it.h) << p.c.page_shift) + row, page, &s.full[st]);
+        }
+        const uint32_t info = __shfl_sync(0xffffffffu, now.info, (i + lane) & 31);
+        if (lane < kTeam) s.info[st][lane] = there ? info : kAbsent;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[st]);
+        __syncwarp();
+      }
+      // the next unit's pages, and once they are here its scales
+      if (i == 0) next_unit(p, prefix, s.seq, total, lane, u);
+      if (i == 4 * kTeam) unit_scales(p, lane, u);
+    }
+    if (steps <= 4 * kTeam) unit_scales(p, lane, u);
+  }
+  if (*reinterpret_cast<volatile int*>(&s.dead)) {
+    // copies still in flight land before the block leaves
+    for (uint32_t m = made > S::kStages ? made - S::kStages : 0; m < made; ++m)
+      mbar_wait_bounded(&s.full[m % S::kStages], (m / S::kStages) & 1, p.c.status);
+    for (uint32_t m = items > 2 ? items - 2 : 0; m < items; ++m)
+      mbar_wait_bounded(&s.item_full[m & 1], (m >> 1) & 1, p.c.status);
+  }
+}
+
+template <int D, int NT>
+__device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t* ring, int warp,
+                             int lane) {
+  using S = Smem<D, NT>;
   constexpr int KS = D / 16;            // steps of 16 along D
-  constexpr int NT = D / 8;             // 8-column tiles of the output
+  constexpr int MT = D / 16;            // 16-row tiles of O^T
   constexpr int VW = D / 32;            // words of a token's values in a lane
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t taken = 0;
+  for (uint32_t turn = 0;; ++turn) {
+    const int buf = turn & 1;
+    if (!wait(s, &s.item_full[buf], (turn >> 1) & 1, p.c.status)) return;
+    const Item& it = s.item[buf];
+    if (it.id < 0) return;
+    const int rows = it.rows, low = it.low, high = it.high, t0 = it.t0;
+    const int steps = (it.t1 - t0 + kStep - 1) / kStep;
+
+    // --- queries: row 8 nt + g as FP16 with a power of two apart
+    uint32_t qb[NT][KS][2];
+    float f[NT][2];                     // logit of a product, rows 2c and 2c + 1
+    int lim[NT][2];                     // last token that they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      uint32_t w[D / 8];                // D / 4 values, two to a word
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint4 v = *(reinterpret_cast<const uint4*>(&s.q[buf][r][c * (D / 4)]) + i);
+        if (r >= rows) v = make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = (int)(top >> 7);    // the largest value is below 2^(e - 126)
+      const float up = e == 255 ? qnan() : pow2(141 - max(e, 20));
+      const float mine = p.scale_log2 * (e == 255 ? 1.0f : pow2(max(e, 20) - 141));
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qb[nt][k][0] = f16x2_of(bf16lo(w[2 * k]) * up, bf16hi(w[2 * k]) * up);
+        qb[nt][k][1] = f16x2_of(bf16lo(w[2 * k + 1]) * up, bf16hi(w[2 * k + 1]) * up);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * nt + 2 * c + i;
+        f[nt][i] = __shfl_sync(0xffffffffu, mine, (2 * c + i) * 4);
+        lim[nt][i] = row < rows ? it.kv - it.n + (it.tile * kRows + row) / p.group : 0x7fffffff;
+      }
+    }
+
+    float o[MT][NT][4];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[j][nt][k] = 0.0f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[nt][i] = neg_inf();
+        l[nt][i] = 0.0f;
+      }
+    int expo = -1000;                   // E; none yet
+
+    for (int i = 0; i < steps; i += kTeam) {
+      const uint32_t st = taken % S::kStages;
+      if (!wait(s, &s.full[st], (taken / S::kStages) & 1, p.c.status)) return;
+      ++taken;
+      const uint32_t info = s.info[st][warp];
+      const int tok = t0 + (i + warp) * kStep;
+      const uint8_t* kb = ring + st * S::kStage + warp * S::kBox;
+      const uint8_t* vb = kb + kTeam * S::kBox;
+      if (info & kAbsent) {             // past the part's end, or no such page
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[st]);
+        continue;
+      }
+      uint32_t kw[2][D / 16];           // D / 4 bytes of tokens g and g + 8
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int r = 8 * t + g;
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(kb + r * D + (((2 * c + q) ^ (r & 7)) << 4));
+            kw[t][4 * q] = v.x; kw[t][4 * q + 1] = v.y;
+            kw[t][4 * q + 2] = v.z; kw[t][4 * q + 3] = v.w;
+          }
+        } else {
+          const uint4 v =
+              *reinterpret_cast<const uint4*>(kb + r * D + ((c ^ ((r >> 1) & 3)) << 4));
+          kw[t][0] = v.x; kw[t][1] = v.y; kw[t][2] = v.z; kw[t][3] = v.w;
+        }
+      }
+      uint32_t vw[4][VW];               // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int r = 2 * c + (t & 1) + 8 * (t >> 1);
+        if constexpr (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(vb + r * D + ((g ^ (r & 7)) << 4));
+          vw[t][0] = v.x; vw[t][1] = v.y; vw[t][2] = v.z; vw[t][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(
+              vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + ((g & 1) << 3));
+          vw[t][0] = v.x; vw[t][1] = v.y;
+        }
+      }
+      // tokens g (0, 1) and g + 8, rows 2c and 2c + 1; even and odd steps of K
+      // apart: half as long a chain of MMAs
+      float sc[NT][4], sd[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[nt][k] = sd[nt][k] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        e4m3x4_to_f16(kw[0][k], a[0], a[2]);
+        e4m3x4_to_f16(kw[1][k], a[1], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(k & 1 ? sd[nt] : sc[nt], a, qb[nt][k][0], qb[nt][k][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[nt][k] += sd[nt][k];
+      __syncwarp();                     // the stage has been read
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+
+      // logits in base 2, masks
+      const float ks = e8m0_value(info & 0xffu);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float a0 = f[nt][0] * ks, a1 = f[nt][1] * ks;
+        sc[nt][0] *= a0; sc[nt][1] *= a1;
+        sc[nt][2] *= a0; sc[nt][3] *= a1;
+      }
+      const uint32_t vbyte = (info >> 8) & 0xffu;
+      if (vbyte == 255) {               // the block's values are NaN
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vw[t][w] = 0x7f7f7f7fu;
+      }
+      if (tok + kStep - 1 > low) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (tok + g + 8 * (k >> 1) > lim[nt][k & 1]) sc[nt][k] = neg_inf();
+        // p is 0 there, but 0 times NaN is not: tokens that no row sees have
+        // any bytes; a NaN of a token that some rows see is kept for those
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int at = tok + 2 * c + (t & 1) + 8 * (t >> 1);
+          if (at > high) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[t][w] = 0;
+          } else if (at > low) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              const uint32_t bad = nan_bytes(vw[t][w]);
+              if (bad) {
+                for (int q = 0; q < 4; ++q)
+                  if (bad >> (8 * q + 7) & 1)
+                    atomicMin(&s.nan_at[buf][g * (D / 8) + 4 * w + q], at);
+                vw[t][w] &= ~((bad >> 7) * 0xffu);
+              }
+            }
+          }
+        }
+      }
+
+      // maxima: raised where a logit passes m + 7
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          raise |= fmaxf(sc[nt][r], sc[nt][2 + r]) > m[nt][r] + kHeadroom;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float x = fmaxf(sc[nt][r], sc[nt][2 + r]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            float d = 1.0f;
+            if (x > m[nt][r] + kHeadroom) {
+              const float to = ceilf(x);
+              d = m[nt][r] == neg_inf() ? 0.0f : pow2_down(m[nt][r] - to);
+              m[nt][r] = to;
+            }
+            l[nt][r] *= d;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[j][nt][r] *= d;
+              o[j][nt][2 + r] *= d;
+            }
+          }
+      }
+      // exponents of the value scales
+      int shift = 0;
+      if (vbyte != 255) {
+        const int e = (int)vbyte - 127;
+        if (e > expo) {
+          if (expo > -1000) {
+            const float d = pow2(max(expo - e, -126));
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[j][nt][k] *= d;
+          }
+          expo = e;
+        }
+        shift = max(e - expo, kMinShift);
+      }
+      const float back = pow2(-shift);
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = (m[nt][0] == neg_inf() ? 0.0f : m[nt][0]) - (kBias + (float)shift);
+        const float b1 = (m[nt][1] == neg_inf() ? 0.0f : m[nt][1]) - (kBias + (float)shift);
+        const float p0 = ex2(sc[nt][0] - b0), p1 = ex2(sc[nt][1] - b1);
+        const float p2 = ex2(sc[nt][2] - b0), p3 = ex2(sc[nt][3] - b1);
+        l[nt][0] = fmaf(p0 + p2, back, l[nt][0]);
+        l[nt][1] = fmaf(p1 + p3, back, l[nt][1]);
+        pb[nt][0] = transpose8(f16x2_of(p0, p1));
+        pb[nt][1] = transpose8(f16x2_of(p2, p3));
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        uint32_t a[4], b[4];
+        e4m3x4_to_f16(__byte_perm(vw[0][w], vw[1][w], 0x5140), a[0], a[1]);
+        e4m3x4_to_f16(__byte_perm(vw[2][w], vw[3][w], 0x5140), a[2], a[3]);
+        e4m3x4_to_f16(__byte_perm(vw[0][w], vw[1][w], 0x7362), b[0], b[1]);
+        e4m3x4_to_f16(__byte_perm(vw[2][w], vw[3][w], 0x7362), b[2], b[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(o[2 * w][nt], a, pb[nt][0], pb[nt][1]);
+          mma_f16(o[2 * w + 1][nt], b, pb[nt][0], pb[nt][1]);
+        }
+      }
+    }
+
+    // --- sums to the joining warp: rows 2c and 2c + 1, values (D / 8) g ..
+    if (!wait(s, &s.sums_empty, (turn & 1) ^ 1, p.c.status)) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = l[nt][r];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int row = 8 * nt + 2 * c + r;
+        if (g == 0) {
+          s.ml[warp][row][0] = m[nt][r];
+          s.ml[warp][row][1] = x;
+        }
+        float* at = &s.o[warp][row][g * (D / 8)];
+#pragma unroll
+        for (int j = 0; j < MT; j += 2)
+          *reinterpret_cast<float4*>(at + 2 * j) =
+              make_float4(o[j][nt][r], o[j][nt][2 + r], o[j + 1][nt][r], o[j + 1][nt][2 + r]);
+      }
+    if (lane == 0) s.expo[warp] = expo;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.sums_full);
+  }
+}
+
+template <int D, int NT>
+__device__ void join_warp(const AttnParams& p, Smem<D, NT>& s, int lane) {
+  constexpr int PER = 128 / D;          // rows of a pass, 4 values to a lane
+  const int d = lane * 4 % D, sub = lane * 4 / D;
+  for (uint32_t turn = 0;; ++turn) {
+    const int buf = turn & 1;
+    if (!wait(s, &s.item_full[buf], (turn >> 1) & 1, p.c.status)) return;
+    const Item it = s.item[buf];
+    if (it.id < 0) return;
+    if (!wait(s, &s.sums_full, turn & 1, p.c.status)) return;
+    int top_e = s.expo[0];
+#pragma unroll
+    for (int w = 1; w < kTeam; ++w) top_e = max(top_e, s.expo[w]);
+    float less[kTeam];
+#pragma unroll
+    for (int w = 0; w < kTeam; ++w) less[w] = pow2(max(s.expo[w] - top_e, -126));
+    const float out_e = top_e > -1000 ? e8m0_value(top_e + 127) : 0.0f;
+    int nan_at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) nan_at[k] = s.nan_at[buf][d + k];
+    auto store = [&](int r, float4 v, float scale) {
+      const int gr = it.tile * kRows + r, tok = gr / p.group;
+      *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
+                                (int64_t)(it.h * p.group + gr % p.group) * D + d) =
+          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
+                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
+    };
+    for (int r = sub; r < it.rows; r += PER) {
+      float top = s.ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, s.ml[w][r][0]);
+      float l = 0.0f;
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kTeam; ++w) {
+        // a warp that saw nothing has sums of 0, or of NaN
+        const float m = s.ml[w][r][0], x = m == neg_inf() ? 1.0f : pow2_down(m - top);
+        const float y = x * less[w];
+        const float4 u = *reinterpret_cast<const float4*>(&s.o[w][r][d]);
+        l = fmaf(s.ml[w][r][1], x, l);
+        v.x = fmaf(u.x, y, v.x); v.y = fmaf(u.y, y, v.y);
+        v.z = fmaf(u.z, y, v.z); v.w = fmaf(u.w, y, v.w);
+      }
+      const int lim = it.kv - it.n + (it.tile * kRows + r) / p.group;
+      if (lim >= nan_at[0]) v.x = qnan();
+      if (lim >= nan_at[1]) v.y = qnan();
+      if (lim >= nan_at[2]) v.z = qnan();
+      if (lim >= nan_at[3]) v.w = qnan();
+      if (it.parts == 1) {
+        store(r, v, l == 0.0f ? 0.0f : out_e / l);
+      } else {
+        const int64_t at =
+            ((((int64_t)it.b * p.max_tiles + it.tile) * p.c.heads + it.h) * p.max_parts + it.split) *
+                p.part_rows + r;
+        *reinterpret_cast<float4*>(p.parts + at * D + d) = v;
+        if (d == 0)
+          *reinterpret_cast<float4*>(p.part_ml + at * kPartWords) =
+              make_float4(top, l, __int_as_float(top_e), 0.0f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (nan_at[k] != 0x7fffffff && sub == 0) s.nan_at[buf][d + k] = 0x7fffffff;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&s.sums_empty);
+      mbar_arrive(&s.item_empty[buf]);
+    }
+  }
+}
+
+// The parts of a sequence's rows, joined in their order: D / 4 lanes to a row of
+// one query head, 4 values each.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const AttnJoinParams p) {
+  constexpr int L = D / 4, PER = 32 / L;
+  const int lane = threadIdx.x & 31, sub = lane / L, d = lane % L * 4;
+  const int64_t warp = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int heads = p.c.heads * p.group;
+  const int64_t row = warp * PER + sub;               // [sequence][token][head]
+  const int head = (int)(row % heads);
+  const int tok = (int)(row / heads % p.tokens);
+  const int64_t b = row / heads / p.tokens;
+  griddep_wait();
+  int row0 = 0, n = 0, kv = 0;
+  bool in = b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
+            n * p.group <= p.few_rows;
+  const int r = tok * p.group + head % p.group, tile = r / kRows;
+  const int len = split_tokens(kv);
+  const int last = min((tile + 1) * kRows, n * p.group) - 1;      // of the tile's rows
+  const int parts = tile_parts(kv - n + last / p.group, len);
+  in = in && parts > 1;
+  if (!__any_sync(0xffffffffu, in)) return;
+  const int64_t first =
+      in ? ((b * p.max_tiles + tile) * p.c.heads + head / p.group) * p.max_parts : 0;
+  const float* ml = p.part_ml + (first * p.part_rows + r % kRows) * kPartWords;
+  const float* at = p.parts + (first * p.part_rows + r % kRows) * D + d;
+  // a row's maxima, sums and exponents: a part to a lane
+  float w[PER], l = 0.0f;
+  int te = -1000;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const float* from = reinterpret_cast<const float*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ml), k * L));
+    const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
+    float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+    if (lane < count)
+      u = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)lane * p.part_rows * kPartWords));
+    float top = u.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
+    const float x = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
+    w[k] = x * pow2(max(__float_as_int(u.z) - e, -126));
+    float sum = u.y * x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (k == sub) {
+      l = sum;
+      te = e;
+    }
+  }
+  float4 v = make_float4(0, 0, 0, 0);
+  const int most = __reduce_max_sync(0xffffffffu, in ? parts : 0);
+  for (int q0 = 0; q0 < most; q0 += 16) {
+    float4 x[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      x[q] = make_float4(0, 0, 0, 0);
+      if (in && q0 + q < parts)
+        x[q] = __ldcg(reinterpret_cast<const float4*>(at + (int64_t)(q0 + q) * p.part_rows * D));
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float y = __shfl_sync(0xffffffffu, w[0], q0 + q);
+      if (PER == 2) {
+        const float t = __shfl_sync(0xffffffffu, w[PER - 1], q0 + q);
+        if (sub) y = t;
+      }
+      if (q0 + q >= parts) y = 0.0f;
+      v.x = fmaf(x[q].x, y, v.x); v.y = fmaf(x[q].y, y, v.y);
+      v.z = fmaf(x[q].z, y, v.z); v.w = fmaf(x[q].w, y, v.w);
+    }
+  }
+  if (!in) return;
+  const float inv = l == 0.0f ? 0.0f : (te > -1000 ? e8m0_value(te + 127) : 0.0f) / l;
+  *reinterpret_cast<uint2*>(p.out + (int64_t)(row0 + tok) * p.ld_out + (int64_t)head * D + d) =
+      make_uint2(f32x2_to_bf16x2_bits(v.x * inv, v.y * inv),
+                 f32x2_to_bf16x2_bits(v.z * inv, v.w * inv));
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+    split_kernel(const __grid_constant__ AttnParams p) {
+  using S = Smem<D, NT>;
   extern __shared__ __align__(1024) uint8_t raw[];
   S& s = *reinterpret_cast<S*>(raw + S::kRing);
   int* prefix = reinterpret_cast<int*>(raw + S::kRing + sizeof(S));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
 
-  if (tid < kWarps * kStages) mbar_init(&s.full[0][0] + tid, 1);
-  fence_mbar_init();
-  prefetch_tensormap(&p.tm);
-  for (int i = tid; i < 2 * D; i += 32 * kWarps) (&s.nan_at[0][0])[i] = 0x7fffffff;
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&s.full[i], 2);
+      mbar_init(&s.empty[i], kTeam);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.item_full[i], 1);
+      mbar_init(&s.item_empty[i], 1);
+    }
+    mbar_init(&s.sums_full, kTeam);
+    mbar_init(&s.sums_empty, 1);
+    s.dead = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tm);
+  }
+  for (int i = tid; i < 2 * D; i += kThreads) (&s.nan_at[0][0])[i] = 0x7fffffff;
+  griddep_launch();                     // of the join kernel, which waits for this one's end
   griddep_wait();
 
-  // items of each sequence, summed up: 128 sequences at a time
+  // items of each sequence, summed up
   int carry = 0;
-  for (int b0 = 0; b0 < p.c.batch; b0 += 32 * kWarps) {
+  for (int b0 = 0; b0 < p.c.batch; b0 += kThreads) {
     const int b = b0 + tid;
     int count = 0;
     if (b < p.c.batch) {
       int row0, n, kv;
-      if (!sequence_of(p.c, b, row0, n, kv)) {
+      const bool fine = sequence_of(p.c, b, row0, n, kv);
+      if (b < kSeqs) s.seq[b] = make_int3(row0, n, kv);
+      if (!fine) {
         if (blockIdx.x == 0) atomicOr(p.c.status, kStatusIndexRange);
       } else if (n > 0 && n * p.group <= p.few_rows) {
-        count = (n * p.group + kRows - 1) / kRows * seq_splits(kv, part_len(kv)) * p.c.heads;
+        count = (n * p.group + kRows - 1) / kRows * seq_splits(kv, split_tokens(kv)) * p.c.heads;
       }
     }
     int sum = count;
@@ -255,392 +798,62 @@ __global__ void __launch_bounds__(32 * kWarps, 2) split_kernel(const __grid_cons
     if (lane == 31) s.scan[warp] = sum;
     __syncthreads();
     int before = carry;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += s.scan[w];
       carry += s.scan[w];
     }
     if (b < p.c.batch) prefix[b] = before + sum - count;
   }
-  __syncthreads();
-  const int total = carry;
-
-  Feed<D> feed{p, prefix, raw + warp * kStages * 2 * S::kBox, s.full[warp], s.slot[warp], warp, lane,
-               total, (int)blockIdx.x, 0, 0, 0, 0, 0, 0, 0, 0, nullptr, false};
-  feed.open();
-  while (!feed.done && feed.made < kStages) feed.push();
-  __syncwarp();
-
-  uint32_t taken = 0;
-  bool dead = false;                    // a copy did not come in time
-  if (p.flags & IG_FLAG_TEST_COPY_TIMEOUT) {      // as if the first had not
-    dead = true;
+  if (tid == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT)) {      // as if a wait had expired
+    s.dead = 1;
     atomicOr(p.c.status, kStatusTimeout);
   }
-  int turn = 0;
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
-    const Item it = item_of(p, prefix, item);
-    if (it.split >= it.parts) continue;
-    const int steps = warp_steps(it, warp);
+  __syncthreads();
 
-    // --- the tile's queries: rows g and g + 8, FP16 with a power of two apart
-    uint32_t qa[KS][4];
-    float f0, f1;                       // logit of a product: times scale_log2 and the row's power
-    int lim0, lim1;                     // last token that the row sees
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = g + 8 * half, gr = it.tile * kRows + r;
-      const bool in = r < it.rows;
-      const int tok = gr / p.group, head = it.h * p.group + gr % p.group;
-      uint32_t w[D / 8];                // D / 4 values of the lane, two to a word
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (in)
-          v = *(reinterpret_cast<const uint4*>(p.q + (int64_t)(it.row0 + tok) * p.ld_q +
-                                               (int64_t)head * D + c * (D / 4)) + i);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      }
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int e = (int)(top >> 7);          // the largest value is below 2^(e - 126)
-      const float up = e == 255 ? qnan() : pow2(141 - max(e, 20));
-      const float f = p.scale_log2 * (e == 255 ? 1.0f : pow2(max(e, 20) - 141));
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qa[k][half] = f16x2_of(bf16lo(w[2 * k]) * up, bf16hi(w[2 * k]) * up);
-        qa[k][2 + half] = f16x2_of(bf16lo(w[2 * k + 1]) * up, bf16hi(w[2 * k + 1]) * up);
-      }
-      const int lim = in ? it.kv - it.n + tok : 0x7fffffff;
-      if (half) { f1 = f; lim1 = lim; } else { f0 = f; lim0 = lim; }
-    }
-
-    float o[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[j][k] = 0.0f;
-    float m0 = neg_inf(), m1 = neg_inf(), l0 = 0.0f, l1 = 0.0f;
-    int expo = -1000;                   // E; none yet
-
-    for (int i = 0; i < steps; ++i) {
-      const uint32_t st = taken % kStages;
-      if (!dead && !mbar_wait_bounded(s.full[warp] + st, (taken / kStages) & 1, p.c.status))
-        dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      if (dead) break;
-      const uint32_t info = s.slot[warp][st];
-      const int tok = it.t0 + (warp + kWarps * i) * kStep;
-      const uint8_t* kb = raw + (warp * kStages + st) * 2 * S::kBox;
-      const uint8_t* vb = kb + S::kBox;
-      uint32_t vw[4][VW];               // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9
-      float sc[2][4];
-      if (!(info & kAbsent)) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int r = 2 * c + (t & 1) + 8 * (t >> 1);
-          if (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(vb + r * D + ((g ^ (r & 7)) << 4));
-            vw[t][0] = v.x; vw[t][1] = v.y;
-            vw[t][VW - 2] = v.z; vw[t][VW - 1] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(
-                vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + ((g & 1) << 3));
-            vw[t][0] = v.x; vw[t][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int r = nt * 8 + g;
-          uint32_t kw[D / 16];          // D / 4 bytes of token r
-          if (D == 128) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint4 v =
-                  *reinterpret_cast<const uint4*>(kb + r * D + (((2 * c + q) ^ (r & 7)) << 4));
-              kw[(4 * q) % (D / 16)] = v.x; kw[(4 * q + 1) % (D / 16)] = v.y;
-              kw[(4 * q + 2) % (D / 16)] = v.z; kw[(4 * q + 3) % (D / 16)] = v.w;
-            }
-          } else {
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(kb + r * D + ((c ^ ((r >> 1) & 3)) << 4));
-            kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sc[nt][k] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) mma_f16(sc[nt], qa[k], lo_f16(kw[k]), hi_f16(kw[k]));
-        }
-      }
-      ++taken;
-      __syncwarp();                     // the stage has been read
-      if (!feed.done) feed.push();
-      if (info & kAbsent) continue;
-
-      // logits in base 2, masks
-      const float ks = e8m0_value(info & 0xffu);
-      const float a0 = f0 * ks, a1 = f1 * ks;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] *= a0; sc[nt][1] *= a0;
-        sc[nt][2] *= a1; sc[nt][3] *= a1;
-      }
-      const uint32_t vbyte = (info >> 8) & 0xffu;
-      if (vbyte == 255) {               // the block's values are NaN
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vw[t][w] = 0x7f7f7f7fu;
-      }
-      if (tok + kStep - 1 > it.low) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (tok + nt * 8 + 2 * c + (k & 1) > (k < 2 ? lim0 : lim1)) sc[nt][k] = neg_inf();
-        // p is 0 there, but 0 times NaN is not: tokens that no row sees have
-        // any bytes; a NaN of a token that some rows see is kept for those
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int at = tok + 2 * c + (t & 1) + 8 * (t >> 1);
-          if (at > it.high) {
-#pragma unroll
-            for (int w = 0; w < VW; ++w) vw[t][w] = 0;
-          } else if (at > it.low) {
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-              const uint32_t bad = nan_bytes(vw[t][w]);
-              if (bad) {
-                for (int q = 0; q < 4; ++q)
-                  if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[turn & 1][g * (D / 8) + 4 * w + q], at);
-                vw[t][w] &= ~((bad >> 7) * 0xffu);
-              }
-            }
-          }
-        }
-      }
-
-      // maxima: raised where a logit passes m + 7
-      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      if (__any_sync(0xffffffffu, x0 > m0 + kHeadroom || x1 > m1 + kHeadroom)) {
-        float y0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-        float y1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, 2));
-        y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, 2));
-        float d0 = 1.0f, d1 = 1.0f;
-        if (y0 > m0 + kHeadroom) {
-          const float to = ceilf(y0);
-          d0 = m0 == neg_inf() ? 0.0f : pow2_down(m0 - to);
-          m0 = to;
-        }
-        if (y1 > m1 + kHeadroom) {
-          const float to = ceilf(y1);
-          d1 = m1 == neg_inf() ? 0.0f : pow2_down(m1 - to);
-          m1 = to;
-        }
-        l0 *= d0;
-        l1 *= d1;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[j][0] *= d0; o[j][1] *= d0;
-          o[j][2] *= d1; o[j][3] *= d1;
-        }
-      }
-      // exponents of the value scales
-      int shift = 0;
-      if (vbyte != 255) {
-        const int e = (int)vbyte - 127;
-        if (e > expo) {
-          if (expo > -1000) {
-            const float d = pow2(max(expo - e, -126));
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[j][k] *= d;
-          }
-          expo = e;
-        }
-        shift = max(e - expo, kMinShift);
-      }
-      const float back = pow2(-shift);
-      const float b0 = (m0 == neg_inf() ? 0.0f : m0) - (kBias + (float)shift);
-      const float b1 = (m1 == neg_inf() ? 0.0f : m1) - (kBias + (float)shift);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] = ex2(sc[nt][0] - b0); sc[nt][1] = ex2(sc[nt][1] - b0);
-        sc[nt][2] = ex2(sc[nt][2] - b1); sc[nt][3] = ex2(sc[nt][3] - b1);
-        l0 = fmaf(sc[nt][0] + sc[nt][1], back, l0);
-        l1 = fmaf(sc[nt][2] + sc[nt][3], back, l1);
-      }
-      uint32_t pa[4];
-      pa[0] = f16x2_of(sc[0][0], sc[0][1]);
-      pa[1] = f16x2_of(sc[0][2], sc[0][3]);
-      pa[2] = f16x2_of(sc[1][0], sc[1][1]);
-      pa[3] = f16x2_of(sc[1][2], sc[1][3]);
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-        const uint32_t x23 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t y01 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-        const uint32_t y23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        mma_f16(o[4 * w], pa, lo_f16(x01), lo_f16(y01));
-        mma_f16(o[4 * w + 1], pa, hi_f16(x01), hi_f16(y01));
-        mma_f16(o[4 * w + 2], pa, lo_f16(x23), lo_f16(y23));
-        mma_f16(o[4 * w + 3], pa, hi_f16(x23), hi_f16(y23));
-      }
-    }
-
-    // --- the four warps' sums, in their order
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (c == 0) {
-      s.ml[warp][g][0] = m0; s.ml[warp][g][1] = l0;
-      s.ml[warp][g + 8][0] = m1; s.ml[warp][g + 8][1] = l1;
-    }
-    if (lane == 0) s.expo[warp] = expo;
-    __syncthreads();
-    int top_e = s.expo[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top_e = max(top_e, s.expo[w]);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = g + 8 * half;
-      if (r < it.rows) {
-        float top = s.ml[0][r][0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.ml[w][r][0]);
-        const float m = half ? m1 : m0;
-        const float d = m == neg_inf() ? 0.0f
-                                       : pow2_down(m - top) * pow2(max(expo - top_e, -126));
-        float* row = s.o[warp][r] + c * (D / 4);
-#pragma unroll
-        for (int j = 0; j < NT; j += 4) {
-          *reinterpret_cast<float4*>(row + j) =
-              make_float4(o[j][2 * half] * d, o[j + 1][2 * half] * d, o[j + 2][2 * half] * d,
-                          o[j + 3][2 * half] * d);
-          *reinterpret_cast<float4*>(row + D / 8 + j) =
-              make_float4(o[j][2 * half + 1] * d, o[j + 1][2 * half + 1] * d,
-                          o[j + 2][2 * half + 1] * d, o[j + 3][2 * half + 1] * d);
-        }
-      }
-    }
-    __syncthreads();
-    const int* nan_at = s.nan_at[turn & 1];
-    if (tid < D) s.nan_at[(turn + 1) & 1][tid] = 0x7fffffff;
-    ++turn;
-    const float out_e = top_e > -1000 ? e8m0_value(top_e + 127) : 0.0f;
-    for (int i = tid; i < it.rows * (D / 4); i += 32 * kWarps) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float top = s.ml[0][r][0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.ml[w][r][0]);
-      float l = 0.0f;
-      float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float m = s.ml[w][r][0];
-        l += m == neg_inf() ? s.ml[w][r][1] : s.ml[w][r][1] * pow2_down(m - top);
-        const float4 u = *reinterpret_cast<const float4*>(s.o[w][r] + d);
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-      }
-      const int gr = it.tile * kRows + r, tok = gr / p.group;
-      const int lim = it.kv - it.n + tok;
-      if (lim >= nan_at[d]) v.x = qnan();
-      if (lim >= nan_at[d + 1]) v.y = qnan();
-      if (lim >= nan_at[d + 2]) v.z = qnan();
-      if (lim >= nan_at[d + 3]) v.w = qnan();
-      if (it.parts == 1) {
-        const float inv = l == 0.0f ? 0.0f : out_e / l;
-        *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
-                                  (int64_t)(it.h * p.group + gr % p.group) * D + d) =
-            make_uint2(f32x2_to_bf16x2_bits(v.x * inv, v.y * inv),
-                       f32x2_to_bf16x2_bits(v.z * inv, v.w * inv));
-      } else {
-        const int64_t at = (int64_t)item * p.part_rows + r;
-        *reinterpret_cast<float4*>(p.parts + at * D + d) = v;
-        if (d == 0)
-          *reinterpret_cast<float4*>(p.part_ml + at * kPartWords) =
-              make_float4(top, l, __int_as_float(top_e), 0.0f);
-      }
-    }
-    if (it.parts == 1) {
-      __syncthreads();
-      continue;
-    }
-
-    // --- the last of the tile's parts to come joins them, in their order
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t* count = p.counters + ((int64_t)it.b * p.max_tiles + it.tile) * p.c.heads + it.h;
-      const uint32_t old = atom_add_acq_rel_gpu(count, 1u);
-      if (old >= (uint32_t)it.parts) atomicOr(p.c.status, kStatusCorrupt);
-      s.last = old + 1 == (uint32_t)it.parts;
-      if (s.last) *count = 0;
-    }
-    __syncthreads();
-    if (!s.last) continue;
-    __threadfence();
-    for (int i = tid; i < it.rows * (D / 4); i += 32 * kWarps) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      const int64_t first = (int64_t)(it.first + (it.h * it.ns) * it.tiles + it.tile);
-      float top = neg_inf();
-      int te = -1000;
-      for (int q = 0; q < it.parts; ++q) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(
-            p.part_ml + ((first + (int64_t)q * it.tiles) * p.part_rows + r) * kPartWords));
-        top = fmaxf(top, u.x);
-        te = max(te, __float_as_int(u.z));
-      }
-      float l = 0.0f;
-      float4 v = make_float4(0, 0, 0, 0);
-      for (int q = 0; q < it.parts; ++q) {
-        const int64_t at = (first + (int64_t)q * it.tiles) * p.part_rows + r;
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * kPartWords));
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.parts + at * D + d));
-        const float w = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
-        const float y = w * pow2(max(__float_as_int(u.z) - te, -126));
-        l = fmaf(u.y, w, l);
-        v.x = fmaf(x.x, y, v.x); v.y = fmaf(x.y, y, v.y);
-        v.z = fmaf(x.z, y, v.z); v.w = fmaf(x.w, y, v.w);
-      }
-      const float inv = l == 0.0f ? 0.0f : (te > -1000 ? e8m0_value(te + 127) : 0.0f) / l;
-      const int gr = it.tile * kRows + r, tok = gr / p.group;
-      *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
-                                (int64_t)(it.h * p.group + gr % p.group) * D + d) =
-          make_uint2(f32x2_to_bf16x2_bits(v.x * inv, v.y * inv),
-                     f32x2_to_bf16x2_bits(v.z * inv, v.w * inv));
-    }
-  }
-
-  if (dead) {
-    // own copies still in flight land before the block's memory is freed
-    while (taken < feed.made) {
-      mbar_wait_bounded(s.full[warp] + taken % kStages, (taken / kStages) & 1, p.c.status);
-      ++taken;
-    }
-  }
+  if (warp < kTeam)
+    compute_warp<D, NT>(p, s, raw, warp, lane);
+  else if (warp == kTeam)
+    copy_warp<D, NT>(p, s, raw, prefix, carry, lane);
+  else
+    join_warp<D, NT>(p, s, lane);
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
-  const size_t smem = Smem<D>::kRing + sizeof(Smem<D>) + sizeof(int) * (size_t)p.c.batch;
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  const size_t smem = Smem<D, NT>::kRing + sizeof(Smem<D, NT>) + sizeof(int) * (size_t)p.c.batch;
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(split_kernel<D>, dim3(2 * sm_count()), dim3(32 * kWarps), smem, st, p);
+  e = launch_pdl(split_kernel<D, NT>, dim3((NT == 1 ? 3 : 2) * sm_count()), dim3(kThreads), smem,
+                 st, p);
+  if (e != cudaSuccess || p.max_parts == 1) return e;
+  AttnJoinParams j;
+  j.c = p.c;
+  j.out = p.out;
+  j.parts = p.parts;
+  j.part_ml = p.part_ml;
+  j.ld_out = p.ld_out;
+  j.group = p.group;
+  j.few_rows = p.few_rows;
+  j.max_tiles = p.max_tiles;
+  j.max_parts = p.max_parts;
+  j.part_rows = p.part_rows;
+  const int most = p.few_rows / p.group;              // tokens of a sequence of this kernel
+  j.tokens = p.c.max_q < most ? p.c.max_q : most;
+  if (j.tokens == 0) return cudaSuccess;              // a kv head's rows are too many
+  const int64_t rows = (int64_t)p.c.batch * j.tokens * p.c.heads * p.group;
+  return launch_pdl(join_kernel<D>, dim3((unsigned)((rows * (D / 4) + 127) / 128)), dim3(128), 0, st,
+                    j);
 }
 
 }  // namespace
 
+// A tile of 8 rows at most (as many as a kv head can have in this call) leaves
+// half the 16 columns unused: one MMA less of two, and three blocks to an SM.
+// The rows' bits are the same in both.
 cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st) {
-  return head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
+  if (p.part_rows <= 8) return head_dim == 128 ? launch<128, 1>(p, st) : launch<64, 1>(p, st);
+  return head_dim == 128 ? launch<128, 2>(p, st) : launch<64, 2>(p, st);
 }
 
 }  // namespace ig
