@@ -62,6 +62,7 @@ struct AttnParams {
   KvParams c;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
+  uint32_t* next;       // items taken beyond each block's first; 0 between calls
   float* parts;         // results of parts [sequence][tile][kv head][part][row][D]
   float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
   int64_t ld_q, ld_out;
@@ -76,6 +77,7 @@ struct AttnParams {
 struct AttnJoinParams {
   KvParams c;
   __nv_bfloat16* out;
+  uint32_t* next;
   const float* parts;
   const float* part_ml;
   int64_t ld_out;
@@ -100,8 +102,8 @@ constexpr int kFewRows = 64;
 // --- splitting a sequence ---------------------------------------------------
 // A sequence's tokens are cut into parts of a length that kv_len alone fixes
 // (so that a row's bits do not depend on the batch): 256 up to 4096 tokens, then
-// whole 512s, at most 32 of them.
-constexpr int kMaxSplits = 32;
+// whole 512s, at most 64 of them.
+constexpr int kMaxSplits = 64;
 constexpr int kPartWords = 4;           // of a row of a part: maximum, sum, exponent, unused
 __host__ __device__ inline int split_tokens(int kv) {
   return kv <= 4096 ? 256 : 512 * ((kv + 512 * kMaxSplits - 1) / (512 * kMaxSplits));

@@ -137,8 +137,8 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
   return IG_OK;
 }
 
-// What the workspace of an attention call holds behind the status word and (not
-// used here) the counters.
+// What the workspace of an attention call holds behind the status word and the
+// counters (of which it uses one).
 struct AttnPlan {
   int group, max_tiles, max_parts, part_rows;
   size_t ml_at, total;
@@ -286,6 +286,7 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.c = kv_params(cache, batch, shape->T, ws);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.next = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kCountersOffset);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.ml_at);
   p.ld_q = shape->ld_q;

@@ -62,7 +62,7 @@ struct Item {
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int kStages = NT == 1 ? 3 : 4;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kBox = kStep * D;              // bytes of a step's keys (or values)
   static constexpr int kStage = 2 * kTeam * kBox;     // keys of four steps, then values
   static constexpr int kRing = kStages * kStage;
@@ -196,20 +196,25 @@ struct Unit {
 
 // The unit after u: of the same item, else of the block's next item that has a
 // part its rows see (id -1: none). Pages only.
+// Which block takes an item does not show in its bits.
 __device__ __forceinline__ void next_unit(const AttnParams& p, const int* prefix, const int3* seq,
                                           int total, int lane, Unit& u) {
   u.step += kUnit;
   if (u.it.id < 0 || u.it.t0 + u.step * kStep >= u.it.t1) {
-    int id = u.it.id < 0 ? (int)blockIdx.x : u.it.id + (int)gridDim.x;
+    // a block's first item is its own, the others go to who asks first
+    int id = (int)blockIdx.x;
     u.step = 0;
-    while (true) {
+    for (bool own = u.it.id < 0;; own = false) {
+      if (!own) {
+        if (lane == 0) id = (int)(atomicAdd(p.next, 1u) + gridDim.x);
+        id = __shfl_sync(0xffffffffu, id, 0);
+      }
       if (id >= total) {
         u.it.id = -1;
         return;
       }
       u.it = item_of(p, prefix, seq, id);
       if (u.it.split < u.it.parts) break;
-      id += gridDim.x;
     }
   }
   u.info = kAbsent;
@@ -665,84 +670,126 @@ __device__ void join_warp(const AttnParams& p, Smem<D, NT>& s, int lane) {
   }
 }
 
-// The parts of a sequence's rows, joined in their order: D / 4 lanes to a row of
-// one query head, 4 values each.
-template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const AttnJoinParams p) {
-  constexpr int L = D / 4, PER = 32 / L;
-  const int lane = threadIdx.x & 31, sub = lane / L, d = lane % L * 4;
-  const int64_t warp = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+// The parts of a sequence's rows, joined: D / 4 lanes to a row of one query head,
+// 4 values each, 128 / D rows to a block. Eight sums, of the parts w, w + 8, ... in
+// their order, added in the order of w; W warps share them. Few rows are a matter
+// of how long it takes to get at a row's parts (W = 8: 256 rows of up to 64 parts
+// 5 us), many of how many rows there are at a time (W = 2: 4096 rows of up to 16
+// parts).
+constexpr int kJoinSums = 8;
+
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
+  constexpr int L = D / 4, PER = 32 / L, SL = kMaxSplits / 32;
+  constexpr int C = kJoinSums / W;      // sums of a warp: w = warp, warp + W, ...
+  constexpr int B = 8 / C;              // parts of each asked for at a time
+  __shared__ float4 sums[kJoinSums][32];
+  __shared__ float weight[PER][kMaxSplits], inverse[PER];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
   const int heads = p.c.heads * p.group;
-  const int64_t row = warp * PER + sub;               // [sequence][token][head]
+  const int64_t row = (int64_t)blockIdx.x * PER + sub;          // [sequence][token][head]
   const int head = (int)(row % heads);
-  const int tok = (int)(row / heads % p.tokens);
-  const int64_t b = row / heads / p.tokens;
+  const int tok = (int)(row / heads % max(p.tokens, 1));
+  const int64_t b = row / heads / max(p.tokens, 1);
   griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0;
   int row0 = 0, n = 0, kv = 0;
   bool in = b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
             n * p.group <= p.few_rows;
   const int r = tok * p.group + head % p.group, tile = r / kRows;
   const int len = split_tokens(kv);
   const int last = min((tile + 1) * kRows, n * p.group) - 1;      // of the tile's rows
-  const int parts = tile_parts(kv - n + last / p.group, len);
+  int parts = in ? tile_parts(kv - n + last / p.group, len) : 1;
   in = in && parts > 1;
-  if (!__any_sync(0xffffffffu, in)) return;
+  if (!__any_sync(0xffffffffu, in)) return;         // the same in all warps
+  if (!in) parts = 1;
   const int64_t first =
       in ? ((b * p.max_tiles + tile) * p.c.heads + head / p.group) * p.max_parts : 0;
   const float* ml = p.part_ml + (first * p.part_rows + r % kRows) * kPartWords;
   const float* at = p.parts + (first * p.part_rows + r % kRows) * D + d;
-  // a row's maxima, sums and exponents: a part to a lane
-  float w[PER], l = 0.0f;
-  int te = -1000;
+  uint4 x[B][C];
+  auto ask = [&](int q0) {
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int q = q0 + kJoinSums * i + W * k + warp;
+        x[i][k] = make_uint4(0, 0, 0, 0);
+        if (q < parts) x[i][k] = ldg_cg_v4(at + (int64_t)q * p.part_rows * D);
+      }
+  };
+  ask(0);
+  // maxima, sums and exponents, by the first warps, a row each: parts `lane` and
+  // `lane` + 32
+  for (int k = warp; k < PER; k += W) {
     const float* from = reinterpret_cast<const float*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ml), k * L));
-    const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
-    float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
-    if (lane < count)
-      u = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)lane * p.part_rows * kPartWords));
-    float top = u.x;
+    const int count = __shfl_sync(0xffffffffu, parts, k * L);
+    float4 u[SL];
+    float top = neg_inf();
+    int e = -1000;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      u[i] = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+      if (lane + 32 * i < count && count > 1)
+        u[i] = __ldcg(reinterpret_cast<const float4*>(
+            from + (int64_t)(lane + 32 * i) * p.part_rows * kPartWords));
+    }
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      top = fmaxf(top, u[i].x);
+      e = max(e, __float_as_int(u[i].z));
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
-    const float x = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
-    w[k] = x * pow2(max(__float_as_int(u.z) - e, -126));
-    float sum = u.y * x;
+    e = __reduce_max_sync(0xffffffffu, e);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const float y = u[i].x == neg_inf() ? 1.0f : pow2_down(u[i].x - top);
+      weight[k][lane + 32 * i] = y * pow2(max(__float_as_int(u[i].z) - e, -126));
+      sum = fmaf(u[i].y, y, sum);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (k == sub) {
-      l = sum;
-      te = e;
-    }
+    if (lane == 0)
+      inverse[k] = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
   }
-  float4 v = make_float4(0, 0, 0, 0);
-  const int most = __reduce_max_sync(0xffffffffu, in ? parts : 0);
-  for (int q0 = 0; q0 < most; q0 += 16) {
-    float4 x[16];
+  __syncthreads();
+  float4 v[C];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      x[q] = make_float4(0, 0, 0, 0);
-      if (in && q0 + q < parts)
-        x[q] = __ldcg(reinterpret_cast<const float4*>(at + (int64_t)(q0 + q) * p.part_rows * D));
-    }
+  for (int k = 0; k < C; ++k) v[k] = make_float4(0, 0, 0, 0);
+  const int most = __reduce_max_sync(0xffffffffu, parts);
+  for (int q0 = 0; q0 < most; q0 += kJoinSums * B) {
+    if (q0) ask(q0);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float y = __shfl_sync(0xffffffffu, w[0], q0 + q);
-      if (PER == 2) {
-        const float t = __shfl_sync(0xffffffffu, w[PER - 1], q0 + q);
-        if (sub) y = t;
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int q = q0 + kJoinSums * i + W * k + warp;
+        if (q < parts) {
+          const float y = weight[sub][q];
+          v[k].x = fmaf(__uint_as_float(x[i][k].x), y, v[k].x);
+          v[k].y = fmaf(__uint_as_float(x[i][k].y), y, v[k].y);
+          v[k].z = fmaf(__uint_as_float(x[i][k].z), y, v[k].z);
+          v[k].w = fmaf(__uint_as_float(x[i][k].w), y, v[k].w);
+        }
       }
-      if (q0 + q >= parts) y = 0.0f;
-      v.x = fmaf(x[q].x, y, v.x); v.y = fmaf(x[q].y, y, v.y);
-      v.z = fmaf(x[q].z, y, v.z); v.w = fmaf(x[q].w, y, v.w);
-    }
   }
-  if (!in) return;
-  const float inv = l == 0.0f ? 0.0f : (te > -1000 ? e8m0_value(te + 127) : 0.0f) / l;
+#pragma unroll
+  for (int k = 0; k < C; ++k) sums[warp + W * k][lane] = v[k];
+  __syncthreads();
+  if (warp != 0 || !in) return;
+  float4 o = sums[0][lane];
+#pragma unroll
+  for (int i = 1; i < kJoinSums; ++i) {
+    const float4 u = sums[i][lane];
+    o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+  }
+  const float inv = inverse[sub];
   *reinterpret_cast<uint2*>(p.out + (int64_t)(row0 + tok) * p.ld_out + (int64_t)head * D + d) =
-      make_uint2(f32x2_to_bf16x2_bits(v.x * inv, v.y * inv),
-                 f32x2_to_bf16x2_bits(v.z * inv, v.w * inv));
+      make_uint2(f32x2_to_bf16x2_bits(o.x * inv, o.y * inv),
+                 f32x2_to_bf16x2_bits(o.z * inv, o.w * inv));
 }
 
 template <int D, int NT>
@@ -826,8 +873,9 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(split_kernel<D, NT>, dim3((NT == 1 ? 3 : 2) * sm_count()), dim3(kThreads), smem,
                  st, p);
-  if (e != cudaSuccess || p.max_parts == 1) return e;
+  if (e != cudaSuccess) return e;
   AttnJoinParams j;
+  j.next = p.next;
   j.c = p.c;
   j.out = p.out;
   j.parts = p.parts;
@@ -840,10 +888,15 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   j.part_rows = p.part_rows;
   const int most = p.few_rows / p.group;              // tokens of a sequence of this kernel
   j.tokens = p.c.max_q < most ? p.c.max_q : most;
-  if (j.tokens == 0) return cudaSuccess;              // a kv head's rows are too many
-  const int64_t rows = (int64_t)p.c.batch * j.tokens * p.c.heads * p.group;
-  return launch_pdl(join_kernel<D>, dim3((unsigned)((rows * (D / 4) + 127) / 128)), dim3(128), 0, st,
-                    j);
+  // (no tokens: a kv head has too many rows; one part: nothing to join. A block
+  // all the same, for the items' counter)
+  const bool any = j.tokens > 0 && p.max_parts > 1;
+  const int64_t rows = any ? (int64_t)p.c.batch * j.tokens * p.c.heads * p.group : 1;
+  if (!any) j.c.batch = 0;
+  constexpr int PER = 128 / D;
+  const dim3 grid((unsigned)((rows + PER - 1) / PER));
+  if (grid.x > 8u * sm_count()) return launch_pdl(join_kernel<D, 2>, grid, dim3(64), 0, st, j);
+  return launch_pdl(join_kernel<D, 8>, grid, dim3(256), 0, st, j);
 }
 
 }  // namespace
