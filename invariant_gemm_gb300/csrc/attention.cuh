@@ -67,6 +67,7 @@ struct AttnParams {
   float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
   int64_t ld_q, ld_out;
   int32_t heads_q, group;   // query heads, and of one kv head
+  uint32_t group_inv;   // 65536 / group, rounded up: row / group for few rows
   int32_t few_rows;     // sequences with at most this many rows a kv head are the split kernel's
   int32_t max_tiles;    // 16-row tiles of such a sequence
   int32_t max_parts, part_rows;

@@ -40,7 +40,7 @@ namespace ig {
 namespace {
 
 constexpr int kTeam = 4;                // warps that compute
-constexpr int kThreads = 32 * (kTeam + 2);
+constexpr int kThreads = 32 * (kTeam + 1);
 constexpr int kStep = kKvBlock;
 constexpr int kRows = 16;               // of a tile
 constexpr int kUnit = 32;               // steps looked up at a time
@@ -62,7 +62,8 @@ struct Item {
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;
+  static constexpr int kBlocks = (D == 128 ? 2 : 3) + (NT == 1);      // to an SM
   static constexpr int kBox = kStep * D;              // bytes of a step's keys (or values)
   static constexpr int kStage = 2 * kTeam * kBox;     // keys of four steps, then values
   static constexpr int kRing = kStages * kStage;
@@ -71,22 +72,23 @@ struct Smem {
   alignas(16) __nv_bfloat16 q[2][8 * NT][D];
   float ml[kTeam][8 * NT][2];
   int expo[kTeam];
-  int nan_at[2][D];
+  alignas(16) int nan_at[2][D];
   Item item[2];
   uint64_t full[kStages], empty[kStages], item_full[2], item_empty[2], sums_full, sums_empty;
   uint32_t info[kStages][kTeam];
   int3 seq[kSeqs];                      // row0, n, kv of the first sequences
-  int scan[kTeam + 2];
+  int scan[kTeam + 1];
   int dead;
 };
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 __device__ __forceinline__ float qnan() { return __uint_as_float(0x7fc00000u); }
 
-// 2^d for a whole d <= 0 (0 below -126, NaN for NaN)
+// 2^d for a whole d <= 0 (0 below -126, NaN for NaN): d + 127 is in the low bits
+// of its sum with 1.5 * 2^23
 __device__ __forceinline__ float pow2_down(float d) {
-  if (d != d) return d;
-  return d < -126.0f ? 0.0f : pow2((int)d);
+  const float r = __uint_as_float(__float_as_uint(d + (12582912.0f + 127.0f)) << 23);
+  return d >= -126.0f ? r : d != d ? d : 0.0f;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -143,6 +145,11 @@ __device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint3
   return __all_sync(0xffffffffu, ok);
 }
 
+// row / group for the few rows of a sequence here.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+  return (int)((uint32_t)row * p.group_inv >> 16);
+}
+
 __device__ __forceinline__ int seq_splits(int kv, int len) { return kv > 0 ? (kv + len - 1) / len : 1; }
 
 // Parts with tokens that a tile sees whose last row sees token `high`.
@@ -177,8 +184,8 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, const int* prefix, 
   it.h = (int)v;
   const int r = it.tile * kRows;
   it.rows = min(kRows, rows - r);
-  it.low = it.kv - it.n + r / p.group;
-  it.high = it.kv - it.n + (r + it.rows - 1) / p.group;
+  it.low = it.kv - it.n + token_of(p, r);
+  it.high = it.kv - it.n + token_of(p, r + it.rows - 1);
   const int end = max(it.high + 1, 0);
   it.parts = tile_parts(it.high, len);
   it.t0 = it.split * len;
@@ -255,6 +262,8 @@ __device__ void copy_warp(const AttnParams& p, Smem<D, NT>& s, uint8_t* ring, co
       ok = wait(s, &s.item_empty[buf], ((items >> 1) & 1) ^ 1, p.c.status);
       if (!ok) break;
       ++items;
+      for (int d = lane; d < D; d += 32) s.nan_at[buf][d] = 0x7fffffff;
+      __syncwarp();
       if (lane == 0) {
         s.item[buf] = u.it;
         const uint32_t bytes = u.it.id < 0 ? 0 : u.it.rows * D * 2;
@@ -263,7 +272,7 @@ __device__ void copy_warp(const AttnParams& p, Smem<D, NT>& s, uint8_t* ring, co
       __syncwarp();
       if (u.it.id < 0) break;
       const int r = u.it.tile * kRows, last = r + u.it.rows;      // rows of the sequence
-      const int tok = r / p.group + lane;
+      const int tok = token_of(p, r) + lane;
       const int from = max(r, tok * p.group), to = min(last, (tok + 1) * p.group);
       if (from < to)
         bulk_g2s(&s.q[buf][from - r][0],
@@ -312,6 +321,66 @@ __device__ void copy_warp(const AttnParams& p, Smem<D, NT>& s, uint8_t* ring, co
       mbar_wait_bounded(&s.full[m % S::kStages], (m / S::kStages) & 1, p.c.status);
     for (uint32_t m = items > 2 ? items - 2 : 0; m < items; ++m)
       mbar_wait_bounded(&s.item_full[m & 1], (m >> 1) & 1, p.c.status);
+  }
+}
+
+// A warp's share of the rows: the four warps' sums, in their order.
+template <int D, int NT>
+__device__ __forceinline__ void join_sums(const AttnParams& p, const Smem<D, NT>& s, int buf,
+                                          int warp, int lane) {
+  constexpr int PER = 128 / D;          // rows of a pass, 4 values to a lane
+  const int d = lane * 4 % D, sub = lane * 4 / D;
+  const Item& it = s.item[buf];
+  int top_e = s.expo[0];
+#pragma unroll
+  for (int w = 1; w < kTeam; ++w) top_e = max(top_e, s.expo[w]);
+  float less[kTeam];
+#pragma unroll
+  for (int w = 0; w < kTeam; ++w) less[w] = pow2(max(s.expo[w] - top_e, -126));
+  const float out_e = top_e > -1000 ? e8m0_value(top_e + 127) : 0.0f;
+  const int4 nan_at = *reinterpret_cast<const int4*>(&s.nan_at[buf][d]);
+  const bool parts = it.parts > 1;
+  const int64_t part =
+      ((((int64_t)it.b * p.max_tiles + it.tile) * p.c.heads + it.h) * p.max_parts + it.split) *
+      p.part_rows;
+#pragma unroll
+  for (int i = 0; i < 2 * NT; i += PER) {
+    const int r = i / PER * kTeam * PER + warp * PER + sub;
+    if (r >= it.rows) break;
+    float m[kTeam], top = neg_inf(), l = 0.0f;
+    float4 u[kTeam], v = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kTeam; ++w) {
+      m[w] = s.ml[w][r][0];
+      u[w] = *reinterpret_cast<const float4*>(&s.o[w][r][d]);
+      top = fmaxf(top, m[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kTeam; ++w) {
+      // a warp that saw nothing has sums of 0, or of NaN
+      const float x = m[w] == neg_inf() ? 1.0f : pow2_down(m[w] - top), y = x * less[w];
+      l = fmaf(s.ml[w][r][1], x, l);
+      v.x = fmaf(u[w].x, y, v.x); v.y = fmaf(u[w].y, y, v.y);
+      v.z = fmaf(u[w].z, y, v.z); v.w = fmaf(u[w].w, y, v.w);
+    }
+    const int gr = it.tile * kRows + r, tok = token_of(p, gr), lim = it.kv - it.n + tok;
+    if (lim >= nan_at.x) v.x = qnan();
+    if (lim >= nan_at.y) v.y = qnan();
+    if (lim >= nan_at.z) v.z = qnan();
+    if (lim >= nan_at.w) v.w = qnan();
+    if (parts) {
+      const int64_t at = part + r;
+      *reinterpret_cast<float4*>(p.parts + at * D + d) = v;
+      if (d == 0)
+        *reinterpret_cast<float4*>(p.part_ml + at * kPartWords) =
+            make_float4(top, l, __int_as_float(top_e), 0.0f);
+    } else {
+      const float scale = l == 0.0f ? 0.0f : out_e / l;
+      *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
+                                (it.h * p.group + gr - tok * p.group) * D + d) =
+          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
+                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
+    }
   }
 }
 
@@ -364,7 +433,7 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
       for (int i = 0; i < 2; ++i) {
         const int row = 8 * nt + 2 * c + i;
         f[nt][i] = __shfl_sync(0xffffffffu, mine, (2 * c + i) * 4);
-        lim[nt][i] = row < rows ? it.kv - it.n + (it.tile * kRows + row) / p.group : 0x7fffffff;
+        lim[nt][i] = row < rows ? it.kv - it.n + token_of(p, it.tile * kRows + row) : 0x7fffffff;
       }
     }
 
@@ -572,7 +641,7 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
       }
     }
 
-    // --- sums to the joining warp: rows 2c and 2c + 1, values (D / 8) g ..
+    // --- sums of all warps: rows 2c and 2c + 1, values (D / 8) g ..
     if (!wait(s, &s.sums_empty, (turn & 1) ^ 1, p.c.status)) return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -596,72 +665,8 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
     if (lane == 0) s.expo[warp] = expo;
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sums_full);
-  }
-}
-
-template <int D, int NT>
-__device__ void join_warp(const AttnParams& p, Smem<D, NT>& s, int lane) {
-  constexpr int PER = 128 / D;          // rows of a pass, 4 values to a lane
-  const int d = lane * 4 % D, sub = lane * 4 / D;
-  for (uint32_t turn = 0;; ++turn) {
-    const int buf = turn & 1;
-    if (!wait(s, &s.item_full[buf], (turn >> 1) & 1, p.c.status)) return;
-    const Item it = s.item[buf];
-    if (it.id < 0) return;
     if (!wait(s, &s.sums_full, turn & 1, p.c.status)) return;
-    int top_e = s.expo[0];
-#pragma unroll
-    for (int w = 1; w < kTeam; ++w) top_e = max(top_e, s.expo[w]);
-    float less[kTeam];
-#pragma unroll
-    for (int w = 0; w < kTeam; ++w) less[w] = pow2(max(s.expo[w] - top_e, -126));
-    const float out_e = top_e > -1000 ? e8m0_value(top_e + 127) : 0.0f;
-    int nan_at[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) nan_at[k] = s.nan_at[buf][d + k];
-    auto store = [&](int r, float4 v, float scale) {
-      const int gr = it.tile * kRows + r, tok = gr / p.group;
-      *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
-                                (int64_t)(it.h * p.group + gr % p.group) * D + d) =
-          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
-                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
-    };
-    for (int r = sub; r < it.rows; r += PER) {
-      float top = s.ml[0][r][0];
-#pragma unroll
-      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, s.ml[w][r][0]);
-      float l = 0.0f;
-      float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < kTeam; ++w) {
-        // a warp that saw nothing has sums of 0, or of NaN
-        const float m = s.ml[w][r][0], x = m == neg_inf() ? 1.0f : pow2_down(m - top);
-        const float y = x * less[w];
-        const float4 u = *reinterpret_cast<const float4*>(&s.o[w][r][d]);
-        l = fmaf(s.ml[w][r][1], x, l);
-        v.x = fmaf(u.x, y, v.x); v.y = fmaf(u.y, y, v.y);
-        v.z = fmaf(u.z, y, v.z); v.w = fmaf(u.w, y, v.w);
-      }
-      const int lim = it.kv - it.n + (it.tile * kRows + r) / p.group;
-      if (lim >= nan_at[0]) v.x = qnan();
-      if (lim >= nan_at[1]) v.y = qnan();
-      if (lim >= nan_at[2]) v.z = qnan();
-      if (lim >= nan_at[3]) v.w = qnan();
-      if (it.parts == 1) {
-        store(r, v, l == 0.0f ? 0.0f : out_e / l);
-      } else {
-        const int64_t at =
-            ((((int64_t)it.b * p.max_tiles + it.tile) * p.c.heads + it.h) * p.max_parts + it.split) *
-                p.part_rows + r;
-        *reinterpret_cast<float4*>(p.parts + at * D + d) = v;
-        if (d == 0)
-          *reinterpret_cast<float4*>(p.part_ml + at * kPartWords) =
-              make_float4(top, l, __int_as_float(top_e), 0.0f);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (nan_at[k] != 0x7fffffff && sub == 0) s.nan_at[buf][d + k] = 0x7fffffff;
+    join_sums<D, NT>(p, s, buf, warp, lane);
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&s.sums_empty);
@@ -793,7 +798,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, Smem<D, NT>::kBlocks)
     split_kernel(const __grid_constant__ AttnParams p) {
   using S = Smem<D, NT>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -808,15 +813,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.item_full[i], 1);
-      mbar_init(&s.item_empty[i], 1);
+      mbar_init(&s.item_empty[i], kTeam);
     }
     mbar_init(&s.sums_full, kTeam);
-    mbar_init(&s.sums_empty, 1);
+    mbar_init(&s.sums_empty, kTeam);
     s.dead = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm);
   }
-  for (int i = tid; i < 2 * D; i += kThreads) (&s.nan_at[0][0])[i] = 0x7fffffff;
   griddep_launch();                     // of the join kernel, which waits for this one's end
   griddep_wait();
 
@@ -859,10 +863,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 
   if (warp < kTeam)
     compute_warp<D, NT>(p, s, raw, warp, lane);
-  else if (warp == kTeam)
-    copy_warp<D, NT>(p, s, raw, prefix, carry, lane);
   else
-    join_warp<D, NT>(p, s, lane);
+    copy_warp<D, NT>(p, s, raw, prefix, carry, lane);
 }
 
 template <int D, int NT>
@@ -871,7 +873,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(split_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(split_kernel<D, NT>, dim3((NT == 1 ? 3 : 2) * sm_count()), dim3(kThreads), smem,
+  e = launch_pdl(split_kernel<D, NT>, dim3(Smem<D, NT>::kBlocks * sm_count()), dim3(kThreads), smem,
                  st, p);
   if (e != cudaSuccess) return e;
   AttnJoinParams j;
