@@ -106,6 +106,8 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
     return IG_ERR_ARG;
   }
   if ((!q && (w_q || q_out)) || (q && !q_out) || (!k && w_k)) return IG_ERR_ARG;
+  if (s->T * ((int64_t)(q ? s->heads_q : 0) + (k ? s->heads_k : 0)) > (1ll << 32))
+    return IG_ERR_UNSUPPORTED;
   const int64_t cq = (int64_t)s->heads_q * s->head_dim, ck = (int64_t)s->heads_k * s->head_dim;
   if ((q && (check_ld(s->ld_q, cq) != IG_OK || check_ld(s->ld_q_out, cq) != IG_OK)) ||
       (k && check_ld(s->ld_k, ck) != IG_OK))
@@ -223,9 +225,7 @@ int ig_kv_append(const ig_rope_shape* shape, const ig_kv_cache* cache, const ig_
   const int64_t most = batch->max_q < shape->T ? batch->max_q : shape->T;
   p.nblocks = (int)((most + 2 * kKvBlock - 2) / kKvBlock);
   p.r.heads_k = 0;
-  if ((int64_t)p.nblocks * batch->batch * cache->heads > (1ll << 31) ||
-      shape->T * (int64_t)p.r.heads_q > (1ll << 32))
-    return IG_ERR_UNSUPPORTED;
+  if ((int64_t)p.nblocks * batch->batch * cache->heads > (1ll << 29)) return IG_ERR_UNSUPPORTED;
   return cuda_status(launch_kv_append(p, cache->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
