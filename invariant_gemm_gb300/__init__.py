@@ -523,24 +523,22 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
 # last tokens.
 
 def _heads(what, name, t, dev, b16):
-    """(T, heads, D, stride between tokens) of an operand of heads."""
+    """(sizes, stride between tokens) of an operand of heads."""
     shape = t.shape
     if t.dtype is b16 and len(shape) == 3 and t.get_device() == dev >= 0:
         T, heads, D = shape
-        if t.is_contiguous():
-            return T, heads, D, heads * D
         ld, hs, inner = t.stride()
         if (inner == 1 or D == 1) and (hs == D or heads == 1):
-            return T, heads, D, (ld if T > 1 else heads * D)
+            return shape, ld if T > 1 else heads * D
     _why(what, name, t, dev, b16, shape)
 
 
-def _like(what, name, t, dev, b16, T, heads, D):
-    """Checks an operand of T tokens of these heads; returns its stride."""
-    got = _heads(what, name, t, dev, b16)
-    if got[:3] != (T, heads, D):
-        _why(what, name, t, dev, b16, (T, heads, D))
-    return got[3]
+def _like(what, name, t, dev, b16, shape):
+    """Checks an operand of these heads; returns its stride."""
+    got, ld = _heads(what, name, t, dev, b16)
+    if got != shape:
+        _why(what, name, t, dev, b16, shape)
+    return ld
 
 
 def _cache_of(what, cache, scales, dev, u8):
@@ -549,36 +547,30 @@ def _cache_of(what, cache, scales, dev, u8):
     if not (cache.dtype is u8 and len(shape) == 5 and shape[1] == 2 and cache.get_device() == dev):
         _why(what, "cache", cache, dev, u8, shape)
     pages, _, heads, page, D = shape
-    inner, blocks = 2 * heads * page * D, page >> 4
-    ps, ss = inner, 2 * heads * blocks
-    if not (scales.dtype is u8 and scales.shape == (pages, 2, heads, blocks) and
-            scales.get_device() == dev):
-        _why(what, "scales", scales, dev, u8, (pages, 2, heads, blocks))
-    if not cache.is_contiguous():
-        if pages > 1:
-            ps = cache.stride(0)
-        if pages and not cache[0].is_contiguous():
+    blocks = page >> 4
+    want = (pages, 2, heads, blocks)
+    if not (scales.dtype is u8 and scales.shape == want and scales.get_device() == dev):
+        _why(what, "scales", scales, dev, u8, want)
+    ps, ss = 2 * heads * page * D, 2 * heads * blocks
+    if not cache.is_contiguous() and pages:
+        ps = cache.stride(0) if pages > 1 else ps
+        if not cache[0].is_contiguous():
             _why(what, "cache", cache, dev, u8, shape)
-    if not scales.is_contiguous():
-        if pages > 1:
-            ss = scales.stride(0)
-        if pages and not scales[0].is_contiguous():
-            _why(what, "scales", scales, dev, u8, (pages, 2, heads, blocks))
+    if not scales.is_contiguous() and pages:
+        ss = scales.stride(0) if pages > 1 else ss
+        if not scales[0].is_contiguous():
+            _why(what, "scales", scales, dev, u8, want)
     return (_KV_CACHE(cache.data_ptr(), scales.data_ptr(), pages, ps, ss, page, heads, D, 0),
             heads, D)
 
 
 def _batch_of(what, cu, kv_len, page_table, dev, i32, max_q):
-    B = kv_len.numel()
-    if not (cu.dtype is i32 and kv_len.dtype is i32 and page_table.dtype is i32 and
-            cu.numel() == B + 1 and cu.is_contiguous() and kv_len.is_contiguous() and
-            page_table.dim() == 2 and page_table.shape[0] == B and page_table.is_contiguous() and
-            cu.get_device() == kv_len.get_device() == page_table.get_device() == dev):
-        _vector(what, "cu", cu, dev, i32, B + 1)
-        _vector(what, "kv_len", kv_len, dev, i32, B)
-        _why(what, "page_table", page_table, dev, i32, (B, page_table.shape[-1]))
-    return _BATCH(cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], B,
-                  max_q)
+    B, cols = page_table.shape if page_table.dim() == 2 else (-1, 0)
+    if not (page_table.dtype is i32 and page_table.is_contiguous() and
+            page_table.get_device() == dev and B >= 0):
+        _why(what, "page_table", page_table, dev, i32, (kv_len.numel(), cols))
+    return _BATCH(_vector(what, "cu", cu, dev, i32, B + 1),
+                  _vector(what, "kv_len", kv_len, dev, i32, B), page_table.data_ptr(), cols, B, max_q)
 
 
 def _angles(what, cos_sin, positions, dev, T, torch):
@@ -586,10 +578,12 @@ def _angles(what, cos_sin, positions, dev, T, torch):
     rows = rot = 0
     pc = pp = None
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            _why(what, "cos_sin", cos_sin, dev, torch.float32, cos_sin.shape)
-        rows, rot = cos_sin.shape
-        pc = _vector(what, "cos_sin", cos_sin, dev, torch.float32, rows * rot)
+        shape = cos_sin.shape
+        if not (len(shape) == 2 and cos_sin.dtype is torch.float32 and cos_sin.is_contiguous() and
+                cos_sin.get_device() == dev):
+            _why(what, "cos_sin", cos_sin, dev, torch.float32, shape)
+        rows, rot = shape
+        pc = cos_sin.data_ptr()
     if positions is not None:
         pp = _vector(what, "positions", positions, dev, torch.int32, T)
     return rows, rot, pc, pp
@@ -614,19 +608,19 @@ def qk_norm_rope(q, k, q_out, k_out, ws, *, w_q=None, w_k=None, cos_sin=None, po
     if lead is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise IGError(-1, "qk_norm_rope: q and q_out, k and k_out go together, one pair at least")
     dev = lead.get_device()
-    T, hq, D, ld_q = _heads(what, "q" if q is not None else "k", lead, dev, b16)
-    hk = ld_k = ld_qo = ld_ko = 0
+    hq = hk = ld_q = ld_k = ld_qo = ld_ko = 0
     pq = pk = pqo = pko = pwq = pwk = None
     if q is not None:
-        ld_qo = _like(what, "q_out", q_out, dev, b16, T, hq, D)
+        shape, ld_q = _heads(what, "q", q, dev, b16)
+        T, hq, D = shape
+        ld_qo = _like(what, "q_out", q_out, dev, b16, shape)
         pq, pqo = q.data_ptr(), q_out.data_ptr()
-    else:
-        hq = ld_q = 0
     if k is not None:
-        Tk, hk, Dk, ld_k = _heads(what, "k", k, dev, b16)
-        if Tk != T or Dk != D:
-            _why(what, "k", k, dev, b16, (T, hk, D))
-        ld_ko = _like(what, "k_out", k_out, dev, b16, T, hk, D)
+        shape, ld_k = _heads(what, "k", k, dev, b16)
+        if q is not None and (shape[0] != T or shape[2] != D):
+            _why(what, "k", k, dev, b16, (T, shape[1], D))
+        T, hk, D = shape
+        ld_ko = _like(what, "k_out", k_out, dev, b16, shape)
         pk, pko = k.data_ptr(), k_out.data_ptr()
     if w_q is not None:
         pwq = _vector(what, "w_q", w_q, dev, b16, D)
@@ -651,8 +645,9 @@ def kv_append(k, v, cache, scales, cu, kv_len, page_table, ws, *, w_k=None, cos_
     import torch
     what, b16 = "kv_append", torch.bfloat16
     dev = k.get_device()
-    T, hk, D, ld_k = _heads(what, "k", k, dev, b16)
-    ld_v = _like(what, "v", v, dev, b16, T, hk, D)
+    shape, ld_k = _heads(what, "k", k, dev, b16)
+    T, hk, D = shape
+    ld_v = _like(what, "v", v, dev, b16, shape)
     c, heads, Dc = _cache_of(what, cache, scales, dev, torch.uint8)
     if heads != hk or Dc != D:
         _why(what, "k", k, dev, b16, (T, heads, Dc))
@@ -662,10 +657,11 @@ def kv_append(k, v, cache, scales, cu, kv_len, page_table, ws, *, w_k=None, cos_
     if (q is None) != (q_out is None):
         raise IGError(-1, "kv_append: q and q_out go together")
     if q is not None:
-        Tq, hq, Dq, ld_q = _heads(what, "q", q, dev, b16)
-        if Tq != T or Dq != D:
+        shape, ld_q = _heads(what, "q", q, dev, b16)
+        hq = shape[1]
+        if shape[0] != T or shape[2] != D:
             _why(what, "q", q, dev, b16, (T, hq, D))
-        ld_qo = _like(what, "q_out", q_out, dev, b16, T, hq, D)
+        ld_qo = _like(what, "q_out", q_out, dev, b16, shape)
         pq, pqo = q.data_ptr(), q_out.data_ptr()
     if w_q is not None:
         pwq = _vector(what, "w_q", w_q, dev, b16, D)
@@ -688,10 +684,11 @@ def kv_gather(cache, scales, cu, kv_len, page_table, k_out, v_out, ws, *, stream
     what, b16 = "kv_gather", torch.bfloat16
     dev = cache.get_device()
     c, heads, D = _cache_of(what, cache, scales, dev, torch.uint8)
-    T, hk, Dk, ld_k = _heads(what, "k_out", k_out, dev, b16)
-    if hk != heads or Dk != D:
+    shape, ld_k = _heads(what, "k_out", k_out, dev, b16)
+    T = shape[0]
+    if shape[1] != heads or shape[2] != D:
         _why(what, "k_out", k_out, dev, b16, (T, heads, D))
-    ld_v = _like(what, "v_out", v_out, dev, b16, T, heads, D)
+    ld_v = _like(what, "v_out", v_out, dev, b16, shape)
     b = _batch_of(what, cu, kv_len, page_table, dev, torch.int32, 0)
     _status_ws(what, ws, dev, torch.uint8)
     rc = (_LIB or lib()).ig_kv_gather(c, b, T, k_out.data_ptr(), ld_k, v_out.data_ptr(), ld_v,
@@ -727,8 +724,9 @@ def paged_attention(q, cache, scales, cu, kv_len, page_table, out, ws, *, max_q=
     import torch
     what, b16 = "paged_attention", torch.bfloat16
     dev = q.get_device()
-    T, hq, D, ld_q = _heads(what, "q", q, dev, b16)
-    ld_o = _like(what, "out", out, dev, b16, T, hq, D)
+    shape, ld_q = _heads(what, "q", q, dev, b16)
+    T, hq, D = shape
+    ld_o = _like(what, "out", out, dev, b16, shape)
     c, heads, Dc = _cache_of(what, cache, scales, dev, torch.uint8)
     if Dc != D:
         _why(what, "q", q, dev, b16, (T, hq, Dc))

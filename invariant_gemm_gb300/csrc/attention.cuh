@@ -62,12 +62,14 @@ struct AttnParams {
   KvParams c;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
-  uint32_t* next;       // items taken beyond each block's first; 0 between calls
+  uint32_t* next;       // items taken beyond each block's first, of the split and of the
+                        // prompt kernel; 0 between calls
   float* parts;         // results of parts [sequence][tile][kv head][part][row][D]
   float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
   int64_t ld_q, ld_out;
   int32_t heads_q, group;   // query heads, and of one kv head
   uint32_t group_inv;   // 65536 / group, rounded up: row / group for few rows
+  float group_rcp;      // 1 / group
   int32_t few_rows;     // sequences with at most this many rows a kv head are the split kernel's
   int32_t max_tiles;    // 16-row tiles of such a sequence
   int32_t max_parts, part_rows;

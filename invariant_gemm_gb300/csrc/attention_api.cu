@@ -293,6 +293,7 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.ld_out = shape->ld_out;
   p.heads_q = shape->heads_q;
   p.group = pl.group;
+  p.group_rcp = 1.0f / (float)pl.group;
   p.group_inv = (uint32_t)((65536 + pl.group - 1) / pl.group);
   p.few_rows = kFewRows;
   p.max_tiles = pl.max_tiles;

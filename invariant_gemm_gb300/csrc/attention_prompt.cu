@@ -37,6 +37,15 @@ constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
 constexpr int kNoBlock = 2000;          // tokens that no row sees, or an absent page
 constexpr int kInfo = 8;                // steps whose pages and scales are held
 
+// The block's rows.
+struct Rows {
+  int b, h, row0;              // sequence, kv head, the sequence's first row of q
+  int tok0, rem;               // its token and query head that the block's first row is
+  int rows, tiles;
+  int low, high;               // last token that the first and the last row see
+  int steps;
+};
+
 template <int D>
 struct Smem {
   static constexpr int kPart = kTile * D;               // bytes of 128 rows of codes
@@ -47,7 +56,7 @@ struct Smem {
   static constexpr int kEnd = kV16 + 4 * kPart;
   uint64_t k_full[2], k_empty[2], v8_full[2], v8_empty[2], v16_full[2], v16_empty[2];
   uint64_t s_full[2], p_full[2];
-  uint64_t info_full[kInfo], info_empty[kInfo], drain;
+  uint64_t info_full[kInfo], info_empty[kInfo], q_raw, q_full, drain;
   // of a step's 8 blocks: scale of the keys; kBias + e - E and 2^(E - e) for p; e
   alignas(16) float ks[kInfo][8], bias[kInfo][8], back[kInfo][8];
   int ve[kInfo][8];
@@ -55,11 +64,11 @@ struct Smem {
   int partly[kInfo];                    // some block of the step is not there
   float less[kInfo];                    // 2^(E before - E) of the step
   int top;                              // E in the end
-  int nan_at[D];
+  int nan_at[D], nans;                  // first NaN token of each value; whether there is one
   float most[2][2][2 * kTile];          // [step % 2][half][row]: largest logit, sum
   uint32_t tmem;
   int dead;
-  int item[8];
+  Rows it;
 };
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
@@ -252,6 +261,104 @@ __device__ __forceinline__ bool all_of(int bar, bool mine) {
   return all != 0;
 }
 
+// row / group for the rows of a block (and the first one's remainder): a float's
+// rounding is far from the 0.5 / group that is between a half and a whole number.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+  return (int)(((float)row + 0.5f) * p.group_rcp);
+}
+
+// The block's queries, from where they were copied to (rows of D bf16 in the place
+// of the first converted values) to the two numbers that make up each: of the warp's
+// 32 rows and its half of D, 8 values of a row to a lane at a time, the row's 8 lanes
+// (D = 64: 4) side by side. Returns what a product of the lane's own row is worth in
+// the softmax's base 2. Rolled loops, and not inlined, as what stores the results: the
+// code of what a block does once comes from far.
+template <int D>
+__device__ __noinline__ float convert_queries(const AttnParams& p, Smem<D>& s, uint8_t* raw) {
+  using S = Smem<D>;
+  constexpr int CH = D / 16;            // 16-byte chunks of half a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 3, half = (warp >> 2) & 1, ch = lane % CH;
+  const int warp_row = t * kTile + (warp & 3) * 32, rows = s.it.rows;
+  const uint8_t* from = raw + S::kV16 + half * D + ch * 16;
+#pragma unroll 2
+  for (int r = warp_row + lane / CH; r < warp_row + 32; r += 32 / CH) {
+    const uint4 w = *reinterpret_cast<const uint4*>(from + r * 2 * D);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+    if (r >= rows) top = 0;
+#pragma unroll
+    for (int o = CH / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (ch == 0) s.most[0][half][r] = __uint_as_float(top);
+  }
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + (warp & 3)) : "memory");
+  auto exponent = [&](int r) {          // the row's largest value is below 2^(this - 126)
+    return (int)(max(__float_as_uint(s.most[0][0][r]), __float_as_uint(s.most[0][1][r])) >> 7);
+  };
+#pragma unroll 1
+  for (int r = warp_row + lane / CH; r < warp_row + 32; r += 32 / CH) {
+    uint4 w = *reinterpret_cast<const uint4*>(from + r * 2 * D);
+    if (r >= rows) w = make_uint4(0, 0, 0, 0);
+    const int e = exponent(r);
+    float up = e == 255 ? qnan() : pow2(134 - max(e, 20));
+    if (p.scale_log2 < 0.0f) up = -up;
+    float x[8], y[8];
+    unpack8(w, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] *= up;
+    const uint2 hi = e4m3_encode8(x);
+    e4m3_decode8(hi, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
+    const int c16 = half * (D / 32) + ch / 2;           // 16-byte chunk of a row of codes
+    const int at = (D == 128 ? c16 ^ (r & 7) : c16 ^ ((r >> 1) & 3)) * 16 + (ch & 1) * 8;
+    uint8_t* dst = raw + S::kQ + t * 2 * S::kPart + (r & 127) * D + at;
+    *reinterpret_cast<uint2*>(dst) = hi;
+    *reinterpret_cast<uint2*>(dst + S::kPart) = e4m3_encode8(y);
+  }
+  const int e = exponent(warp_row + lane);
+  return fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
+}
+
+// Half a row of the results: l is the sum of its p.
+template <int D>
+__device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, float l,
+                                           uint32_t to) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = (warp >> 2) & 1;
+  const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;
+  const Rows& it = s.it;
+  const int tok = token_of(p, it.rem + my_row);
+  const bool in = my_row < it.rows;
+  uint4* dst = reinterpret_cast<uint4*>(
+      p.out + (int64_t)(it.row0 + it.tok0 + tok) * p.ld_out +
+      (int64_t)(it.h * p.group + it.rem + my_row - tok * p.group) * D + half * (D / 2));
+  const int expo = s.top;
+  const bool nans = s.nans;
+  const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float v[16];
+    if (it.steps > 0) tmem_ld16(to + 16 * c, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
+    if (nans) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((in ? it.low + tok : 0x7fffffff) >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
+    }
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        dst[2 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
+                                    f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
+                                    f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
+                                    f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ AttnParams p) {
@@ -275,13 +382,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.info_full[i], 1);
       mbar_init(&s.info_empty[i], 21);
     }
+    mbar_init(&s.q_raw, 1);
+    mbar_init(&s.q_full, 16);
     mbar_init(&s.drain, 1);
     s.dead = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm);
   }
   if (tid < D) s.nan_at[tid] = 0x7fffffff;
+  if (tid == 0) s.nans = 0;
   griddep_wait();
+  if (tid == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT)) {      // as if a wait had expired
+    s.dead = 1;
+    atomicOr(p.c.status, kStatusTimeout);
+  }
 
   // the block's rows: sequences in order, a sequence's last rows first
   if (warp == 0) {
@@ -302,101 +416,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int l = __ffs(hit) - 1;
         if (lane == l) {
           const int v = at - (sum - count);
-          s.item[0] = b0 + l;
-          s.item[1] = v % p.c.heads;
-          s.item[2] = count / p.c.heads - 1 - v / p.c.heads;
-          s.item[3] = row0;
-          s.item[4] = n;
-          s.item[5] = kv;
+          const int row = (count / p.c.heads - 1 - v / p.c.heads) * 2 * kTile;
+          Rows it;
+          it.b = b0 + l;
+          it.h = v % p.c.heads;
+          it.row0 = row0;
+          it.tok0 = row / p.group;
+          it.rem = row % p.group;
+          it.rows = min(2 * kTile, n * p.group - row);
+          it.tiles = it.rows > kTile ? 2 : 1;
+          it.low = kv - n + it.tok0;
+          it.high = it.low + token_of(p, it.rem + it.rows - 1);
+          it.steps = it.high >= 0 ? it.high / kTile + 1 : 0;
+          s.it = it;
+          mbar_arrive_expect_tx(&s.q_raw, it.rows * D * 2);
         }
         found = b0 + l;
       }
       at -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) s.item[6] = found;
+    if (lane == 0 && found < 0) s.it.b = -1;
     __syncwarp();
     if (found >= 0) {
-      tmem_alloc(&s.tmem, 512);
-      tmem_relinquish();
+      // the queries: the heads of one kv head lie together
+      const int rem = s.it.rem, end = rem + s.it.rows;
+      for (int tok = lane; tok * p.group < end; tok += 32) {
+        const int x = max(rem, tok * p.group), y = min(end, (tok + 1) * p.group);
+        bulk_g2s(raw + S::kV16 + (x - rem) * 2 * D,
+                 p.q + (int64_t)(s.it.row0 + s.it.tok0 + tok) * p.ld_q +
+                     (int64_t)(s.it.h * p.group + x - tok * p.group) * D,
+                 (uint32_t)(y - x) * D * 2, &s.q_raw);
+      }
     }
+  } else if (warp == 1) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s.item[6] < 0) return;
-  const int b = s.item[0], h = s.item[1], row_first = s.item[2] * 2 * kTile;
-  const int row0 = s.item[3], n = s.item[4], kv = s.item[5];
-  const int all_rows = n * p.group;
-  const int rows = min(2 * kTile, all_rows - row_first);
-  const int tiles = rows > kTile ? 2 : 1;
-  const int low = kv - n + row_first / p.group;                  // last token its first row sees
-  const int high = kv - n + (row_first + rows - 1) / p.group;    // and its last row
-  const int steps = high >= 0 ? high / kTile + 1 : 0;
   const uint32_t tmem = s.tmem;
-
-  // ---- queries: half a row to a thread
+  if (s.it.b < 0) {
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int h = s.it.h, tiles = s.it.tiles, low = s.it.low, high = s.it.high, steps = s.it.steps;
   const int half = (warp >> 2) & 1;
   const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;      // of warps 0-15
-  float f = 0.0f;                       // logit of a product, base 2
-  int lim = 0x7fffffff;                 // last token that the row sees
-  uint4 w[D / 16];
-  if (warp < 16) {
-    const int gr = row_first + my_row;
-    const bool in = my_row < rows;
-    const int tok = gr / p.group, head = h * p.group + gr % p.group;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(row0 + tok) * p.ld_q +
-                                                      (int64_t)head * D + half * (D / 2));
-    if (in) lim = kv - n + tok;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
-    }
-    s.most[0][half][my_row] = __uint_as_float(top);
-  }
-  __syncthreads();
-  if (warp < 16) {
-    const uint32_t top = max(__float_as_uint(s.most[0][0][my_row]),
-                             __float_as_uint(s.most[0][1][my_row]));
-    const int e = (int)(top >> 7);      // the largest value is below 2^(e - 126)
-    float up = e == 255 ? qnan() : pow2(134 - max(e, 20));
-    f = fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
-    if (p.scale_log2 < 0.0f) up = -up;
-    const int r = my_row;
-    uint8_t* hi = raw + S::kQ + (r >> 7) * 2 * S::kPart + (r & 127) * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {  // 16 values: 16 bytes of each part
-      uint32_t a[4], c[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x[8], y[8];
-        unpack8(w[2 * i + j], x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= up;
-        const uint2 q = e4m3_encode8(x);
-        e4m3_decode8(q, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
-        const uint2 t = e4m3_encode8(y);
-        a[2 * j] = q.x; a[2 * j + 1] = q.y;
-        c[2 * j] = t.x; c[2 * j + 1] = t.y;
-      }
-      const int ch = half * (D / 32) + i;
-      const int at = (D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) * 16;
-      *reinterpret_cast<uint4*>(hi + at) = make_uint4(a[0], a[1], a[2], a[3]);
-      *reinterpret_cast<uint4*>(hi + S::kPart + at) = make_uint4(c[0], c[1], c[2], c[3]);
-    }
-    fence_proxy_async_smem();
-  }
-  if (tid == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT)) {      // as if a wait had expired
-    s.dead = 1;
-    atomicOr(p.c.status, kStatusTimeout);
-  }
-  __syncthreads();
 
   // 512 threads with 96 registers and 256 with 48: the 61440 of the launch
   if (warp < 8 * tiles) {
@@ -406,11 +472,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + lanes;
     const uint32_t to = tmem + 2 * kTile + t * D + half * (D / 2) + lanes;
-    const int tile_low = kv - n + (row_first + t * kTile) / p.group;
+    const int tile_low = low + token_of(p, s.it.rem + t * kTile);
+    const int lim = my_row < s.it.rows ? low + token_of(p, s.it.rem + my_row)
+                                       : 0x7fffffff;                    // last token it sees
     const int pair_bar = 1 + t * 4 + (warp & 3);        // the two warps of these rows
+    bool ok = all_of(9 + t, wait<true>(s, &s.q_raw, 0, p.c.status));
+    float f = 0.0f;                     // logit of a product, base 2
+    if (ok) {
+      f = convert_queries<D>(p, s, raw);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.q_full);
+    }
     float m = neg_inf(), l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < steps; ++j) {
+    for (int j = 0; ok && j < steps; ++j) {
       const int in = j % kInfo;
       ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
       // what the scales have to say is here before the products are
@@ -532,40 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       // (first half) + (second half), for both the same
       l = s.most[steps & 1][0][my_row] + s.most[steps & 1][1][my_row];
-      const int gr = row_first + my_row;
-      const bool in = my_row < rows;
-      const int tok = gr / p.group, head = h * p.group + gr % p.group;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(row0 + tok) * p.ld_out +
-                                            (int64_t)head * D + half * (D / 2));
-      const int expo = s.top;
-      const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float v[16];
-        if (steps > 0) {
-          tmem_ld16(to + 16 * c, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[i] = l == 0.0f ? 0.0f : v[i] * inv;
-          if (lim >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
-        }
-        if (in) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            dst[2 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
-                                        f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
-                                        f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
-                                        f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
-        }
-      }
+      store_results<D>(p, s, l, to);
     }
   } else if (warp < 16) {
     more_registers<96>();
-    // the second tile has no rows: only its share of the scales' barrier
+    // the second tile has no rows: only its share of the barriers
+    if (lane == 0) mbar_arrive(&s.q_full);
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo;
       if (!wait<true>(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
@@ -576,9 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------- values
     fewer_registers<48>();
     const int r = tid - 512;            // token of the step
+    bool ok = wait<true>(s, &s.q_full, 0, p.c.status);  // the queries were where the values go
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
-      bool ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
+      ok = ok && wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status) &&
                 wait<true>(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
                 wait<true>(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -606,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // seen by some rows only: a NaN is kept for those
               const uint32_t bad = ((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
               if (at > low && bad) {
+                s.nans = 1;
                 for (int q = 0; q < 4; ++q)
                   if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[64 * d + 4 * i + q], at);
                 u[i] &= ~((bad >> 7) * 0xffu);
@@ -674,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
    } else if (warp == 22) {
     // ------------------------------------------------------- pages and scales
     // a block to a lane, four steps at a time, ahead of the copies
-    const int32_t* table = p.c.table + (int64_t)b * p.c.ld_table;
+    const int32_t* table = p.c.table + (int64_t)s.it.b * p.c.ld_table;
     const int blocks = 1 << (p.c.page_shift - 4);
     bool ok = true;
     int expo = -1000;                   // E, the largest value scale so far
@@ -739,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    bool ok = wait(s, &s.k_full[0], 0, p.c.status);
+    bool ok = wait<true>(s, &s.q_full, 0, p.c.status) && wait(s, &s.k_full[0], 0, p.c.status);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       for (int t = 0; t < tiles; ++t) qk(t, 0);
@@ -778,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (s.dead && warp == 20) mbar_wait_bounded(&s.q_raw, 0, p.c.status);
   if (s.dead && warp == 21) {
     // MMAs still at work end before the tensor memory is given back
     tc_fence_after();
@@ -786,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_bounded(&s.drain, 0, p.c.status);
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

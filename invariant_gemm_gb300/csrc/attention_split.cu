@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   const int tok = (int)(row / heads % max(p.tokens, 1));
   const int64_t b = row / heads / max(p.tokens, 1);
   griddep_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.next[threadIdx.x] = 0;
   int row0 = 0, n = 0, kv = 0;
   bool in = b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
             n * p.group <= p.few_rows;
