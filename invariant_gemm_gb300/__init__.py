@@ -524,21 +524,21 @@ def block_norm(h, y=None, w_post=None, w_pre=None, *, gate=None, scale=1.0, eps=
 
 def _heads(what, name, t, dev, b16):
     """(sizes, stride between tokens) of an operand of heads."""
-    shape = t.shape
-    if t.dtype is b16 and len(shape) == 3 and t.get_device() == dev >= 0:
-        T, heads, D = shape
-        ld, hs, inner = t.stride()
-        if (inner == 1 or D == 1) and (hs == D or heads == 1):
-            return shape, ld if T > 1 else heads * D
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3 and t.dtype is b16 and t.get_device() == dev >= 0:
+        _, heads, D = shape
+        if strides[2] == 1 and (strides[1] == D or heads == 1) or 0 in shape:
+            return shape, strides[0] if shape[0] > 1 else heads * D
     _why(what, name, t, dev, b16, shape)
 
 
 def _like(what, name, t, dev, b16, shape):
     """Checks an operand of these heads; returns its stride."""
-    got, ld = _heads(what, name, t, dev, b16)
-    if got != shape:
-        _why(what, name, t, dev, b16, shape)
-    return ld
+    if t.shape == shape:
+        if t.dtype is b16 and t.is_contiguous() and t.get_device() == dev >= 0:
+            return shape[1] * shape[2]
+        return _heads(what, name, t, dev, b16)[1]
+    _why(what, name, t, dev, b16, shape)
 
 
 def _cache_of(what, cache, scales, dev, u8):
@@ -565,12 +565,17 @@ def _cache_of(what, cache, scales, dev, u8):
 
 
 def _batch_of(what, cu, kv_len, page_table, dev, i32, max_q):
-    B, cols = page_table.shape if page_table.dim() == 2 else (-1, 0)
-    if not (page_table.dtype is i32 and page_table.is_contiguous() and
-            page_table.get_device() == dev and B >= 0):
-        _why(what, "page_table", page_table, dev, i32, (kv_len.numel(), cols))
-    return _BATCH(_vector(what, "cu", cu, dev, i32, B + 1),
-                  _vector(what, "kv_len", kv_len, dev, i32, B), page_table.data_ptr(), cols, B, max_q)
+    shape = page_table.shape
+    if not (len(shape) == 2 and page_table.dtype is i32 and page_table.is_contiguous() and
+            page_table.get_device() == dev):
+        _why(what, "page_table", page_table, dev, i32, shape)
+    B, cols = shape
+    if not (cu.dtype is i32 and kv_len.dtype is i32 and cu.numel() == B + 1 and
+            kv_len.numel() == B and cu.is_contiguous() and kv_len.is_contiguous() and
+            cu.get_device() == kv_len.get_device() == dev):
+        _vector(what, "cu", cu, dev, i32, B + 1)
+        _vector(what, "kv_len", kv_len, dev, i32, B)
+    return _BATCH(cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), cols, B, max_q)
 
 
 def _angles(what, cos_sin, positions, dev, T, torch):
