@@ -62,11 +62,15 @@ struct AttnParams {
   KvParams c;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
-  uint32_t* next;       // items taken beyond each block's first, of the split and of the
-                        // prompt kernel; 0 between calls
+  uint32_t* next;       // [0] items of the split kernel taken beyond each block's first,
+                        // [1] whether the prompt kernel cut a sequence; 0 between calls
   float* parts;         // results of parts [sequence][tile][kv head][part][row][D]
   float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
+  float* big;           // the prompt kernel's parts [sequence][item][row][D]
+  float* big_ml;        // [sequence][item][row][kPartWords]
   int64_t ld_q, ld_out;
+  int32_t big_rows;     // rows that an item has room for
+  int32_t big_by_row;   // see big_place
   int32_t heads_q, group;   // query heads, and of one kv head
   uint32_t group_inv;   // 65536 / group, rounded up: row / group for few rows
   float group_rcp;      // 1 / group
@@ -84,7 +88,7 @@ struct AttnJoinParams {
   const float* parts;
   const float* part_ml;
   int64_t ld_out;
-  int32_t group, few_rows, tokens, max_tiles, max_parts, part_rows;
+  int32_t group, few_rows, tokens, max_tiles, max_parts, part_rows, big_by_row;
 };
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t st);
@@ -110,6 +114,38 @@ constexpr int kMaxSplits = 64;
 constexpr int kPartWords = 4;           // of a row of a part: maximum, sum, exponent, unused
 __host__ __device__ inline int split_tokens(int kv) {
   return kv <= 4096 ? 256 : 512 * ((kv + 512 * kMaxSplits - 1) / (512 * kMaxSplits));
+}
+
+// The prompt kernel cuts a sequence's tokens too where its rows are few blocks' work
+// (256 rows of a kv head each): into up to 16 parts, so many that blocks times parts
+// fill a GPU's 152 SMs once at most, of three steps of 128 tokens at least. Again
+// nothing but the sequence's own sizes decides.
+constexpr int kPromptRows = 256;
+constexpr int kPromptStep = 128;
+constexpr int kPromptItems = 152;       // of a sequence that is cut
+constexpr int kPromptParts = 16;
+__host__ __device__ inline int prompt_parts(int64_t rows, int kv, int heads) {
+  const int64_t blocks = (rows + kPromptRows - 1) / kPromptRows * heads;
+  if (blocks > kPromptItems / 2) return 1;
+  int parts = kPromptItems / (int)blocks;
+  const int steps = (kv + kPromptStep - 1) / kPromptStep;
+  if (parts > steps / 3) parts = steps / 3;
+  if (parts > kPromptParts) parts = kPromptParts;
+  return parts < 1 ? 1 : parts;
+}
+// Place of a sequence that the prompt kernel cuts in the workspace: its number or, where
+// there are more sequences than can have over kFewRows rows, by where its rows begin
+// (two such sequences' rows begin kFewRows + 1 apart at least).
+__host__ __device__ inline int64_t big_place(bool by_row, int b, int64_t row0, int group) {
+  return by_row ? row0 * group / (kFewRows + 1) : b;
+}
+// Steps to a part.
+__host__ __device__ inline int prompt_len(int kv, int parts) {
+  return ((kv + kPromptStep - 1) / kPromptStep + parts - 1) / parts;
+}
+// Parts that a tile sees whose last row sees token `high`.
+__host__ __device__ inline int prompt_seen(int high, int len) {
+  return high < 0 || len < 1 ? 1 : high / kPromptStep / len + 1;
 }
 
 #ifdef __CUDACC__

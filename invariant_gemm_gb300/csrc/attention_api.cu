@@ -143,7 +143,8 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
 // counters (of which it uses one).
 struct AttnPlan {
   int group, max_tiles, max_parts, part_rows;
-  size_t ml_at, total;
+  int big_rows, big_by_row;
+  size_t ml_at, big_at, big_ml_at, total;    // behind the counters
 };
 
 int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, AttnPlan* pl) {
@@ -169,7 +170,20 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
   const int64_t items = (int64_t)b->batch * pl->max_tiles * c->heads * pl->max_parts;
   if (items > (1ll << 30)) return IG_ERR_UNSUPPORTED;
   pl->ml_at = align_up((size_t)items * pl->part_rows * c->head_dim * 4, 256);
-  pl->total = kMapOffset + pl->ml_at + (size_t)items * pl->part_rows * kPartWords * 4;
+  pl->big_at = align_up(pl->ml_at + (size_t)items * pl->part_rows * kPartWords * 4, 256);
+  // sequences that the prompt kernel may cut: more rows than the split kernel's, of
+  // few enough tiles, long enough
+  pl->big_rows = pl->big_by_row = 0;
+  int64_t big = 0;
+  if (rows > kFewRows && s->T * pl->group > kFewRows &&
+      prompt_parts(kFewRows + 1, (int)cap, c->heads) > 1) {
+    const int64_t places = s->T * pl->group / (kFewRows + 1) + 1;
+    pl->big_by_row = places < b->batch;
+    pl->big_rows = (int)(rows < kPromptRows ? rows : kPromptRows);
+    big = (pl->big_by_row ? places : b->batch) * kPromptItems * pl->big_rows;
+  }
+  pl->big_ml_at = align_up(pl->big_at + (size_t)big * c->head_dim * 4, 256);
+  pl->total = kMapOffset + pl->big_ml_at + (size_t)big * kPartWords * 4;
   return IG_OK;
 }
 
@@ -289,6 +303,10 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.next = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kCountersOffset);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.ml_at);
+  p.big = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.big_at);
+  p.big_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.big_ml_at);
+  p.big_rows = pl.big_rows;
+  p.big_by_row = pl.big_by_row;
   p.ld_q = shape->ld_q;
   p.ld_out = shape->ld_out;
   p.heads_q = shape->heads_q;

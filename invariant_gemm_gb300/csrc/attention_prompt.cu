@@ -43,7 +43,9 @@ struct Rows {
   int tok0, rem;               // its token and query head that the block's first row is
   int rows, tiles;
   int low, high;               // last token that the first and the last row see
-  int steps;
+  int step0, steps;            // its steps: of the part of the tokens that is its
+  int parts;                   // parts that the rows see; with several the results go to
+  int64_t part;                // row `part` of the parts on
 };
 
 template <int D>
@@ -322,19 +324,21 @@ __device__ __noinline__ float convert_queries(const AttnParams& p, Smem<D>& s, u
   return fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
 }
 
-// Half a row of the results: l is the sum of its p.
+// Half a row of the results, l the sum of its p: into the output or, of one part of
+// several, as it stands into the workspace.
 template <int D>
-__device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, float l,
+__device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, float m, float l,
                                            uint32_t to) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = (warp >> 2) & 1;
   const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;
   const Rows& it = s.it;
   const int tok = token_of(p, it.rem + my_row);
-  const bool in = my_row < it.rows;
+  const bool in = my_row < it.rows, whole = it.parts == 1;
   uint4* dst = reinterpret_cast<uint4*>(
       p.out + (int64_t)(it.row0 + it.tok0 + tok) * p.ld_out +
       (int64_t)(it.h * p.group + it.rem + my_row - tok * p.group) * D + half * (D / 2));
-  const int expo = s.top;
+  float4* part = reinterpret_cast<float4*>(p.big + (it.part + my_row) * D + half * (D / 2));
+  const int expo = s.top, lim = it.low + tok;
   const bool nans = s.nans;
   const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
 #pragma unroll 1
@@ -342,20 +346,109 @@ __device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, floa
     float v[16];
     if (it.steps > 0) tmem_ld16(to + 16 * c, v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
+    for (int i = 0; i < 16; ++i) v[i] = l == 0.0f ? 0.0f : whole ? v[i] * inv : v[i];
     if (nans) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if ((in ? it.low + tok : 0x7fffffff) >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
+        if (lim >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
     }
-    if (in) {
+    if (!in) continue;
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         dst[2 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
                                     f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
                                     f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
                                     f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        part[4 * c + i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
+  }
+  if (in && !whole && half == 0)
+    *reinterpret_cast<float4*>(p.big_ml + (it.part + my_row) * kPartWords) =
+        make_float4(m, l, __int_as_float(expo), 0.0f);
+}
+
+// The parts of the rows of a token, joined in their order: D / 4 lanes to a query head,
+// 4 values each; all parts of a row asked for together.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const AttnJoinParams p) {
+  constexpr int L = D / 4, PER = 32 / L;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
+  const int t = blockIdx.x;
+  griddep_wait();
+  if (__ldcg(p.next + 1) == 0) return;  // no sequence was cut
+  int b = 0;
+  for (int hi = p.c.batch; hi - b > 1;) {       // the last sequence that starts at or before t
+    const int mid = (b + hi) >> 1;
+    if (__ldg(p.c.cu + mid) <= t) b = mid; else hi = mid;
+  }
+  int row0, n, kv;
+  if (!sequence_of(p.c, b, row0, n, kv) || t < row0 || t >= row0 + n || n * p.group <= p.few_rows)
+    return;
+  const int cut = prompt_parts(n * p.group, kv, p.c.heads);
+  if (cut == 1) return;
+  const int len = prompt_len(kv, cut), heads = p.c.heads * p.group, tok = t - row0;
+  const int tiles = (n * p.group + kPromptRows - 1) / kPromptRows;
+  for (int h0 = warp * PER; h0 < heads; h0 += kJoinWarps * PER) {
+    const int h = min(h0 + sub, heads - 1), r = tok * p.group + h % p.group;
+    const int tile = r / kPromptRows;
+    const int last = min((tile + 1) * kPromptRows, n * p.group) - 1;
+    const int parts = prompt_seen(kv - n + last / p.group, len);
+    const bool in = h0 + sub < heads && parts > 1;
+    // item (tiles - 1 - tile, part, kv head) of the sequence
+    const int64_t first = big_place(p.big_by_row, b, row0, p.group) * kPromptItems +
+                          (tiles - 1 - tile) * cut * p.c.heads + h / p.group;
+    const int64_t pitch = (int64_t)p.c.heads * p.part_rows;
+    const int64_t at = first * p.part_rows + r % kPromptRows;
+    uint4 x[kPromptParts];
+#pragma unroll
+    for (int q = 0; q < kPromptParts; ++q) {
+      x[q] = make_uint4(0, 0, 0, 0);
+      if (in && q < parts) x[q] = ldg_cg_v4(p.parts + (at + q * pitch) * D + d);
+    }
+    float w = 0.0f, scale = 0.0f;       // of part `lane % L` of this lane's row
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t from = __shfl_sync(0xffffffffu, at, k * L);
+      const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
+      float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+      if (lane < count)
+        u = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (from + lane * pitch) * kPartWords));
+      float top = u.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
+      const float y = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
+      float sum = u.y * y;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float mine = __shfl_sync(0xffffffffu, y * pow2(max(__float_as_int(u.z) - e, -126)),
+                                     lane % L);
+      if (k == sub) {
+        w = mine;
+        scale = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
+      }
+    }
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kPromptParts; ++q) {
+      const float y = __shfl_sync(0xffffffffu, w, sub * L + q);
+      if (q < parts) {
+        v.x = fmaf(__uint_as_float(x[q].x), y, v.x);
+        v.y = fmaf(__uint_as_float(x[q].y), y, v.y);
+        v.z = fmaf(__uint_as_float(x[q].z), y, v.z);
+        v.w = fmaf(__uint_as_float(x[q].w), y, v.w);
+      }
+    }
+    if (in)
+      *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_out + (int64_t)h * D + d) =
+          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
+                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
   }
 }
 
@@ -404,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row0, n, kv, count = 0;
       if (b0 + lane < p.c.batch && sequence_of(p.c, b0 + lane, row0, n, kv) &&
           n * p.group > p.few_rows)
-        count = (n * p.group + 2 * kTile - 1) / (2 * kTile) * p.c.heads;
+        count = (n * p.group + 2 * kTile - 1) / (2 * kTile) * p.c.heads *
+                prompt_parts(n * p.group, kv, p.c.heads);
       int sum = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -415,11 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (hit) {
         const int l = __ffs(hit) - 1;
         if (lane == l) {
-          const int v = at - (sum - count);
-          const int row = (count / p.c.heads - 1 - v / p.c.heads) * 2 * kTile;
+          uint32_t v = at - (sum - count);
+          const int cut = prompt_parts(n * p.group, kv, p.c.heads);
+          const int first = b0 + l;
+          const int64_t slot =
+              big_place(p.big_by_row, first, row0, p.group) * kPromptItems + (int)v;
           Rows it;
-          it.b = b0 + l;
-          it.h = v % p.c.heads;
+          it.h = (int)next_digit(v, p.c.heads);
+          const int part = (int)next_digit(v, cut);
+          const int row = (count / p.c.heads / cut - 1 - (int)v) * 2 * kTile;
           it.row0 = row0;
           it.tok0 = row / p.group;
           it.rem = row % p.group;
@@ -427,9 +525,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.tiles = it.rows > kTile ? 2 : 1;
           it.low = kv - n + it.tok0;
           it.high = it.low + token_of(p, it.rem + it.rows - 1);
-          it.steps = it.high >= 0 ? it.high / kTile + 1 : 0;
+          const int len = prompt_len(kv, cut);
+          it.parts = prompt_seen(it.high, len);
+          it.step0 = part * len;
+          it.steps = max(0, min(it.high >= 0 ? it.high / kTile + 1 : 0, it.step0 + len) - it.step0);
+          it.part = slot * p.big_rows;
+          it.b = part < it.parts ? first : -1;
           s.it = it;
-          mbar_arrive_expect_tx(&s.q_raw, it.rows * D * 2);
+          if (it.b >= 0) mbar_arrive_expect_tx(&s.q_raw, it.rows * D * 2);
+          if (it.parts > 1) p.next[1] = 1;      // there are parts to join
         }
         found = b0 + l;
       }
@@ -437,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0 && found < 0) s.it.b = -1;
     __syncwarp();
-    if (found >= 0) {
+    if (s.it.b >= 0) {
       // the queries: the heads of one kv head lie together
       const int rem = s.it.rem, end = rem + s.it.rows;
       for (int tok = lane; tok * p.group < end; tok += 32) {
@@ -461,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int h = s.it.h, tiles = s.it.tiles, low = s.it.low, high = s.it.high, steps = s.it.steps;
+  const int tok0 = s.it.step0 * kTile;  // its first token
   const int half = (warp >> 2) & 1;
   const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;      // of warps 0-15
 
@@ -501,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = all_of(9 + t, ok);
       if (!ok) break;
       tc_fence_after();
-      const int t0 = j * kTile + half * kHalf;
+      const int t0 = tok0 + j * kTile + half * kHalf;
       // half a row's products, all in registers; columns that the row does not
       // see are -inf: in few steps, so the others have no look at them
       float v[kHalf];
@@ -607,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       // (first half) + (second half), for both the same
       l = s.most[steps & 1][0][my_row] + s.most[steps & 1][1][my_row];
-      store_results<D>(p, s, l, to);
+      store_results<D>(p, s, m, l, to);
     }
   } else if (warp < 16) {
     more_registers<96>();
@@ -630,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait<true>(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
                 wait<true>(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const int at = j * kTile + r, e = s.ve[in][r >> 4];
+      const int at = tok0 + j * kTile + r, e = s.ve[in][r >> 4];
       const uint8_t* src = raw + S::kV8 + st * S::kPart + r * D;
       uint8_t* dst = raw + S::kV16 + st * 2 * S::kPart + r * 128;
 #pragma unroll 1
@@ -689,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       const bool there = lane < 8 && s.ve[in][lane & 7] != kNoBlock;
       const int32_t page = s.page[in][lane & 7];
-      const int row = (j * kTile + (lane & 7) * kKvBlock) & ((1 << p.c.page_shift) - 1);
+      const int row = (tok0 + j * kTile + (lane & 7) * kKvBlock) & ((1 << p.c.page_shift) - 1);
       const uint32_t have = __ballot_sync(0xffffffffu, there);
       if (lane == 0) mbar_arrive(&s.info_empty[in]);
       ok = wait<true>(s, &s.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
@@ -729,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int expo = -1000;                   // E, the largest value scale so far
     if (lane == 0) s.top = expo;
     for (int j0 = 0; ok && j0 < steps; j0 += 4) {
-      const int tok = j0 * kTile + lane * kKvBlock;
+      const int tok = tok0 + j0 * kTile + lane * kKvBlock;
       bool there = tok <= high;
       int32_t page = 0;
       uint32_t kb = 127, vb = 0;
@@ -845,16 +950,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   const size_t smem = Smem<D>::kEnd + sizeof(Smem<D>);
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(prompt_kernel<D>), allowed);
   if (e != cudaSuccess) return e;
   // at most so many tiles: whole ones, and one more for each sequence that can
   // have more rows than the split kernel takes
   const int64_t rows = p.c.T * p.group;
   const int64_t seqs = rows / (p.few_rows + 1);
-  const int64_t tiles = rows / (2 * kTile) + (seqs < p.c.batch ? seqs : p.c.batch);
-  return launch_pdl(prompt_kernel<D>, dim3((unsigned)(tiles * p.c.heads)), dim3(kThreads), smem, st,
-                    p);
+  const int64_t some = seqs < p.c.batch ? seqs : p.c.batch;
+  int64_t items = (rows / (2 * kTile) + some) * p.c.heads;
+  // those that are cut have kPromptItems items at most
+  if (p.big_rows) items += some * kPromptItems;
+  e = launch_pdl(prompt_kernel<D>, dim3((unsigned)items), dim3(kThreads), smem, st, p);
+  if (e != cudaSuccess || !p.big_rows) return e;
+  AttnJoinParams j;
+  j.c = p.c;
+  j.out = p.out;
+  j.next = p.next;
+  j.parts = p.big;
+  j.part_ml = p.big_ml;
+  j.ld_out = p.ld_out;
+  j.group = p.group;
+  j.few_rows = p.few_rows;
+  j.part_rows = p.big_rows;
+  j.big_by_row = p.big_by_row;
+  return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)p.c.T), dim3(32 * kJoinWarps), 0, st, j);
 }
 
 }  // namespace

@@ -870,8 +870,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NT>::kBlocks)
 template <int D, int NT>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   const size_t smem = Smem<D, NT>::kRing + sizeof(Smem<D, NT>) + sizeof(int) * (size_t)p.c.batch;
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(split_kernel<D, NT>), allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(split_kernel<D, NT>, dim3(Smem<D, NT>::kBlocks * sm_count()), dim3(kThreads), smem,
                  st, p);

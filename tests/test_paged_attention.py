@@ -52,6 +52,40 @@ def test_long_contexts(kv):
     b.check(q, b.attend(q))
 
 
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (64, 9, 3), (128, 16, 1)])
+def test_few_blocks_over_long_contexts(D, hq, hkv):
+    """More than 64 rows a kv head, few blocks of them: a sequence's tokens are cut
+    into parts. Tiles that end before the last parts; parts of a step and a bit."""
+    need_gpu()
+    lengths = [(65, 3000), (1, 50), (300, 900), (20, 4097), (9, 5000), (100, 100), (130, 4000)]
+    b = Batch(lengths, hq, hkv, D, 32, seed=hq).fill()
+    q = b.rows(hq, 2.0).cuda()
+    args = b.device_args()
+    got = b.attend(q, args=args)
+    b.check(q, got)
+    assert torch.equal(got, rows_alone(b, q, args))
+
+
+def test_a_prompt_among_many_sequences():
+    """More sequences than can have over 64 rows."""
+    need_gpu()
+    lengths = [(1, 40)] * 60 + [(20, 2000)] + [(1, 300)] * 40 + [(17, 3000)]
+    b = Batch(lengths, 8, 2, 64, 32, seed=22).fill()
+    q = b.rows(8, 2.0)
+    b.check(q, b.attend(q))
+
+
+def test_nan_in_parts():
+    need_gpu()
+    b = Batch([(40, 3000), (30, 2500)], 4, 2, 128, 16, seed=23).fill()
+    b.codes[b.table[0, 2980 // 16], 1, 1, 2980 % 16, 37] = 0x7f        # seen by some rows
+    b.codes[b.table[1, 10], 1, 0, 3, 5] = 0xff                         # by all
+    q = b.rows(4)
+    out = b.check(q, b.attend(q))
+    assert np.isnan(out[20:40, 2, 37]).all() and not np.isnan(out[:20]).any()
+    assert np.isnan(out[40:, 0, 5]).all()
+
+
 def test_empty_sequences_and_rows_that_see_nothing():
     """No new tokens, no tokens at all, more new tokens than there are in all;
     rows of no sequence stay as they were."""
