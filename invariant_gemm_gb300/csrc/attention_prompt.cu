@@ -379,76 +379,77 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const AttnJoinParams p) {
   constexpr int L = D / 4, PER = 32 / L;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
-  const int t = blockIdx.x;
   griddep_wait();
   if (__ldcg(p.next + 1) == 0) return;  // no sequence was cut
-  int b = 0;
-  for (int hi = p.c.batch; hi - b > 1;) {       // the last sequence that starts at or before t
-    const int mid = (b + hi) >> 1;
-    if (__ldg(p.c.cu + mid) <= t) b = mid; else hi = mid;
-  }
-  int row0, n, kv;
-  if (!sequence_of(p.c, b, row0, n, kv) || t < row0 || t >= row0 + n || n * p.group <= p.few_rows)
-    return;
-  const int cut = prompt_parts(n * p.group, kv, p.c.heads);
-  if (cut == 1) return;
-  const int len = prompt_len(kv, cut), heads = p.c.heads * p.group, tok = t - row0;
-  const int tiles = (n * p.group + kPromptRows - 1) / kPromptRows;
-  for (int h0 = warp * PER; h0 < heads; h0 += kJoinWarps * PER) {
-    const int h = min(h0 + sub, heads - 1), r = tok * p.group + h % p.group;
-    const int tile = r / kPromptRows;
-    const int last = min((tile + 1) * kPromptRows, n * p.group) - 1;
-    const int parts = prompt_seen(kv - n + last / p.group, len);
-    const bool in = h0 + sub < heads && parts > 1;
-    // item (tiles - 1 - tile, part, kv head) of the sequence
-    const int64_t first = big_place(p.big_by_row, b, row0, p.group) * kPromptItems +
-                          (tiles - 1 - tile) * cut * p.c.heads + h / p.group;
-    const int64_t pitch = (int64_t)p.c.heads * p.part_rows;
-    const int64_t at = first * p.part_rows + r % kPromptRows;
-    uint4 x[kPromptParts];
-#pragma unroll
-    for (int q = 0; q < kPromptParts; ++q) {
-      x[q] = make_uint4(0, 0, 0, 0);
-      if (in && q < parts) x[q] = ldg_cg_v4(p.parts + (at + q * pitch) * D + d);
+  for (int t = blockIdx.x; t < p.c.T; t += gridDim.x) {
+    int b = 0;
+    for (int hi = p.c.batch; hi - b > 1;) {       // the last sequence that starts at or before t
+      const int mid = (b + hi) >> 1;
+      if (__ldg(p.c.cu + mid) <= t) b = mid; else hi = mid;
     }
-    float w = 0.0f, scale = 0.0f;       // of part `lane % L` of this lane's row
+    int row0, n, kv;
+    if (!sequence_of(p.c, b, row0, n, kv) || t < row0 || t >= row0 + n || n * p.group <= p.few_rows)
+      continue;
+    const int cut = prompt_parts(n * p.group, kv, p.c.heads);
+    if (cut == 1) continue;
+    const int len = prompt_len(kv, cut), heads = p.c.heads * p.group, tok = t - row0;
+    const int tiles = (n * p.group + kPromptRows - 1) / kPromptRows;
+    for (int h0 = warp * PER; h0 < heads; h0 += kJoinWarps * PER) {
+      const int h = min(h0 + sub, heads - 1), r = tok * p.group + h % p.group;
+      const int tile = r / kPromptRows;
+      const int last = min((tile + 1) * kPromptRows, n * p.group) - 1;
+      const int parts = prompt_seen(kv - n + last / p.group, len);
+      const bool in = h0 + sub < heads && parts > 1;
+      // item (tiles - 1 - tile, part, kv head) of the sequence
+      const int64_t first = big_place(p.big_by_row, b, row0, p.group) * kPromptItems +
+                            (tiles - 1 - tile) * cut * p.c.heads + h / p.group;
+      const int64_t pitch = (int64_t)p.c.heads * p.part_rows;
+      const int64_t at = first * p.part_rows + r % kPromptRows;
+      uint4 x[kPromptParts];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int64_t from = __shfl_sync(0xffffffffu, at, k * L);
-      const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
-      float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
-      if (lane < count)
-        u = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (from + lane * pitch) * kPartWords));
-      float top = u.x;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
-      const float y = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
-      float sum = u.y * y;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float mine = __shfl_sync(0xffffffffu, y * pow2(max(__float_as_int(u.z) - e, -126)),
-                                     lane % L);
-      if (k == sub) {
-        w = mine;
-        scale = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
+      for (int q = 0; q < kPromptParts; ++q) {
+        x[q] = make_uint4(0, 0, 0, 0);
+        if (in && q < parts) x[q] = ldg_cg_v4(p.parts + (at + q * pitch) * D + d);
       }
-    }
-    float4 v = make_float4(0, 0, 0, 0);
+      float w = 0.0f, scale = 0.0f;       // of part `lane % L` of this lane's row
 #pragma unroll
-    for (int q = 0; q < kPromptParts; ++q) {
-      const float y = __shfl_sync(0xffffffffu, w, sub * L + q);
-      if (q < parts) {
-        v.x = fmaf(__uint_as_float(x[q].x), y, v.x);
-        v.y = fmaf(__uint_as_float(x[q].y), y, v.y);
-        v.z = fmaf(__uint_as_float(x[q].z), y, v.z);
-        v.w = fmaf(__uint_as_float(x[q].w), y, v.w);
+      for (int k = 0; k < PER; ++k) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, k * L);
+        const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
+        float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+        if (lane < count)
+          u = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (from + lane * pitch) * kPartWords));
+        float top = u.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
+        const float y = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
+        float sum = u.y * y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float mine = __shfl_sync(0xffffffffu, y * pow2(max(__float_as_int(u.z) - e, -126)),
+                                       lane % L);
+        if (k == sub) {
+          w = mine;
+          scale = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
+        }
       }
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < kPromptParts; ++q) {
+        const float y = __shfl_sync(0xffffffffu, w, sub * L + q);
+        if (q < parts) {
+          v.x = fmaf(__uint_as_float(x[q].x), y, v.x);
+          v.y = fmaf(__uint_as_float(x[q].y), y, v.y);
+          v.z = fmaf(__uint_as_float(x[q].z), y, v.z);
+          v.w = fmaf(__uint_as_float(x[q].w), y, v.w);
+        }
+      }
+      if (in)
+        *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_out + (int64_t)h * D + d) =
+            make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
+                       f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
     }
-    if (in)
-      *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_out + (int64_t)h * D + d) =
-          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
-                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
   }
 }
 
@@ -577,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + lanes;
     const uint32_t to = tmem + 2 * kTile + t * D + half * (D / 2) + lanes;
-    const int tile_low = low + token_of(p, s.it.rem + t * kTile);
-    const int lim = my_row < s.it.rows ? low + token_of(p, s.it.rem + my_row)
+    // (tokens from the part's first on)
+    const int tile_low = low - tok0 + token_of(p, s.it.rem + t * kTile);
+    const int lim = my_row < s.it.rows ? low - tok0 + token_of(p, s.it.rem + my_row)
                                        : 0x7fffffff;                    // last token it sees
     const int pair_bar = 1 + t * 4 + (warp & 3);        // the two warps of these rows
     bool ok = all_of(9 + t, wait<true>(s, &s.q_raw, 0, p.c.status));
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = all_of(9 + t, ok);
       if (!ok) break;
       tc_fence_after();
-      const int t0 = tok0 + j * kTile + half * kHalf;
+      const int t0 = j * kTile + half * kHalf;
       // half a row's products, all in registers; columns that the row does not
       // see are -inf: in few steps, so the others have no look at them
       float v[kHalf];
@@ -728,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------------- values
     fewer_registers<48>();
     const int r = tid - 512;            // token of the step
+    const int lo = low - tok0, hi = high - tok0;        // from the part's first token on
     bool ok = wait<true>(s, &s.q_full, 0, p.c.status);  // the queries were where the values go
     for (int j = 0; j < steps; ++j) {
       const int in = j % kInfo, st = j & 1;
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait<true>(s, &s.v8_full[st], (j >> 1) & 1, p.c.status) &&
                 wait<true>(s, &s.v16_empty[st], ((j >> 1) & 1) ^ 1, p.c.status);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const int at = tok0 + j * kTile + r, e = s.ve[in][r >> 4];
+      const int at = j * kTile + r, e = s.ve[in][r >> 4];
       const uint8_t* src = raw + S::kV8 + st * S::kPart + r * D;
       uint8_t* dst = raw + S::kV16 + st * 2 * S::kPart + r * 128;
 #pragma unroll 1
@@ -748,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               src + (D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) * 16);
           u[4 * i] = x.x; u[4 * i + 1] = x.y; u[4 * i + 2] = x.z; u[4 * i + 3] = x.w;
         }
-        if (at > low || e >= kNaNExp) {
-          if (at > high || e == kNoBlock) {
+        if (at > lo || e >= kNaNExp) {
+          if (at > hi || e == kNoBlock) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) u[i] = 0;     // p is 0, but 0 times NaN is not
           } else {
@@ -758,10 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (e == kNaNExp) u[i] = 0x7f7f7f7fu;
               // seen by some rows only: a NaN is kept for those
               const uint32_t bad = ((u[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (at > low && bad) {
+              if (at > lo && bad) {
                 s.nans = 1;
                 for (int q = 0; q < 4; ++q)
-                  if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[64 * d + 4 * i + q], at);
+                  if (bad >> (8 * q + 7) & 1) atomicMin(&s.nan_at[64 * d + 4 * i + q], tok0 + at);
                 u[i] &= ~((bad >> 7) * 0xffu);
               }
             }
@@ -974,7 +977,9 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   j.few_rows = p.few_rows;
   j.part_rows = p.big_rows;
   j.big_by_row = p.big_by_row;
-  return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)p.c.T), dim3(32 * kJoinWarps), 0, st, j);
+  const int64_t most = 4 * sm_count();
+  return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)(p.c.T < most ? p.c.T : most)),
+                    dim3(32 * kJoinWarps), 0, st, j);
 }
 
 }  // namespace
