@@ -493,9 +493,9 @@ typedef struct ig_batch {
  * for the rot_dim / 2 pairs, with the cosines cos_sin[p][0 .. rot_dim/2) and the
  * sines cos_sin[p][rot_dim/2 .. rot_dim) of the token's position p
  * (cos_sin FP32 [table_rows][rot_dim], positions int32 [T]). q or k may be NULL,
- * with their outputs. q_out may be q and k_out may be k (same strides). A token whose position is
- * outside the table gets NaN, and ws records IG_ERR_INDEX_RANGE. w_q and w_k
- * are bf16 [head_dim]. */
+ * with their outputs. q_out may be q and k_out may be k (same strides). A token
+ * whose position is outside the table gets NaN, and ws records
+ * IG_ERR_INDEX_RANGE. w_q and w_k are bf16 [head_dim]. */
 int ig_qk_norm_rope(const ig_rope_shape* shape, const void* q, const void* k, const void* w_q,
                     const void* w_k, const float* cos_sin, const int32_t* positions, void* q_out,
                     void* k_out, void* ws, size_t ws_bytes, void* stream);
@@ -508,7 +508,9 @@ int ig_qk_norm_rope(const ig_rope_shape* shape, const void* q, const void* k, co
  * least their scale, and where it grew they are divided by as much. Values are
  * rounded to nearest, ties to even; what is not finite is held as NaN. Rows of
  * the block behind the last token keep their bytes.
- * Two sequences of a call must not share a block that one of them writes.
+ * A block that is written must be one token range of one sequence: not shared
+ * by two sequences, nor on a page that the page table names twice (its bytes are
+ * unspecified otherwise; pages that are only read may be shared freely).
  * Tokens appended one by one and together get the same scales, and the same
  * codes but for values under 2^-6 scale, which a growing scale rounds again.
  * k and v have batch->cu's rows of shape->T; ld_k is the stride of k. */
@@ -541,7 +543,9 @@ typedef struct ig_attn_shape {
 
 /* Bytes of workspace of ig_paged_attention for these sizes (of batch: batch,
  * max_q and ld_table; of cache: page, heads and head_dim); 0 for invalid ones.
- * Zeroed once after it is allocated; calls that may overlap need one each. */
+ * Zeroed once after it is allocated; calls that may overlap, captured ones too,
+ * need one each. The library's other calls may share it where they do not overlap;
+ * a token map in it does not outlive ig_paged_attention. */
 size_t ig_attention_workspace_bytes(const ig_attn_shape* shape, const ig_kv_cache* cache,
                                     const ig_batch* batch);
 
@@ -550,7 +554,10 @@ size_t ig_attention_workspace_bytes(const ig_attn_shape* shape, const ig_kv_cach
  * over the tokens j <= kv_len - rows + i for row i of a sequence's `rows`. Rows
  * that see no token (rows > kv_len) are 0. Products of the held values in
  * the tensor cores with FP32 sums, softmax in FP32; p is rounded to 11 bits for
- * the product with v. out may not be q. */
+ * the product with v. A sequence of at most 64 rows a kv head (rows times heads_q
+ * / heads) is one kernel's, of more another's, which takes the values of a query
+ * under 2^-9 of its largest to within 2^-17 of it. out may not be q, nor overlap
+ * what the call reads. */
 int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
                        const ig_batch* batch, const void* q, void* out, void* ws,
                        size_t ws_bytes, void* stream);

@@ -140,7 +140,7 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
 }
 
 // What the workspace of an attention call holds behind the status word and the
-// counters (of which it uses one).
+// counters (of which it uses two).
 struct AttnPlan {
   int group, max_tiles, max_parts, part_rows;
   int big_rows, big_by_row;
@@ -182,6 +182,10 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
     pl->big_rows = (int)(rows < kPromptRows ? rows : kPromptRows);
     big = (pl->big_by_row ? places : b->batch) * kPromptItems * pl->big_rows;
   }
+  // (blocks of the prompt kernel: as its launch counts them)
+  const int64_t many = s->T * pl->group;
+  if ((many / kPromptRows + b->batch) * c->heads + (int64_t)b->batch * kPromptItems >= 1ll << 31)
+    return IG_ERR_UNSUPPORTED;
   pl->big_ml_at = align_up(pl->big_at + (size_t)big * c->head_dim * 4, 256);
   pl->total = kMapOffset + pl->big_ml_at + (size_t)big * kPartWords * 4;
   return IG_OK;

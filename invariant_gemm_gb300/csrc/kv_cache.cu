@@ -270,6 +270,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
     *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.b) = q.y;
   }
   if (warp != 0) return;
+  __syncwarp();                         // every lane has read the scale that was
   if (older && byte > was && byte < 255) {
     // the older tokens by the grown scale
     const float less = pow2(max(was - byte, -126));
