@@ -543,6 +543,7 @@ typedef struct ig_attn_shape {
 
 /* Bytes of workspace of ig_paged_attention for these sizes (of batch: batch,
  * max_q and ld_table; of cache: page, heads and head_dim); 0 for invalid ones.
+ * Enough for every call with fewer tokens, sequences, pages or a smaller max_q.
  * Zeroed once after it is allocated; calls that may overlap, captured ones too,
  * need one each. The library's other calls may share it where they do not overlap;
  * a token map in it does not outlive ig_paged_attention. */
