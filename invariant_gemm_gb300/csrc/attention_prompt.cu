@@ -179,27 +179,6 @@ __device__ __forceinline__ float factor(float f, float ks) {
   const float k = f * ks;
   return k < 1.18e-38f ? 1.18e-38f : k;
 }
-// Pairs of FP32 values: one instruction for both.
-__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 split2(uint64_t a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // A warpgroup's share of the block's registers (768 threads launched with 80).
 template <int N>
 __device__ __forceinline__ void more_registers() {

@@ -25,69 +25,111 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int l) {
   return {4 * l, (p.rot >> 1) + 4 * l, 4 * l};
 }
 
-struct Angles {
-  float4 c, s;
+// A lane's eight values as pairs: x[0], x[1] the first group, x[2], x[3] the second.
+struct Values {
+  uint64_t x[4];
 };
 
-__device__ __forceinline__ Angles load_angles(const RopeParams& p, int64_t pos, int pair) {
-  const float* row = p.cos_sin + pos * p.rot;
-  return {__ldg(reinterpret_cast<const float4*>(row + pair)),
-          __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + pair))};
+__device__ __forceinline__ uint64_t bf16x2_to_pair(uint32_t u) {
+  return pair2(bf16lo(u), bf16hi(u));
+}
+__device__ __forceinline__ Values unpack(uint2 a, uint2 b) {
+  return {{bf16x2_to_pair(a.x), bf16x2_to_pair(a.y), bf16x2_to_pair(b.x), bf16x2_to_pair(b.y)}};
+}
+__device__ __forceinline__ uint32_t pair_to_bf16x2(uint64_t v) {
+  const float2 f = split2(v);
+  return f32x2_to_bf16x2_bits(f.x, f.y);
 }
 
-__device__ __forceinline__ void unpack4(uint2 u, float* f) {
-  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-}
-__device__ __forceinline__ uint2 pack4(const float* f) {
-  return make_uint2(f32x2_to_bf16x2_bits(f[0], f[1]), f32x2_to_bf16x2_bits(f[2], f[3]));
-}
+// What a head's norm weights w and its token's rotation do to a lane's values:
+// y[i] = x[i] same[i] + partner(x)[i] other[i], with 1 / rms left to multiply. The
+// products of w with cosines and sines are made once for all heads of a token.
+struct Turn {
+  uint64_t same[4], other[4];
+};
 
-// Norm (the lane's own: w its 8 weights; others of the warp may have one where it
-// has none) and rotation of the head that D / 8 lanes hold. Every lane of the warp
-// takes part.
-template <int D, bool INTER>
-__device__ __forceinline__ void norm_rotate(const RopeParams& p, bool any, bool mine,
-                                            const float (&w)[8], bool turned, const Angles& t,
-                                            float (&f)[8]) {
-  constexpr int L = D / 8;
-  if (any) {
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s0 = fmaf(f[i], f[i], s0);
-      s1 = fmaf(f[i + 1], f[i + 1], s1);
-    }
-    float ss = s0 + s1;
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = mine ? rsqrtf(fmaf(ss, 1.0f / D, p.eps)) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * w[i];
-  }
-  if (turned) {
-    const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int one = INTER ? 2 * i : i, two = INTER ? 2 * i + 1 : i + 4;
-      const float x1 = f[one], x2 = f[two];
-      f[one] = fmaf(-x2, s[i], x1 * c[i]);
-      f[two] = fmaf(x1, s[i], x2 * c[i]);
-    }
-  }
+// The value that turns with each: of the other group, or the neighbour.
+template <bool INTER>
+__device__ __forceinline__ uint64_t partner(const Values& v, int i) {
+  if (!INTER) return v.x[i ^ 2];
+  const float2 f = split2(v.x[i]);
+  return pair2(f.y, f.x);
 }
 
 // Weights of the lane's values, 1 where there are none.
-__device__ __forceinline__ void load_weight(const RopeParams& p, const __nv_bfloat16* w,
-                                            const Place& at, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-  if (!w) return;
-  unpack4(__ldg(reinterpret_cast<const uint2*>(w + at.a)), f);
-  unpack4(__ldg(reinterpret_cast<const uint2*>(w + at.b)), f + 4);
+__device__ __forceinline__ Values load_weight(const RopeParams& p, const __nv_bfloat16* w,
+                                              const Place& at) {
+  const uint64_t one = pair2(1.0f, 1.0f);
+  if (!w) return {{one, one, one, one}};
+  Values v = unpack(__ldg(reinterpret_cast<const uint2*>(w + at.a)),
+                    __ldg(reinterpret_cast<const uint2*>(w + at.b)));
   if (p.plus_one) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += 1.0f;
+    for (int i = 0; i < 4; ++i) v.x[i] = add2(v.x[i], one);
   }
+  return v;
+}
+
+// Row `pos` of the table, with the weights; where the lane's values are not rotated
+// (`other` is not looked at) the weights alone.
+template <bool INTER>
+__device__ __forceinline__ Turn turn_of(const RopeParams& p, const Values& w, const Place& at,
+                                        bool turned, int64_t pos) {
+  Turn t = {};
+  if (!turned) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.same[i] = w.x[i];
+    return t;
+  }
+  const float* row = p.cos_sin + pos * p.rot;
+  const float4 c = __ldg(reinterpret_cast<const float4*>(row + at.pair));
+  const float4 s = __ldg(reinterpret_cast<const float4*>(row + (p.rot >> 1) + at.pair));
+  if (INTER) {
+    const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.same[i] = mul2(w.x[i], pair2(cs[i], cs[i]));
+      t.other[i] = mul2(partner<true>(w, i), pair2(-sn[i], sn[i]));
+    }
+  } else {
+    const uint64_t cs[2] = {pair2(c.x, c.y), pair2(c.z, c.w)};
+    const uint64_t sn[2] = {pair2(s.x, s.y), pair2(s.z, s.w)};
+    const uint64_t neg[2] = {pair2(-s.x, -s.y), pair2(-s.z, -s.w)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.same[i] = mul2(w.x[i], cs[i & 1]);
+      t.other[i] = mul2(w.x[i ^ 2], i < 2 ? neg[i] : sn[i & 1]);
+    }
+  }
+  return t;
+}
+
+// Norm (where there is one) and rotation of the head that D / 8 lanes hold. Every
+// lane of the warp takes part.
+template <int D, bool INTER>
+__device__ __forceinline__ Values norm_rotate(const RopeParams& p, bool norm, bool turned,
+                                              const Turn& t, const Values& v) {
+  constexpr int L = D / 8;
+  Values y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y.x[i] = mul2(v.x[i], t.same[i]);
+  if (turned) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.x[i] = fma2(partner<INTER>(v, i), t.other[i], y.x[i]);
+  }
+  if (norm) {
+    uint64_t sq = mul2(v.x[0], v.x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sq = fma2(v.x[i], v.x[i], sq);
+    const float2 both = split2(sq);
+    float ss = both.x + both.y;
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float inv = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.x[i] = mul2(y.x[i], pair2(inv, inv));
+  }
+  return y;
 }
 
 // Position of a token; false where the table does not have it.
@@ -97,58 +139,51 @@ __device__ __forceinline__ bool in_table(const RopeParams& p, int64_t pos) {
   return ok;
 }
 
-// Heads first .. first + PASSES * (256 / D) - 1 of token t, of the heads of q
-// and then of k, into q_out and k_out by one warp; pos(): the token's position,
-// asked for where there is a rotation, behind the loads of the heads.
+// Warps that the heads of a token take: those of q and of k have their own, so that
+// a warp has one pointer and one set of weights.
+template <int PER>
+__host__ __device__ __forceinline__ uint32_t chunks_of(const RopeParams& p) {
+  return (uint32_t)((p.heads_q + PER - 1) / PER + (p.heads_k + PER - 1) / PER);
+}
+
+// PASSES * (256 / D) heads of token t, the chunk's, of q or k into q_out or k_out by
+// one warp; pos(): the token's position, asked for where there is a rotation, behind
+// the loads of the heads.
 template <int D, bool INTER, int PASSES, typename Pos>
-__device__ __forceinline__ void heads_of_token(const RopeParams& p, int64_t t, int first, Pos pos) {
+__device__ __forceinline__ void heads_of_token(const RopeParams& p, int64_t t, int chunk, Pos pos) {
   constexpr int L = D / 8, PER = 32 / L;
   const int lane = threadIdx.x & 31, l = lane % L;
   const Place at = place_of<INTER>(p, l);
-  const int heads = p.heads_q + p.heads_k;
+  const int chunks_q = (p.heads_q + PASSES * PER - 1) / (PASSES * PER);
+  const bool is_q = chunk < chunks_q;
+  const int first = (is_q ? chunk : chunk - chunks_q) * (PASSES * PER) + lane / L;
+  const int heads = is_q ? p.heads_q : p.heads_k;
+  const __nv_bfloat16* x = (is_q ? p.q + t * p.ld_q : p.k + t * p.ld_k) + first * D;
+  __nv_bfloat16* y = (is_q ? p.q_out + t * p.ld_qo : p.k_out + t * p.ld_ko) + first * D;
+  const __nv_bfloat16* weight = is_q ? p.w_q : p.w_k;
   uint2 raw[PASSES][2];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const int h = first + i * PER + lane / L;
     raw[i][0] = raw[i][1] = make_uint2(0, 0);
-    if (h < heads) {
-      const __nv_bfloat16* x = h < p.heads_q
-                                   ? p.q + t * p.ld_q + (int64_t)h * D
-                                   : p.k + t * p.ld_k + (int64_t)(h - p.heads_q) * D;
-      raw[i][0] = *reinterpret_cast<const uint2*>(x + at.a);
-      raw[i][1] = *reinterpret_cast<const uint2*>(x + at.b);
+    if (first + i * PER < heads) {
+      raw[i][0] = *reinterpret_cast<const uint2*>(x + i * PER * D + at.a);
+      raw[i][1] = *reinterpret_cast<const uint2*>(x + i * PER * D + at.b);
     }
   }
-  Angles angles = {};
-  bool bad = false, turned = false;
-  if (p.cos_sin) {
-    const int64_t row = pos();
-    bad = !in_table(p, row);
-    turned = !bad && at.pair >= 0;
-    if (turned) angles = load_angles(p, row, at.pair);
-  }
-  float wq[8], wk[8];
-  load_weight(p, p.w_q, at, wq);
-  load_weight(p, p.w_k, at, wk);
-  const bool any = p.w_q || p.w_k;
+  const Values w = load_weight(p, weight, at);
+  const int64_t row = p.cos_sin ? pos() : 0;
+  const bool bad = p.cos_sin && !in_table(p, row), turned = p.cos_sin && !bad && at.pair >= 0;
+  const Turn turn = turn_of<INTER>(p, w, at, turned, row);
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    if (first + i * PER >= heads) break;
-    const int h = first + i * PER + lane / L;
-    const bool is_q = h < p.heads_q;
-    float f[8], w[8];
-    unpack4(raw[i][0], f);
-    unpack4(raw[i][1], f + 4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = is_q ? wq[j] : wk[j];
-    norm_rotate<D, INTER>(p, any, is_q ? p.w_q != nullptr : p.w_k != nullptr, w, turned, angles, f);
-    uint2 o0 = pack4(f), o1 = pack4(f + 4);
+    const Values v = norm_rotate<D, INTER>(p, weight != nullptr, turned, turn,
+                                           unpack(raw[i][0], raw[i][1]));
+    uint2 o0 = make_uint2(pair_to_bf16x2(v.x[0]), pair_to_bf16x2(v.x[1]));
+    uint2 o1 = make_uint2(pair_to_bf16x2(v.x[2]), pair_to_bf16x2(v.x[3]));
     if (bad) o0 = o1 = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-    if (h < heads) {
-      __nv_bfloat16* y = is_q ? p.q_out + t * p.ld_qo + (int64_t)h * D
-                              : p.k_out + t * p.ld_ko + (int64_t)(h - p.heads_q) * D;
-      *reinterpret_cast<uint2*>(y + at.a) = o0;
-      *reinterpret_cast<uint2*>(y + at.b) = o1;
+    if (first + i * PER < heads) {
+      *reinterpret_cast<uint2*>(y + i * PER * D + at.a) = o0;
+      *reinterpret_cast<uint2*>(y + i * PER * D + at.b) = o1;
     }
   }
 }
@@ -157,14 +192,14 @@ constexpr int kWarps = 4;               // of a block of these kernels
 
 template <int D, bool INTER, int PASSES>
 __global__ void __launch_bounds__(32 * kWarps) qk_kernel(RopeParams p) {
-  constexpr int PER = PASSES * 256 / D;
-  const int chunks = (p.heads_q + p.heads_k + PER - 1) / PER;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = item / chunks;
+  // (below 2^32: at most half as many as there are heads of tokens, and one a token)
+  const uint32_t chunks = chunks_of<PASSES * 256 / D>(p);
+  uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int chunk = (int)next_digit(item, chunks);
   griddep_wait();
-  if (t >= p.T) return;
-  heads_of_token<D, INTER, PASSES>(p, t, (int)(item - t * chunks) * PER,
-                                   [&] { return (int64_t)__ldg(p.positions + t); });
+  if (item >= p.T) return;
+  heads_of_token<D, INTER, PASSES>(p, item, chunk,
+                                   [&] { return (int64_t)__ldg(p.positions + item); });
 }
 
 // One block of 16 tokens of one head and side, by W warps (of one thread block where
@@ -193,22 +228,14 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
   const __nv_bfloat16* src = (side ? p.v : p.r.k) + (int64_t)h * D;
   const int64_t ld = side ? p.ld_v : p.r.ld_k;
   uint2 raw[PASSES][2];
-  Angles angles[PASSES];
-  bool bad[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int pos = begin + i * PER;
     raw[i][0] = raw[i][1] = make_uint2(0, 0);
-    bad[i] = false;
     if (pos < end) {
       const int64_t t = row0 + pos - first;
       raw[i][0] = *reinterpret_cast<const uint2*>(src + t * ld + at.a);
       raw[i][1] = *reinterpret_cast<const uint2*>(src + t * ld + at.b);
-      if (side == 0 && p.r.cos_sin) {
-        const int64_t row = p.r.positions ? (int64_t)__ldg(p.r.positions + t) : (int64_t)pos;
-        bad[i] = !in_table(p.r, row);
-        if (!bad[i] && at.pair >= 0) angles[i] = load_angles(p.r, row, at.pair);
-      }
     }
   }
   const bool there = page >= 0 && page < c.pages;
@@ -218,34 +245,66 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
   uint8_t* scale = c.scales + page * c.scale_stride + head / kKvBlock;
   const bool older = start < first;
   const int was = older && there ? *scale : 0;
-  float w[8];
-  load_weight(p.r, side == 0 ? p.r.w_k : nullptr, at, w);
-  const bool norm = side == 0 && p.r.w_k;
-  float f[PASSES][8], top = 0.0f;
+  Values f[PASSES];
+  float top = 0.0f;                     // largest magnitude, infinity among them, NaN not
+  if (side == 0) {
+    const Values w = load_weight(p.r, p.r.w_k, at);
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const bool mine = begin + i * PER < end;
-    unpack4(raw[i][0], f[i]);
-    unpack4(raw[i][1], f[i] + 4);
-    norm_rotate<D, INTER>(p.r, norm, norm, w,
-                          side == 0 && p.r.cos_sin && mine && !bad[i] && at.pair >= 0, angles[i],
-                          f[i]);
-    if (mine) {
+    for (int i = 0; i < PASSES; ++i) {
+      const int pos = begin + i * PER;
+      bool bad = false;
+      int64_t row = pos;
+      if (p.r.cos_sin && pos < end) {
+        if (p.r.positions) row = __ldg(p.r.positions + row0 + pos - first);
+        bad = !in_table(p.r, row);
+      }
+      const bool turned = p.r.cos_sin && pos < end && !bad && at.pair >= 0;
+      f[i] = norm_rotate<D, INTER>(p.r, p.r.w_k != nullptr, turned,
+                                   turn_of<INTER>(p.r, w, at, turned, row),
+                                   unpack(raw[i][0], raw[i][1]));
+      if (bad) {
+        const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (bad[i]) f[i][j] = __uint_as_float(0x7fc00000u);
-        const float m = fabsf(f[i][j]);
-        if (m < __uint_as_float(0x7f800000u)) top = fmaxf(top, m);
+        for (int j = 0; j < 4; ++j) f[i].x[j] = pair2(nan, nan);
       }
     }
-  }
-  // (no value is negative, so whole numbers compare as they do)
-  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  if constexpr (W > 1) {
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
+  } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) top = fmaxf(top, tops[i]);
+    for (int i = 0; i < PASSES; ++i) f[i] = unpack(raw[i][0], raw[i][1]);
+  }
+  auto largest = [&] {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = split2(f[i].x[j]);
+        m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+    // (no value is negative, so whole numbers compare as they do)
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if constexpr (W > 1) {
+      if (lane == 0) tops[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = fmaxf(m, tops[i]);
+    }
+    return m;
+  };
+  top = largest();
+  if (top == __uint_as_float(0x7f800000u)) {
+    // what is not finite is held as NaN, and has no say in the scale
+    if constexpr (W > 1) __syncthreads();       // the warps' maxima are read
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 x = split2(f[i].x[j]);
+        if (fabsf(x.x) == top) x.x = __uint_as_float(0x7fc00000u);
+        if (fabsf(x.y) == top) x.y = __uint_as_float(0x7fc00000u);
+        f[i].x[j] = pair2(x.x, x.y);
+      }
+    top = largest();
   }
   if (!there) {
     if (lane == 0) atomicOr(c.status, kStatusIndexRange);
@@ -260,14 +319,14 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
   for (int i = 0; i < PASSES; ++i) {
     const int pos = begin + i * PER;
     if (pos >= end) continue;
-    float g[8];
+    uint32_t q[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      g[j] = fabsf(f[i][j]) < __uint_as_float(0x7f800000u) ? f[i][j] * down
-                                                          : __uint_as_float(0x7fc00000u);
-    const uint2 q = e4m3_encode8(g);
-    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.a) = q.x;
-    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.b) = q.y;
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = split2(mul2(f[i].x[j], pair2(down, down)));
+      q[j] = f32x2_to_e4m3x2(x.x, x.y);
+    }
+    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.a) = q[0] | q[1] << 16;
+    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.b) = q[2] | q[3] << 16;
   }
   if (warp != 0) return;
   __syncwarp();                         // every lane has read the scale that was
@@ -317,15 +376,14 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
     if ((int)item < p.c.batch) append_block<D, INTER, W>(p, (int)item, blk, h, side, tops);
     return;
   }
-  const int64_t item = (int64_t)(blockIdx.x - kv_blocks) * kWarps + (threadIdx.x >> 5);
-  const int chunks = (p.r.heads_q + PER - 1) / PER;
-  const int64_t t = item / chunks;
+  uint32_t t = (blockIdx.x - kv_blocks) * kWarps + (threadIdx.x >> 5);
+  const int chunk = (int)next_digit(t, chunks_of<PER>(p.r));
   if (t >= p.r.T) return;
   const int b = sequence_at(p.c.cu, p.c.batch, t);
   int row0, n, kv;
-  if (!sequence_of(p.c, b, row0, n, kv) || t < row0 || t >= row0 + n) return;
-  heads_of_token<D, INTER, PASSES>(p.r, t, (int)(item - t * chunks) * PER, [&] {
-    return p.r.positions ? (int64_t)__ldg(p.r.positions + t) : (int64_t)kv - n + (t - row0);
+  if (!sequence_of(p.c, b, row0, n, kv) || (int)t < row0 || (int)t >= row0 + n) return;
+  heads_of_token<D, INTER, PASSES>(p.r, t, chunk, [&] {
+    return p.r.positions ? (int64_t)__ldg(p.r.positions + t) : (int64_t)kv - n + ((int)t - row0);
   });
 }
 
@@ -386,8 +444,9 @@ __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const GatherParams 
         e4m3_decode8(j ? make_uint2(raw[k].z, raw[k].w) : make_uint2(raw[k].x, raw[k].y), f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[q] *= scale;
-        const uint2 lo = pack4(f), hi = pack4(f + 4);
-        *(reinterpret_cast<uint4*>(out) + 2 * (i % L) + j) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        *(reinterpret_cast<uint4*>(out) + 2 * (i % L) + j) =
+            make_uint4(f32x2_to_bf16x2_bits(f[0], f[1]), f32x2_to_bf16x2_bits(f[2], f[3]),
+                       f32x2_to_bf16x2_bits(f[4], f[5]), f32x2_to_bf16x2_bits(f[6], f[7]));
       }
     }
   }
@@ -404,8 +463,8 @@ cudaError_t qk(const RopeParams& p, cudaStream_t st) {
   const bool many = p.T * ((heads + PER - 1) / PER) > 64 * (int64_t)sm_count();
   auto go = [&](auto kern, int passes) {
     const int per = passes * PER;
-    return launch_pdl(kern, dim3(blocks_of(p.T * ((heads + per - 1) / per))), dim3(32 * kWarps), 0,
-                      st, p);
+    const int64_t chunks = (p.heads_q + per - 1) / per + (p.heads_k + per - 1) / per;
+    return launch_pdl(kern, dim3(blocks_of(p.T * chunks)), dim3(32 * kWarps), 0, st, p);
   };
   if (p.interleaved) return many ? go(qk_kernel<D, true, 4>, 4) : go(qk_kernel<D, true, 1>, 1);
   return many ? go(qk_kernel<D, false, 4>, 4) : go(qk_kernel<D, false, 1>, 1);
