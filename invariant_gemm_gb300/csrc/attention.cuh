@@ -78,6 +78,7 @@ struct AttnParams {
   int32_t max_tiles;    // 16-row tiles of such a sequence
   int32_t max_parts, part_rows;
   int32_t flags;
+  int32_t after_prompt; // the split kernel runs beside the prompt kernel and ends behind it
   float scale_log2;     // scale * log2(e)
 };
 
@@ -94,8 +95,14 @@ struct AttnJoinParams {
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_kv_append(const AppendParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_kv_gather(const GatherParams& p, int head_dim, cudaStream_t st);
-cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st);
+// Attention, in this order: the prompt kernel (where a sequence can have many rows), the
+// split kernel, the prompt kernel's join (where it can cut a sequence), the split
+// kernel's. The first lets the second start with its own last blocks; the second does
+// not end before the first has; the joins wait for what is before them.
 cudaError_t launch_attention_prompt(const AttnParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attention_prompt_join(const AttnParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attention_join(const AttnParams& p, int head_dim, cudaStream_t st);
 
 // {D, rows of a page, pages} of codes; box {D, 16, 1}, rows of 128 or 64 bytes
 // swizzled by as much. IG_OK or IG_ERR_CUDA.

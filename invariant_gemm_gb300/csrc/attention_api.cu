@@ -324,11 +324,13 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.flags = shape->flags;
   p.scale_log2 = shape->scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((int64_t)batch->max_q * pl.group > kFewRows && shape->T * pl.group > kFewRows) {
-    const cudaError_t e = launch_attention_prompt(p, cache->head_dim, st);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
-  return cuda_status(launch_attention_split(p, cache->head_dim, st));
+  const int D = cache->head_dim;
+  p.after_prompt = (int64_t)batch->max_q * pl.group > kFewRows && shape->T * pl.group > kFewRows;
+  cudaError_t e = p.after_prompt ? launch_attention_prompt(p, D, st) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_attention_split(p, D, st);
+  if (e == cudaSuccess && p.big_rows) e = launch_attention_prompt_join(p, D, st);
+  if (e == cudaSuccess) e = launch_attention_join(p, D, st);
+  return cuda_status(e);
 }
 
 }  // extern "C"

@@ -41,7 +41,8 @@ constexpr int kInfo = 8;                // steps whose pages and scales are held
 struct Rows {
   int b, h, row0;              // sequence, kv head, the sequence's first row of q
   int tok0, rem;               // its token and query head that the block's first row is
-  int rows, tiles;
+  int rows;
+  bool twin;                   // one tile of rows: the two take its steps in turn
   int low, high;               // last token that the first and the last row see
   int step0, steps;            // its steps: of the part of the tokens that is its
   int parts;                   // parts that the rows see; with several the results go to
@@ -65,9 +66,10 @@ struct Smem {
   int page[kInfo][8];
   int partly[kInfo];                    // some block of the step is not there
   float less[kInfo];                    // 2^(E before - E) of the step
-  int top;                              // E in the end
+  int top[2];                           // E in the end, of the even and the odd steps
   int nan_at[D], nans;                  // first NaN token of each value; whether there is one
   float most[2][2][2 * kTile];          // [step % 2][half][row]: largest logit, sum
+  float base[2 * kTile];                // m in the end
   uint32_t tmem;
   int dead;
   Rows it;
@@ -87,6 +89,17 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_minus(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -232,13 +245,14 @@ __device__ __forceinline__ bool wait(S& s, uint64_t* bar, uint32_t parity, uint3
   return true;
 }
 
-// Barrier of a tile's eight warps; whether all came with true.
+// Barrier of a tile's eight warps (or of both tiles'); whether all came with true.
+template <int N = 256>
 __device__ __forceinline__ bool all_of(int bar, bool mine) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, %2, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(all) : "r"((uint32_t)mine), "r"(bar) : "memory");
+      "bar.red.and.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all) : "r"((uint32_t)mine), "r"(bar), "n"(N) : "memory");
   return all != 0;
 }
 
@@ -260,8 +274,10 @@ __device__ __noinline__ float convert_queries(const AttnParams& p, Smem<D>& s, u
   constexpr int CH = D / 16;            // 16-byte chunks of half a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = warp >> 3, half = (warp >> 2) & 1, ch = lane % CH;
-  const int warp_row = t * kTile + (warp & 3) * 32, rows = s.it.rows;
-  const uint8_t* from = raw + S::kV16 + half * D + ch * 16;
+  const int warp_row = t * kTile + (warp & 3) * 32;
+  // (the two tiles have the same rows where they take turns)
+  const int same = s.it.twin ? t * kTile : 0, rows = s.it.rows + same;
+  const uint8_t* from = raw + S::kV16 + half * D + ch * 16 - same * 2 * D;
 #pragma unroll 2
   for (int r = warp_row + lane / CH; r < warp_row + 32; r += 32 / CH) {
     const uint4 w = *reinterpret_cast<const uint4*>(from + r * 2 * D);
@@ -285,69 +301,117 @@ __device__ __noinline__ float convert_queries(const AttnParams& p, Smem<D>& s, u
     const int e = exponent(r);
     float up = e == 255 ? qnan() : pow2(134 - max(e, 20));
     if (p.scale_log2 < 0.0f) up = -up;
-    float x[8], y[8];
-    unpack8(w, x);
+    // (as FP16 it loses what is under 2^-32 of the row's largest)
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] *= up;
-    const uint2 hi = e4m3_encode8(x);
-    e4m3_decode8(hi, y);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = split2(mul2(pair2(bf16lo(u[k]), bf16hi(u[k])), pair2(up, up)));
+      const uint32_t h = f16x2_of(x.x, x.y);
+      hi[k] = f16x2_to_e4m3x2(h);
+      lo[k] = f16x2_to_e4m3x2(f16x2_minus(h, e4m3x2_to_f16x2((uint16_t)hi[k])));
+    }
     const int c16 = half * (D / 32) + ch / 2;           // 16-byte chunk of a row of codes
     const int at = (D == 128 ? c16 ^ (r & 7) : c16 ^ ((r >> 1) & 3)) * 16 + (ch & 1) * 8;
     uint8_t* dst = raw + S::kQ + t * 2 * S::kPart + (r & 127) * D + at;
-    *reinterpret_cast<uint2*>(dst) = hi;
-    *reinterpret_cast<uint2*>(dst + S::kPart) = e4m3_encode8(y);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>(dst + S::kPart) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
   }
   const int e = exponent(warp_row + lane);
   return fabsf(p.scale_log2) * (e == 255 ? 1.0f : pow2(max(e, 20) - 134));
 }
 
-// Half a row of the results, l the sum of its p: into the output or, of one part of
-// several, as it stands into the workspace.
+// What a thread has of the results, half a row (of two tiles that took turns over the
+// same row a quarter, and both their sums): into the output or, of one part of
+// several, as it stands into the workspace. m, l: maximum and sum of p of its tile.
 template <int D>
-__device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, float m, float l,
-                                           uint32_t to) {
+__device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, uint8_t* raw,
+                                           float m, float l, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = (warp >> 2) & 1;
-  const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;
   const Rows& it = s.it;
-  const int tok = token_of(p, it.rem + my_row);
-  const bool in = my_row < it.rows, whole = it.parts == 1;
-  uint4* dst = reinterpret_cast<uint4*>(
-      p.out + (int64_t)(it.row0 + it.tok0 + tok) * p.ld_out +
-      (int64_t)(it.h * p.group + it.rem + my_row - tok * p.group) * D + half * (D / 2));
-  float4* part = reinterpret_cast<float4*>(p.big + (it.part + my_row) * D + half * (D / 2));
-  const int expo = s.top, lim = it.low + tok;
+  const bool twin = it.twin;
+  const int t = warp >> 3, local = (warp & 3) * 32 + lane, my_row = twin ? local : t * kTile + local;
+  const int first = twin ? (2 * t + half) * (D / 4) : half * (D / 2), count = twin ? D / 4 : D / 2;
+  int expo = s.top[1];
+  float w0 = 1.0f, w1 = 0.0f;
+  uint32_t from = tmem + 2 * kTile + ((uint32_t)((warp & 3) * 32) << 16) + first;
+  if (!twin) {
+    from += t * D;
+    if (it.steps & 1) expo = s.top[0];
+  } else {
+    const float m0 = s.base[local], m1 = s.base[kTile + local];
+    const float l0 = s.most[1][0][local] + s.most[1][1][local];
+    const float l1 = s.most[1][0][kTile + local] + s.most[1][1][kTile + local];
+    const int e0 = s.top[0], e1 = s.top[1];
+    m = fmaxf(m0, m1);
+    expo = max(e0, e1);
+    const float y0 = m0 == neg_inf() ? 1.0f : pow2_down(m0 - m);
+    const float y1 = m1 == neg_inf() ? 1.0f : pow2_down(m1 - m);
+    l = l0 * y0 + l1 * y1;
+    w0 = y0 * pow2(max(e0 - expo, -126));
+    w1 = y1 * pow2(max(e1 - expo, -126));
+  }
+  const bool whole = it.parts == 1;
+  const int lim = it.low + token_of(p, it.rem + my_row);
   const bool nans = s.nans;
   const float inv = l == 0.0f ? 0.0f : (expo > -1000 ? e8m0_value(expo + 127) : 0.0f) / l;
+  // the warp's 32 rows of `chunks` 16-byte chunks, in shared memory that nothing else
+  // uses any more: a lane has a row there, and takes whole lines of the rows from there
+  const int shift = (whole ? 3 : 2) - (twin ? 1 : 0) - (D == 64 ? 1 : 0) + (whole ? 0 : 2);
+  const int chunks = 1 << shift;
+  uint4* const mine = reinterpret_cast<uint4*>(raw) + (warp * 32 << shift);
+  auto place = [&](int r, int ch) {
+    return (r << shift) + (ch ^ (shift >= 3 ? r & 7 : shift == 2 ? r >> 1 & 3 : r >> 2 & 1));
+  };
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = 0; c < count / 16; ++c) {
     float v[16];
-    if (it.steps > 0) tmem_ld16(to + 16 * c, v);
+    if (it.steps > 0) tmem_ld16(from + 16 * c, v);
+    if (twin) {
+      float u[16];
+      if (it.steps > 1) tmem_ld16(from + D + 16 * c, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = v[i] * w0 + (it.steps > 1 ? u[i] * w1 : 0.0f);
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = l == 0.0f ? 0.0f : whole ? v[i] * inv : v[i];
     if (nans) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (lim >= s.nan_at[half * (D / 2) + 16 * c + i]) v[i] = qnan();
+        if (lim >= s.nan_at[first + 16 * c + i]) v[i] = qnan();
     }
-    if (!in) continue;
     if (whole) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        dst[2 * c + i] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
-                                    f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
-                                    f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
-                                    f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
+        mine[place(lane, 2 * c + i)] = make_uint4(f32x2_to_bf16x2_bits(v[8 * i], v[8 * i + 1]),
+                                                  f32x2_to_bf16x2_bits(v[8 * i + 2], v[8 * i + 3]),
+                                                  f32x2_to_bf16x2_bits(v[8 * i + 4], v[8 * i + 5]),
+                                                  f32x2_to_bf16x2_bits(v[8 * i + 6], v[8 * i + 7]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        part[4 * c + i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        *reinterpret_cast<float4*>(&mine[place(lane, 4 * c + i)]) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
   }
-  if (in && !whole && half == 0)
+  if (my_row < it.rows && !whole && first == 0)
     *reinterpret_cast<float4*>(p.big_ml + (it.part + my_row) * kPartWords) =
         make_float4(m, l, __int_as_float(expo), 0.0f);
+  __syncwarp();
+  const int ch = lane & (chunks - 1), row0 = my_row - lane;
+#pragma unroll 2
+  for (int r = lane >> shift; r < 32 && row0 + r < it.rows; r += 32 >> shift) {
+    const uint4 u = mine[place(r, ch)];
+    const int row = row0 + r;
+    if (whole) {
+      const int tok = token_of(p, it.rem + row);
+      reinterpret_cast<uint4*>(p.out + (int64_t)(it.row0 + it.tok0 + tok) * p.ld_out +
+                               (int64_t)(it.h * p.group + it.rem + row - tok * p.group) * D +
+                               first)[ch] = u;
+    } else {
+      reinterpret_cast<uint4*>(p.big + (it.part + row) * D + first)[ch] = u;
+    }
+  }
 }
 
 // The parts of the rows of a token, joined in their order: D / 4 lanes to a query head,
@@ -358,9 +422,14 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const AttnJoinParams p) {
   constexpr int L = D / 4, PER = 32 / L;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
+  griddep_launch();                     // of the split kernel's join, which waits for the end
   griddep_wait();
   if (__ldcg(p.next + 1) == 0) return;  // no sequence was cut
-  for (int t = blockIdx.x; t < p.c.T; t += gridDim.x) {
+  const int heads = p.c.heads * p.group;
+  const unsigned chunks = (unsigned)(heads + kJoinWarps * PER - 1) / (kJoinWarps * PER);
+  for (int64_t item = blockIdx.x; item < p.c.T * chunks; item += gridDim.x) {
+    const int t = (int)(item / chunks);
+    const int h0 = ((int)(item - (int64_t)t * chunks) * kJoinWarps + warp) * PER;
     int b = 0;
     for (int hi = p.c.batch; hi - b > 1;) {       // the last sequence that starts at or before t
       const int mid = (b + hi) >> 1;
@@ -371,9 +440,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const Attn
       continue;
     const int cut = prompt_parts(n * p.group, kv, p.c.heads);
     if (cut == 1) continue;
-    const int len = prompt_len(kv, cut), heads = p.c.heads * p.group, tok = t - row0;
+    const int len = prompt_len(kv, cut), tok = t - row0;
     const int tiles = (n * p.group + kPromptRows - 1) / kPromptRows;
-    for (int h0 = warp * PER; h0 < heads; h0 += kJoinWarps * PER) {
+    if (h0 < heads) {
       const int h = min(h0 + sub, heads - 1), r = tok * p.group + h % p.group;
       const int tile = r / kPromptRows;
       const int last = min((tile + 1) * kPromptRows, n * p.group) - 1;
@@ -451,10 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], 8);
     }
-    for (int i = 0; i < kInfo; ++i) {
-      mbar_init(&s.info_full[i], 1);
-      mbar_init(&s.info_empty[i], 21);
-    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(&s.info_full[i], 1);
     mbar_init(&s.q_raw, 1);
     mbar_init(&s.q_full, 16);
     mbar_init(&s.drain, 1);
@@ -465,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < D) s.nan_at[tid] = 0x7fffffff;
   if (tid == 0) s.nans = 0;
   griddep_wait();
+  griddep_launch();                     // of the split kernel: all it reads is there
   if (tid == 0 && (p.flags & IG_FLAG_TEST_COPY_TIMEOUT)) {      // as if a wait had expired
     s.dead = 1;
     atomicOr(p.c.status, kStatusTimeout);
@@ -502,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.tok0 = row / p.group;
           it.rem = row % p.group;
           it.rows = min(2 * kTile, n * p.group - row);
-          it.tiles = it.rows > kTile ? 2 : 1;
+          it.twin = it.rows <= kTile;
           it.low = kv - n + it.tok0;
           it.high = it.low + token_of(p, it.rem + it.rows - 1);
           const int len = prompt_len(kv, cut);
@@ -522,6 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && found < 0) s.it.b = -1;
     __syncwarp();
     if (s.it.b >= 0) {
+      // of a step's readers: softmax warps of one tile or of both, values, copies
+      if (lane < kInfo) mbar_init(&s.info_empty[lane], (s.it.twin ? 8 : 16) + 5);
+      fence_mbar_init();
       // the queries: the heads of one kv head lie together
       const int rem = s.it.rem, end = rem + s.it.rows;
       for (int tok = lane; tok * p.group < end; tok += 32) {
@@ -544,35 +614,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  const int h = s.it.h, tiles = s.it.tiles, low = s.it.low, high = s.it.high, steps = s.it.steps;
+  const int h = s.it.h, low = s.it.low, high = s.it.high, steps = s.it.steps;
+  const bool twin = s.it.twin;
   const int tok0 = s.it.step0 * kTile;  // its first token
   const int half = (warp >> 2) & 1;
-  const int my_row = (warp >> 3) * kTile + (warp & 3) * 32 + lane;      // of warps 0-15
 
   // 512 threads with 96 registers and 256 with 48: the 61440 of the launch
-  if (warp < 8 * tiles) {
+  if (warp < 16) {
     // ---------------------------------------------------------------- softmax
+    // a tile's steps: all, or every second one from its number on
     more_registers<96>();
-    const int t = warp >> 3;
+    const int t = warp >> 3, mine = twin ? (steps + 1 - t) >> 1 : steps;
+    const int slot = t * kTile + (warp & 3) * 32 + lane;
+    const int my_row = twin ? slot - t * kTile : slot, top_row = twin ? 0 : t * kTile;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + lanes;
     const uint32_t to = tmem + 2 * kTile + t * D + half * (D / 2) + lanes;
     // (tokens from the part's first on)
-    const int tile_low = low - tok0 + token_of(p, s.it.rem + t * kTile);
+    const int tile_low = low - tok0 + token_of(p, s.it.rem + top_row);
     const int lim = my_row < s.it.rows ? low - tok0 + token_of(p, s.it.rem + my_row)
                                        : 0x7fffffff;                    // last token it sees
     const int pair_bar = 1 + t * 4 + (warp & 3);        // the two warps of these rows
     bool ok = all_of(9 + t, wait<true>(s, &s.q_raw, 0, p.c.status));
     float f = 0.0f;                     // logit of a product, base 2
     if (ok) {
-      f = convert_queries<D>(p, s, raw);
+      // (without steps nobody reads them, and the results go through their place)
+      if (steps > 0) f = convert_queries<D>(p, s, raw);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_full);
     }
     float m = neg_inf(), l = 0.0f;
-    for (int j = 0; ok && j < steps; ++j) {
-      const int in = j % kInfo;
+    for (int n = 0; ok && n < mine; ++n) {
+      const int j = twin ? 2 * n + t : n, in = j % kInfo;
       ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
       // what the scales have to say is here before the products are
       const float4 ks = *reinterpret_cast<const float4*>(&s.ks[in][4 * half]);
@@ -583,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float down = s.less[in];
       // one warp of the tile looks for the products, the others wait for it: looks
       // share a queue with the exponentials
-      if ((warp & 7) == 0) ok = ok && wait(s, &s.s_full[t], j & 1, p.c.status);
+      if ((warp & 7) == 0) ok = ok && wait(s, &s.s_full[t], n & 1, p.c.status);
       ok = all_of(9 + t, ok);
       if (!ok) break;
       tc_fence_after();
@@ -619,9 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float x = fmaxf(max3(y[0], y[1], y[2]), y[3]);
       // the other half's; both have their products in registers from here on, so
       // P may take the place of S
-      s.most[j & 1][half][my_row] = x;
+      s.most[n & 1][half][slot] = x;
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-      x = fmaxf(x, s.most[j & 1][half ^ 1][my_row]);
+      x = fmaxf(x, s.most[n & 1][half ^ 1][slot]);
       if (x > m + kHeadroom) {
         const float up = ceilf(x), d = m == neg_inf() ? 0.0f : pow2_down(m - up);
         m = up;
@@ -657,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       l = fmaf(sums[2], back.z, l);
       l = fmaf(sums[3], back.w, l);
       // the sums so far by the new maximum and exponent
-      if (j > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
+      if (n > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
         constexpr int N = D / 2 < 32 ? D / 2 : 32;
 #pragma unroll
         for (int c = 0; c < D / 2; c += N) {
@@ -683,28 +757,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ---- the rows' results
-    if (ok && steps > 0) {
-      if ((warp & 7) == 0) ok = wait(s, &s.s_full[t], steps & 1, p.c.status);
+    if (ok && mine > 0) {
+      if ((warp & 7) == 0) ok = wait(s, &s.s_full[t], mine & 1, p.c.status);
       ok = all_of(9 + t, ok);
     }
     tc_fence_after();
-    if (ok) {
-      s.most[steps & 1][half][my_row] = l;
+    if (twin) {
+      tc_fence_before();
+      ok = all_of<512>(11, ok);         // no maximum is looked at any more
+      s.most[1][half][slot] = l;
+      if (half == 0) s.base[slot] = m;
+      ok = all_of<512>(11, ok);
+      tc_fence_after();
+    } else if (ok) {
+      // (the last step's maxima may still be read, in the place of its parity)
+      s.most[mine & 1][half][slot] = l;
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       // (first half) + (second half), for both the same
-      l = s.most[steps & 1][0][my_row] + s.most[steps & 1][1][my_row];
-      store_results<D>(p, s, m, l, to);
+      l = s.most[mine & 1][0][slot] + s.most[mine & 1][1][slot];
     }
-  } else if (warp < 16) {
-    more_registers<96>();
-    // the second tile has no rows: only its share of the barriers
-    if (lane == 0) mbar_arrive(&s.q_full);
-    for (int j = 0; j < steps; ++j) {
-      const int in = j % kInfo;
-      if (!wait<true>(s, &s.info_full[in], (j / kInfo) & 1, p.c.status)) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.info_empty[in]);
-    }
+    if (ok) store_results<D>(p, s, raw, m, l, tmem);
   } else if (warp < 20) {
     // ----------------------------------------------------------------- values
     fewer_registers<48>();
@@ -814,7 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = 1 << (p.c.page_shift - 4);
     bool ok = true;
     int expo = -1000;                   // E, the largest value scale so far
-    if (lane == 0) s.top = expo;
+    int old[2] = {expo, expo};          // E of the step before and of the one before that
+    if (lane == 0) s.top[0] = s.top[1] = expo;
     for (int j0 = 0; ok && j0 < steps; j0 += 4) {
       const int tok = tok0 + j0 * kTile + lane * kKvBlock;
       bool there = tok <= high;
@@ -850,10 +923,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           s.partly[in] = (have >> (8 * i) & 0xffu) != 0xffu;
-          s.less[in] = expo > -1000 ? pow2(max(expo - to, -126)) : 1.0f;
-          s.top = to;
+          const int then = twin ? old[1] : old[0];      // of the tile's step before
+          s.less[in] = then > -1000 ? pow2(max(then - to, -126)) : 1.0f;
+          s.top[(j0 + i) & 1] = to;
         }
-        expo = to;
+        old[1] = old[0];
+        old[0] = expo = to;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.info_full[in]);
       }
@@ -875,39 +950,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
+    auto pv = [&](int t, int j, bool acc, bool last) {
+      const uint32_t v = base + S::kV16 + (j & 1) * 2 * S::kPart;
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          mma_f16_tm(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * i, desc_values(v + 2048 * i),
+                     ipv, acc || i > 0);
+        if (last) umma_commit(&s.s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto free = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
     bool ok = wait<true>(s, &s.q_full, 0, p.c.status) && wait(s, &s.k_full[0], 0, p.c.status);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      for (int t = 0; t < tiles; ++t) qk(t, 0);
-      if (elect_one()) umma_commit(&s.k_empty[0]);
-      __syncwarp();
-    }
-    for (int j = 0; ok && j < steps; ++j) {
-      ok = wait(s, &s.v16_full[j & 1], (j >> 1) & 1, p.c.status);
-      if (ok && j + 1 < steps)
-        ok = wait(s, &s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.c.status);
-      for (int t = 0; t < tiles; ++t) {
-        ok = ok && wait(s, &s.p_full[t], j & 1, p.c.status);
+    if (!twin) {
+      if (ok) {
+        qk(0, 0);
+        qk(1, 0);
+        free(&s.k_empty[0]);
+      }
+      for (int j = 0; ok && j < steps; ++j) {
+        ok = wait(s, &s.v16_full[j & 1], (j >> 1) & 1, p.c.status);
+        if (ok && j + 1 < steps)
+          ok = wait(s, &s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, p.c.status);
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && wait(s, &s.p_full[t], j & 1, p.c.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          pv(t, j, j > 0, j + 1 == steps);
+          if (j + 1 < steps) qk(t, j + 1);
+        }
+        if (!ok) break;
+        free(&s.v16_empty[j & 1]);
+        if (j + 1 < steps) free(&s.k_empty[(j + 1) & 1]);
+      }
+    } else {
+      // step j is tile j % 2's; its next one is two steps on
+      for (int j = 0; ok && j < 2 && j < steps; ++j) {
+        ok = wait(s, &s.k_full[j], 0, p.c.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        qk(j, j);
+        free(&s.k_empty[j]);
+      }
+      for (int j = 0; ok && j < steps; ++j) {
+        const int t = j & 1;
+        ok = wait(s, &s.v16_full[t], (j >> 1) & 1, p.c.status) &&
+             wait(s, &s.p_full[t], (j >> 1) & 1, p.c.status);
+        if (ok && j + 2 < steps) ok = wait(s, &s.k_full[t], ((j + 2) >> 1) & 1, p.c.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t v = base + S::kV16 + (j & 1) * 2 * S::kPart;
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_f16_tm(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * i,
-                       desc_values(v + 2048 * i), ipv, j > 0 || i > 0);
-          if (j + 1 == steps) umma_commit(&s.s_full[t]);
+        pv(t, j, j > 1, j + 2 >= steps);
+        free(&s.v16_empty[t]);
+        if (j + 2 < steps) {
+          qk(t, j + 2);
+          free(&s.k_empty[t]);
         }
-        __syncwarp();
-        if (j + 1 < steps) qk(t, j + 1);
       }
-      if (!ok) break;
-      if (elect_one()) {
-        umma_commit(&s.v16_empty[j & 1]);
-        if (j + 1 < steps) umma_commit(&s.k_empty[(j + 1) & 1]);
-      }
-      __syncwarp();
     }
    }
   }
@@ -943,8 +1048,11 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   int64_t items = (rows / (2 * kTile) + some) * p.c.heads;
   // those that are cut have kPromptItems items at most
   if (p.big_rows) items += some * kPromptItems;
-  e = launch_pdl(prompt_kernel<D>, dim3((unsigned)items), dim3(kThreads), smem, st, p);
-  if (e != cudaSuccess || !p.big_rows) return e;
+  return launch_pdl(prompt_kernel<D>, dim3((unsigned)items), dim3(kThreads), smem, st, p);
+}
+
+template <int D>
+cudaError_t launch_join(const AttnParams& p, cudaStream_t st) {
   AttnJoinParams j;
   j.c = p.c;
   j.out = p.out;
@@ -956,8 +1064,9 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   j.few_rows = p.few_rows;
   j.part_rows = p.big_rows;
   j.big_by_row = p.big_by_row;
-  const int64_t most = 4 * sm_count();
-  return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)(p.c.T < most ? p.c.T : most)),
+  constexpr int PER = kJoinWarps * 128 / D;             // heads to a block at a time
+  const int64_t items = p.c.T * ((p.heads_q + PER - 1) / PER), most = 4 * sm_count();
+  return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)(items < most ? items : most)),
                     dim3(32 * kJoinWarps), 0, st, j);
 }
 
@@ -965,6 +1074,9 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
 
 cudaError_t launch_attention_prompt(const AttnParams& p, int head_dim, cudaStream_t st) {
   return head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
+}
+cudaError_t launch_attention_prompt_join(const AttnParams& p, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
 }
 
 }  // namespace ig

@@ -822,7 +822,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NT>::kBlocks)
     prefetch_tensormap(&p.tm);
   }
   griddep_launch();                     // of the join kernel, which waits for this one's end
-  griddep_wait();
+  // (the prompt kernel lets this one start behind its own wait: what was before is there)
+  if (!p.after_prompt) griddep_wait();
 
   // items of each sequence, summed up
   int carry = 0;
@@ -865,6 +866,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NT>::kBlocks)
     compute_warp<D, NT>(p, s, raw, warp, lane);
   else
     copy_warp<D, NT>(p, s, raw, prefix, carry, lane);
+  if (p.after_prompt) griddep_wait();   // the joins wait for this kernel's end alone
 }
 
 template <int D, int NT>
@@ -873,9 +875,12 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(split_kernel<D, NT>), allowed);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(split_kernel<D, NT>, dim3(Smem<D, NT>::kBlocks * sm_count()), dim3(kThreads), smem,
-                 st, p);
-  if (e != cudaSuccess) return e;
+  return launch_pdl(split_kernel<D, NT>, dim3(Smem<D, NT>::kBlocks * sm_count()), dim3(kThreads),
+                    smem, st, p);
+}
+
+template <int D>
+cudaError_t launch_join(const AttnParams& p, cudaStream_t st) {
   AttnJoinParams j;
   j.next = p.next;
   j.c = p.c;
@@ -909,6 +914,9 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
 cudaError_t launch_attention_split(const AttnParams& p, int head_dim, cudaStream_t st) {
   if (p.part_rows <= 8) return head_dim == 128 ? launch<128, 1>(p, st) : launch<64, 1>(p, st);
   return head_dim == 128 ? launch<128, 2>(p, st) : launch<64, 2>(p, st);
+}
+cudaError_t launch_attention_join(const AttnParams& p, int head_dim, cudaStream_t st) {
+  return head_dim == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
 }
 
 }  // namespace ig
