@@ -73,6 +73,7 @@ struct AttnParams {
   int32_t big_by_row;   // see big_place
   int32_t heads_q, group;   // query heads, and of one kv head
   uint32_t group_inv;   // 65536 / group, rounded up: row / group for few rows
+  uint32_t group_magic, heads_magic;    // see divide
   float group_rcp;      // 1 / group
   int32_t few_rows;     // sequences with at most this many rows a kv head are the split kernel's
   int32_t max_tiles;    // 16-row tiles of such a sequence
@@ -155,7 +156,23 @@ __host__ __device__ inline int prompt_seen(int high, int len) {
   return high < 0 || len < 1 ? 1 : high / kPromptStep / len + 1;
 }
 
+// For divide(): (2^32 - 1) / d.
+inline uint32_t magic_of(int d) { return 0xffffffffu / (uint32_t)d; }
+
 #ifdef __CUDACC__
+// v / d and, in v, the rest; with magic = (2^32 - 1) / d rounded down the product is two
+// below the quotient at most.
+__device__ __forceinline__ uint32_t divide(uint32_t& v, uint32_t d, uint32_t magic) {
+  uint32_t q = __umulhi(v, magic);
+  v -= q * d;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (v >= d) {
+      v -= d;
+      ++q;
+    }
+  return q;
+}
 // New tokens of sequence b: rows row0 .. row0 + n - 1, the last of kv tokens.
 // False (and the status word says so) where they are out of range.
 __device__ __forceinline__ bool sequence_of(const KvParams& c, int b, int& row0, int& n, int& kv) {

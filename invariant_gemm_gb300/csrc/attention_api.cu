@@ -317,6 +317,8 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.group = pl.group;
   p.group_rcp = 1.0f / (float)pl.group;
   p.group_inv = (uint32_t)((65536 + pl.group - 1) / pl.group);
+  p.group_magic = magic_of(pl.group);
+  p.heads_magic = magic_of(cache->heads);
   p.few_rows = kFewRows;
   p.max_tiles = pl.max_tiles;
   p.max_parts = pl.max_parts;
