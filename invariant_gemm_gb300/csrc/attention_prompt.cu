@@ -19,7 +19,19 @@
 //
 // Warps: 0-7 and 8-15 the softmax of a tile each, half a row to a thread; 16-19
 // the values; 20 the copies; 21 the MMAs; 22 the pages and scales. The two tiles
-// take turns: while one is in the softmax the tensor cores work on the other.
+// take turns: while one is in the softmax the tensor cores work on the other. Where a
+// block has 128 rows at most, both tiles have these rows, one the even steps and one
+// the odd ones, and their sums are joined at the end (64 sequences of 64 rows over 8192
+// tokens: a step 1700 clocks instead of 3500).
+//
+// What bounds it: a step of both tiles takes 3500 clocks of which the tensor cores work
+// 2050 by their nominal rate; the rest is the chain products - maximum - exponentials -
+// P of the two tiles, whose issue slots (54 %) and barriers do not all hide behind the
+// other tile's. Beside its steps a block costs 20000 clocks: 2400 to find its rows,
+// 8000 to load and convert 64 KB of queries, 2000 to the first products, 2300 from the
+// last P to the last sums, 6000 for the results, 2000 to the next block. 2048 tokens over
+// 32768 (32 query, 8 kv heads of 128): 868 us, 1230 TFLOP/s; three prompts of up to 4095
+// tokens 214 us.
 #include "attention.cuh"
 #include "umma_mx4.cuh"
 

@@ -3,17 +3,17 @@
 //
 // Rows are a kv head's: `group` query heads for each new token, 16 rows to a
 // tile. A work item is one tile, one kv head and one part of the sequence's
-// tokens (split_tokens). Items are dealt to blocks that stay, three to an SM
-// where a tile has 8 rows at most, else two. In a block four warps compute, one
-// copies ahead and one joins:
+// tokens (split_tokens). Items go to whichever block asks first (a counter in the
+// workspace), of blocks that stay: three to an SM where a tile has 8 rows at most,
+// else two. In a block four warps compute and one copies ahead:
 //   copies   pages and scales of the part, a step of 16 tokens (a block of the
 //            cache) to a lane, asked for while the part before is on its way;
 //            then one TMA box for a step's keys and one for its values, four
 //            steps to a stage of the ring; the item's queries
-//   compute  a step of each stage to a warp
-//   join     the four warps' sums, in their order, into the output or, where the
-//            rows see several parts, into the workspace
-// A second kernel joins the parts, in their order.
+//   compute  a step of each stage to a warp; then a share each of the four warps'
+//            sums, in their order, into the output or, where the rows see several
+//            parts, into the workspace
+// A second kernel joins the parts, in an order that their number fixes.
 //
 // FP16 tensor-core products with the tokens as rows (M) and the query rows as
 // columns (N, 8 at a time): S^T = K Q^T and O^T = V^T P^T, so that 8 rows a kv
@@ -32,6 +32,13 @@
 // the fragments are what lies together: a lane's keys are 32 consecutive bytes of
 // two tokens, its values 16 consecutive bytes of four tokens; the box's swizzle
 // makes both 128-bit loads free of bank conflicts.
+//
+// What bounds it: HBM. 64 sequences of up to 8192 tokens, 8 kv heads of 128, 8 rows each:
+// 598 MB in 109 us (5.5 TB/s), issue slots 51 %; the join of the parts behind it 8 us.
+// 8 of up to 65536, 4 rows each: 104 us for 622 MB with the join (6.0 TB/s). Small calls
+// are the chain launch - lengths - pages - copies - products - join: 777 tokens 9.8 us
+// through the binding. With more than 16 rows each tile reads and converts the tokens
+// again, from L2: 32 rows 306 us where 8 take 117.
 #include "attention.cuh"
 #include "warp_mma.cuh"
 

@@ -5,7 +5,9 @@
 // both values of a rotated pair are in one lane: with halves as pairs a group of
 // the first half and its partner, with neighbours as pairs 8 values in a row. 64-bit
 // loads and stores, a butterfly over D / 8 lanes for the norm, nothing else between
-// lanes.
+// lanes. Arithmetic goes by pairs of FP32 values: with single ones and the weights apart
+// from the rotation the instructions bound all three (8192 tokens of 64 + 8 heads of 128
+// in 64.9 us at 73 % of the issue slots, now 54.1 us at 61 %: 5.7 TB/s, and HBM).
 #include "attention.cuh"
 
 namespace ig {
@@ -454,8 +456,9 @@ __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const GatherParams 
 
 unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kWarps - 1) / kWarps); }
 
-// Passes: a warp takes several heads of a token with one look at its angles
-// where there are many, one pass of them where the call is small.
+// Passes: a warp takes four passes of heads of a token with one look at its angles
+// where that leaves 16 warps to an SM at least, one pass where the call is smaller (a
+// token of 40 heads of 128: 20 warps instead of 5). The bits are the same.
 template <int D>
 cudaError_t qk(const RopeParams& p, cudaStream_t st) {
   constexpr int PER = 256 / D;
@@ -488,8 +491,10 @@ cudaError_t append_launch(const AppendParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, append_kernel<D, INTER, PASSES, W>, p, kv_blocks);
 }
 
-// One warp a block where no sequence has more new tokens than it holds at a time,
-// else four.
+// One warp to a block of the cache where no sequence has more new tokens than it holds
+// at a time (single tokens: 256 sequences 4096 warps), else four, whose loads are on their
+// way together. Five prompts of up to 3001 tokens, 64 + 8 heads of 128: 79 us for 447 MB,
+// issue slots 70 %.
 template <int D, bool INTER>
 cudaError_t append(const AppendParams& p, cudaStream_t st) {
   constexpr int PER = 256 / D;
