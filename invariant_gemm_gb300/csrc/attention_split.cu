@@ -703,8 +703,8 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   const int head = (int)(row % heads);
   const int tok = (int)(row / heads % max(p.tokens, 1));
   const int64_t b = row / heads / max(p.tokens, 1);
-  griddep_wait();
-  if (blockIdx.x == 0 && threadIdx.x < 2) p.next[threadIdx.x] = 0;
+  // (the kernels before this one start behind all that was before them, so the lengths
+  // are there already)
   int row0 = 0, n = 0, kv = 0;
   bool in = b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
             n * p.group <= p.few_rows;
@@ -713,6 +713,8 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   const int last = min((tile + 1) * kRows, n * p.group) - 1;      // of the tile's rows
   int parts = in ? tile_parts(kv - n + last / p.group, len) : 1;
   in = in && parts > 1;
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.next[threadIdx.x] = 0;
   if (!__any_sync(0xffffffffu, in)) return;         // the same in all warps
   if (!in) parts = 1;
   const int64_t first =
@@ -828,9 +830,9 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NT>::kBlocks)
     fence_mbar_init();
     prefetch_tensormap(&p.tm);
   }
-  griddep_launch();                     // of the join kernel, which waits for this one's end
   // (the prompt kernel lets this one start behind its own wait: what was before is there)
   if (!p.after_prompt) griddep_wait();
+  griddep_launch();                     // of the join kernel, which waits for this one's end
 
   // items of each sequence, summed up
   int carry = 0;
