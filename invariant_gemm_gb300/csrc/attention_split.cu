@@ -205,7 +205,7 @@ struct Unit {
   Item it;
   int step;                    // first of the unit's steps
   int32_t page;
-  uint32_t info;
+  uint32_t key, value;         // scales, not looked at before a step is handed on
 };
 
 // The unit after u: of the same item, else of the block's next item that has a
@@ -231,7 +231,8 @@ __device__ __forceinline__ void next_unit(const AttnParams& p, const int* prefix
       if (u.it.split < u.it.parts) break;
     }
   }
-  u.info = kAbsent;
+  u.key = kAbsent;
+  u.value = 0;
   u.page = 0;
   const int tok = u.it.t0 + (u.step + lane) * kStep;
   if (tok < u.it.t1)
@@ -245,7 +246,8 @@ __device__ __forceinline__ void unit_scales(const AttnParams& p, int lane, Unit&
     const int blocks = 1 << (p.c.page_shift - 4);
     const uint8_t* s = p.c.scales + u.page * p.c.scale_stride + u.it.h * blocks +
                        ((tok & ((1 << p.c.page_shift) - 1)) / kKvBlock);
-    u.info = __ldg(s) | (uint32_t)__ldg(s + p.c.heads * blocks) << 8;
+    u.key = __ldg(s);
+    u.value = __ldg(s + p.c.heads * blocks);
   } else {
     atomicOr(p.c.status, kStatusIndexRange);
   }
@@ -310,8 +312,9 @@ __device__ void copy_warp(const AttnParams& p, Smem<D, NT>& s, uint8_t* ring, co
           tma_load_3d(at + kTeam * S::kBox, &p.tm, 0,
                       ((p.c.heads + now.it.h) << p.c.page_shift) + row, page, &s.full[st]);
         }
-        const uint32_t info = __shfl_sync(0xffffffffu, now.info, (i + lane) & 31);
-        if (lane < kTeam) s.info[st][lane] = there ? info : kAbsent;
+        const uint32_t key = __shfl_sync(0xffffffffu, now.key, (i + lane) & 31);
+        const uint32_t value = __shfl_sync(0xffffffffu, now.value, (i + lane) & 31);
+        if (lane < kTeam) s.info[st][lane] = there ? key | value << 8 : kAbsent;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[st]);
         __syncwarp();
