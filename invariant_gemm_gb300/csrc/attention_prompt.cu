@@ -202,6 +202,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
         : "r"(taddr) : "memory");
   }
 }
+// 16 bytes from global to shared memory, of which the first `bytes` are read and the
+// others 0.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes) : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -302,26 +308,24 @@ __device__ __noinline__ float convert_queries(const AttnParams& p, Smem<D>& s, u
   {
     const __nv_bfloat16* q = p.q + (int64_t)(it.row0 + it.tok0) * p.ld_q +
                              (int64_t)it.h * p.group * D + half * (D / 2) + ch * 8;
-    uint4 w[CH];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int r = warp_row + lane / CH + 32 / CH * i, at = it.rem + r - same;
-      const int tok = token_of(p, at);
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows)
-        w[i] = *reinterpret_cast<const uint4*>(q + tok * p.ld_q + (at - tok * p.group) * D);
+#pragma unroll 1
+    for (int r = warp_row + lane / CH; r < warp_row + 32; r += 32 / CH) {
+      const int at = it.rem + r - same, tok = token_of(p, at);
+      const bool in = r < rows;
+      cp_async16(from + r * 2 * D, in ? q + tok * p.ld_q + (at - tok * p.group) * D : q, in ? 16 : 0);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncwarp();
+#pragma unroll 2
+  for (int r = warp_row + lane / CH; r < warp_row + 32; r += 32 / CH) {
+    const uint4 w = *reinterpret_cast<const uint4*>(from + r * 2 * D);
+    // (magnitudes of bf16 compare as whole numbers do)
+    uint32_t top = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                            __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int r = warp_row + lane / CH + 32 / CH * i;
-      *reinterpret_cast<uint4*>(from + r * 2 * D) = w[i];
-      // (magnitudes of bf16 compare as whole numbers do)
-      uint32_t top = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                              __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-#pragma unroll
-      for (int o = CH / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (ch == 0) s.most[0][half][r] = __uint_as_float(max(top & 0xffffu, top >> 16));
-    }
+    for (int o = CH / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (ch == 0) s.most[0][half][r] = __uint_as_float(max(top & 0xffffu, top >> 16));
   }
   asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + (warp & 3)) : "memory");
   auto exponent = [&](int r) {          // the row's largest value is below 2^(this - 126)
@@ -442,7 +446,7 @@ __device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, uint
         make_float4(m, l, __int_as_float(expo), 0.0f);
   __syncwarp();
   const int ch = lane & (chunks - 1), row0 = my_row - lane;
-#pragma unroll 4
+#pragma unroll 1
   for (int r = lane >> shift; r < 32 && row0 + r < it.rows; r += 32 >> shift) {
     const uint4 u = mine[place(r, ch)];
     const int row = row0 + r;
