@@ -131,7 +131,7 @@ __host__ __device__ inline int split_tokens(int kv) {
 // The prompt kernel cuts a sequence's tokens too where its rows are few blocks' work
 // (256 rows of a kv head each): into up to 16 parts, so many that blocks times parts
 // fill a GPU's 152 SMs once at most, of six steps of 128 tokens at least. Again
-// nothing but the sequence's own sizes decides. (A block costs 20000 clocks beside its
+// nothing but the sequence's own sizes decides. (A block costs 23000 clocks beside its
 // steps of 3500. Parts of 3, 5, 8 and 12 steps at least, 32 query and 8 kv heads of 128:
 // one sequence, 200 tokens over 2000 33, 35, 39, 44 us; 16 of up to 200 over up to
 // 3000 199, 168, 141, 122 us.)

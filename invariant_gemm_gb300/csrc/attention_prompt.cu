@@ -27,10 +27,10 @@
 // What bounds it: a step of both tiles takes 3500 clocks of which the tensor cores work
 // 2050 by their nominal rate; the rest is the chain products - maximum - exponentials -
 // P of the two tiles, whose issue slots (54 %) and barriers do not all hide behind the
-// other tile's. Beside its steps a block costs 20000 clocks: 2400 to find its rows,
-// 8000 to load and convert 64 KB of queries, 2000 to the first products, 2300 from the
-// last P to the last sums, 6000 for the results, 2000 to the next block. 2048 tokens over
-// 32768 (32 query, 8 kv heads of 128): 868 us, 1230 TFLOP/s; three prompts of up to 4095
+// other tile's. Beside its steps a block costs 23000 clocks: 2400 to find its rows,
+// 9000 to load and convert 64 KB of queries, 1900 to the first products, 2300 from the
+// last P to the last sums, 5500 for the results, 2100 to the next block. 2048 tokens over
+// 32768 (32 query, 8 kv heads of 128): 871 us, 1220 TFLOP/s; three prompts of up to 4095
 // tokens 214 us.
 #include "attention.cuh"
 #include "umma_mx4.cuh"
