@@ -546,7 +546,8 @@ typedef struct ig_attn_shape {
  * Enough for every call with fewer tokens, sequences, pages or a smaller max_q.
  * Zeroed once after it is allocated; calls that may overlap, captured ones too,
  * need one each. The library's other calls may share it where they do not overlap;
- * a token map in it does not outlive ig_paged_attention. */
+ * a token map in it does not outlive ig_paged_attention. After IG_ERR_CUDA of a call
+ * it has to be zeroed again. */
 size_t ig_attention_workspace_bytes(const ig_attn_shape* shape, const ig_kv_cache* cache,
                                     const ig_batch* batch);
 

@@ -244,3 +244,57 @@ def test_many_sequences():
         b = Batch(lengths, hq, 1, 128, 16, seed=51).fill()
         q = b.rows(hq)
         b.check(q, b.attend(q))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(65, 1), (128, 1), (200, 2), (300, 1), (1024, 1)])
+@pytest.mark.parametrize("lengths", [[(1, 70), (1, 1), (2, 300)], [(1, 3000)], [(3, 2), (0, 5), (1, 129)]])
+def test_many_query_heads_of_one_kv_head(hq, hkv, lengths):
+    """A token's rows alone are more than a tile, or than a block."""
+    need_gpu()
+    b = Batch(lengths, hq, hkv, 64, 32, seed=hq).fill()
+    q = b.rows(hq)
+    b.check(q, b.attend(q))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_beyond_the_table_of_angles(inter):
+    """Tokens whose place the table does not have: NaN keys and queries, values as they
+    are, and the status says so."""
+    need_gpu()
+    b = Batch([(20, 25), (1, 9), (1, 11)], 4, 2, 64, 16, seed=60)
+    q, k, v = b.rows(4), b.rows(2), b.rows(2)
+    args = b.device_args()
+    ws, out = ig.mx4_workspace(), torch.zeros(b.T, 4, 64, dtype=B16, device="cuda")
+    cs = torch.ones(10, 64, device="cuda")
+    ig.kv_append(k.cuda(), v.cuda(), *args, ws, cos_sin=cs, q=q.cuda(), q_out=out, max_q=b.max_q,
+                 flags=ig.ROPE_INTERLEAVED if inter else 0)
+    assert ig.check_status(ws) == -10 and ig.check_status(ws) == 0
+    codes, scales = args[0].cpu().numpy(), args[1].cpu().numpy()
+    at = np.concatenate([np.arange(kv - n, kv) for n, kv in b.lengths])
+    assert (out.isnan().all(-1).all(-1).cpu().numpy() == (at >= 10)).all()
+    assert not out.isnan()[torch.from_numpy(at < 10)].any()
+    for s, (n, kv) in enumerate(b.lengths):
+        kk, vv = ref.held(codes, scales, b.table[s], kv)
+        new = np.arange(kv - n, kv)
+        assert np.isnan(kk[new[new >= 10]]).all() and np.isfinite(kk[new[new < 10]]).all()
+        assert np.isfinite(vv[new]).all()
+
+
+@pytest.mark.gpu
+def test_nothing_in_a_batch():
+    """No sequences, no tokens, sequences of no tokens."""
+    need_gpu()
+    z = lambda *s, t=B16: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    cache, scales = z(2, 2, 2, 16, 64, t=torch.uint8), z(2, 2, 2, 1, t=torch.uint8)
+    for B, T in ((0, 0), (0, 5), (3, 0), (3, 5)):
+        cu, kv, table = z(B + 1, t=I32), z(B, t=I32), z(B, 4, t=I32)
+        q, k, out = z(T, 4, 64), z(T, 2, 64), torch.full((T, 4, 64), 7.0, device="cuda").to(B16)
+        ws = ig.attention_workspace(q, cache, table)
+        kept = torch.full((T, 2, 64), 7.0, device="cuda").to(B16)
+        ig.kv_append(k, k, cache, scales, cu, kv, table, ws, q=q, q_out=out)
+        ig.paged_attention(q, cache, scales, cu, kv, table, out, ws)
+        ig.kv_gather(cache, scales, cu, kv, table, kept, kept.clone(), ws)
+        assert ig.check_status(ws) == 0
+        assert (out == 7).all() and (kept == 7).all() and not cache.any()
