@@ -298,3 +298,72 @@ def test_nothing_in_a_batch():
         ig.kv_gather(cache, scales, cu, kv, table, kept, kept.clone(), ws)
         assert ig.check_status(ws) == 0
         assert (out == 7).all() and (kept == 7).all() and not cache.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (64, 12, 3)])
+def test_rows_of_cut_sequences_do_not_depend_on_the_batch(D, hq, hkv):
+    """Sequences cut into parts, blocks of one tile and of two, few rows among them: each
+    bit for bit as alone, wherever it stands."""
+    need_gpu()
+    lengths = [(25, 4000), (1, 500), (100, 3000), (17, 2500), (200, 2000), (3, 9)]
+    b = Batch(lengths, hq, hkv, D, 32, seed=70).fill()
+    q = b.rows(hq, 2.0).cuda()
+    args = b.device_args()
+    whole = b.attend(q, args=args)
+    b.check(q, whole)
+    for i, (n, kv) in enumerate(lengths):
+        r = slice(int(b.cu[i]), int(b.cu[i + 1]))
+        one = (args[0], args[1], torch.tensor([0, n], dtype=I32, device="cuda"), args[3][i:i + 1],
+               args[4][i:i + 1])
+        assert torch.equal(whole[r], b.attend(q[r], max_q=n, args=one)), (i, n, kv)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,inter", [(128, False), (64, True)])
+def test_norms_and_appends_do_not_depend_on_the_batch(D, inter):
+    """The same bits in calls of a token and of thousands, in and out of place."""
+    need_gpu()
+    flags = ig.ROPE_INTERLEAVED if inter else 0
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, hq, hk = 3001, 24, 5
+    x = torch.randn(T, hq + 2 * hk, D, device="cuda", generator=g).to(B16)
+    w = torch.rand(D, device="cuda", generator=g).to(B16)
+    turn = torch.arange(4000)[:, None] * 10000.0 ** (-torch.arange(D // 2) * 2.0 / D)
+    cs = torch.cat([turn.cos(), turn.sin()], 1).float().cuda()
+    pos = torch.randint(0, 4000, (T,), dtype=I32, device="cuda", generator=g)
+    ws = ig.mx4_workspace()
+
+    def normed(r, place):
+        q, k = x[r, :hq].clone(), x[r, hq:hq + hk].clone()
+        qo, ko = (q, k) if place else (torch.empty_like(q), torch.empty_like(k))
+        ig.qk_norm_rope(q, k, qo, ko, ws, w_q=w, w_k=w, cos_sin=cs, positions=pos[r], flags=flags)
+        return qo, ko
+
+    whole = normed(slice(0, T), False)
+    for r in (slice(0, T), slice(0, 1), slice(1500, 1504), slice(T - 1, T)):
+        for place in (False, True):
+            for a, b in zip(whole, normed(r, place)):
+                assert torch.equal(a[r], b)
+
+    # sequences of one to many new tokens, together and each alone
+    lengths = [(1, 17), (2, 40), (1, 1), (1000, 1200), (4, 4), (700, 703), (1, 3000)]
+    b = Batch(lengths, hq, hk, D, 32, seed=71).fill()
+    n = b.T
+    q, k, v = x[:n, :hq], x[:n, hq:hq + hk], x[:n, hq + hk:]
+
+    def appended(seqs):
+        codes, scales, cu, kv, table = b.device_args()
+        out = torch.zeros(n, hq, D, dtype=B16, device="cuda")
+        for first, last in seqs:
+            r = slice(int(b.cu[first]), int(b.cu[last]))
+            ig.kv_append(k[r], v[r], codes, scales, cu[first:last + 1] - int(b.cu[first]),
+                         kv[first:last], table[first:last], ws, w_k=w, cos_sin=cs, q=q[r],
+                         q_out=out[r], w_q=w, flags=flags,
+                         max_q=max(m for m, _ in lengths[first:last]))
+        assert ig.check_status(ws) == 0
+        return codes, scales, out
+
+    together = appended([(0, len(lengths))])
+    alone = appended([(i, i + 1) for i in range(len(lengths))])
+    assert all(torch.equal(a, c) for a, c in zip(together, alone))
