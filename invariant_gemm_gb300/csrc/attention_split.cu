@@ -691,8 +691,9 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
 // 4 values each, 128 / D rows to a block. Eight sums, of the parts w, w + 8, ... in
 // their order, added in the order of w; W warps share them. Few rows are a matter
 // of how long it takes to get at a row's parts (W = 8: 256 rows of up to 64 parts
-// 5 us), many of how many rows there are at a time (W = 2: 4096 rows of up to 16
-// parts).
+// 5 us), many of how many rows there are at a time: the whole call with W = 1, 2 and 4
+// 113.3, 114.7 and 115.8 us for 4096 rows of up to 16 parts, 73.9, 76.8 and 81.6 for
+// 8192 of up to 4. 792 blocks of two rows: W = 8 18.7 us, 1 17.8.
 constexpr int kJoinSums = 8;
 
 template <int D, int W>
@@ -704,14 +705,13 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   __shared__ float weight[PER][kMaxSplits], inverse[PER];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
   const int heads = p.c.heads * p.group;
-  const int64_t row = (int64_t)blockIdx.x * PER + sub;          // [sequence][token][head]
-  const int head = (int)(row % heads);
-  const int tok = (int)(row / heads % max(p.tokens, 1));
-  const int64_t b = row / heads / max(p.tokens, 1);
+  uint32_t b = blockIdx.x * PER + sub;          // [sequence][token][head], below 2^30
+  const int head = (int)next_digit(b, heads);
+  const int tok = (int)next_digit(b, max(p.tokens, 1));
   // (the kernels before this one start behind all that was before them, so the lengths
   // are there already)
   int row0 = 0, n = 0, kv = 0;
-  bool in = b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
+  bool in = (int)b < p.c.batch && sequence_of(p.c, (int)b, row0, n, kv) && tok < n &&
             n * p.group <= p.few_rows;
   const int r = tok * p.group + head % p.group, tile = r / kRows;
   const int len = split_tokens(kv);
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   if (!__any_sync(0xffffffffu, in)) return;         // the same in all warps
   if (!in) parts = 1;
   const int64_t first =
-      in ? ((b * p.max_tiles + tile) * p.c.heads + head / p.group) * p.max_parts : 0;
+      in ? (((int64_t)b * p.max_tiles + tile) * p.c.heads + head / p.group) * p.max_parts : 0;
   const float* ml = p.part_ml + (first * p.part_rows + r % kRows) * kPartWords;
   const float* at = p.parts + (first * p.part_rows + r % kRows) * D + d;
   uint4 x[B][C];
@@ -916,7 +916,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t st) {
   if (!any) j.c.batch = 0;
   constexpr int PER = 128 / D;
   const dim3 grid((unsigned)((rows + PER - 1) / PER));
-  if (grid.x > 8u * sm_count()) return launch_pdl(join_kernel<D, 2>, grid, dim3(64), 0, st, j);
+  if (grid.x > 4u * sm_count()) return launch_pdl(join_kernel<D, 1>, grid, dim3(32), 0, st, j);
   return launch_pdl(join_kernel<D, 8>, grid, dim3(256), 0, st, j);
 }
 
