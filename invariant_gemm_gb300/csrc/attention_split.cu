@@ -34,12 +34,12 @@
 // makes both 128-bit loads free of bank conflicts.
 //
 // What bounds it: HBM. 64 sequences of up to 8192 tokens, 8 kv heads of 128, 8 rows each:
-// 598 MB in 108 us (5.5 TB/s), issue slots half used; the join of the parts behind it 7
+// 598 MB in 108 us (5.5 TB/s), issue slots half used; the join of the parts behind it 5
 // us. 8 of up to 65536, 4 rows each: 103 us for 622 MB with the join (6.0 TB/s). Small
 // calls are the chain start - lengths (0.9 us) - pages, queries, copies (1.8) - products of
 // four steps to a warp (2.7) - join of the warps (0.6) - join of the parts (2): 777 tokens
 // 8.9 us. With more than 16 rows each tile reads and converts the tokens again, from L2:
-// 32 rows 305 us where 8 take 115. (Tiles of 32 rows, queries in shared memory, one block
+// 32 rows 305 us where 8 take 113. (Tiles of 32 rows, queries in shared memory, one block
 // of 254 registers to an SM: 434 us.)
 #include "attention.cuh"
 #include "warp_mma.cuh"
