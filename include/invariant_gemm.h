@@ -506,8 +506,9 @@ int ig_qk_norm_rope(const ig_rope_shape* shape, const void* q, const void* k, co
  * smallest 2^e, e >= -120, with max|value| <= 448 2^e over the finite values of
  * its new tokens; where older tokens of the sequence are in the block it is at
  * least their scale, and where it grew they are divided by as much. Values are
- * rounded to nearest, ties to even; what is not finite is held as NaN. Rows of
- * the block behind the last token keep their bytes.
+ * rounded to nearest, ties to even (keys that FP32 cannot tell from the middle
+ * between two codes by their FP64 values); what is not finite is held as NaN.
+ * Rows of the block behind the last token keep their bytes.
  * A block that is written must be one token range of one sequence: not shared
  * by two sequences, nor on a page that the page table names twice (its bytes are
  * unspecified otherwise; pages that are only read may be shared freely).

@@ -204,6 +204,64 @@ __global__ void __launch_bounds__(32 * kWarps) qk_kernel(RopeParams p) {
                                    [&] { return (int64_t)__ldg(p.positions + item); });
 }
 
+// A key is off by a few units of the last place that FP32 has for the larger of it and the
+// value that it is rotated with, and where it lies as near to the middle between two codes
+// it would be rounded to the farther one: 1.2 of a million keys were. Those within 2^-20 of
+// that larger one are worked out again in FP64 (4 us of 97, append and read-back of
+// five prompts of up to 3001 tokens): 0.04 of a million are left.
+//
+// Whether a value in steps of the scale is that near: the middles of codes of 3 mantissa
+// bits have the top one of the 20 bits below. (Under 2^-6 they lie elsewhere; there a code's
+// step is 2^-17 of the largest code and its choice of no weight.)
+__device__ __forceinline__ bool near_middle(float x, float other) {
+  const float middle = __uint_as_float((__float_as_uint(x) & 0xfff00000u) | 0x80000u);
+  return fabsf(x - middle) <= fmaxf(fabsf(x), fabsf(other)) * 0x1p-20f;
+}
+
+// Keys as norm_rotate has them, from FP64, times 2^-e; rounded to FP32 towards 0, with
+// the last bit set where that left anything, so that the next rounding is the only one.
+template <int D, bool INTER>
+__device__ __noinline__ Values keys_again(const RopeParams& p, Place at, uint2 a, uint2 b,
+                                          bool turned, int64_t row, int e) {
+  constexpr int L = D / 8;
+  const uint32_t in[4] = {a.x, a.y, b.x, b.y};
+  double x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (double)(i & 1 ? bf16hi(in[i >> 1]) : bf16lo(in[i >> 1]));
+  double scale = __longlong_as_double((long long)(1023 - e) << 52);
+  if (p.w_k) {
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    scale *= rsqrt(ss / D + (double)p.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = __bfloat162float(p.w_k[(i < 4 ? at.a : at.b - 4) + i]);
+      x[i] *= (double)w + (p.plus_one ? 1.0 : 0.0);
+    }
+  }
+  if (turned) {
+    const float* angles = p.cos_sin + row * p.rot + at.pair;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int one = INTER ? 2 * i : i, two = INTER ? 2 * i + 1 : i + 4;
+      const double c = angles[i], n = angles[(p.rot >> 1) + i], x1 = x[one], x2 = x[two];
+      x[one] = x1 * c - x2 * n;
+      x[two] = x2 * c + x1 * n;
+    }
+  }
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double v = x[i] * scale;
+    f[i] = __double2float_rz(v);
+    if ((double)f[i] != v) f[i] = __uint_as_float(__float_as_uint(f[i]) | 1u);
+  }
+  return {{pair2(f[0], f[1]), pair2(f[2], f[3]), pair2(f[4], f[5]), pair2(f[6], f[7])}};
+}
+
 // One block of 16 tokens of one head and side, by W warps (of one thread block where
 // they are four) that take its new tokens in turn, PASSES times 256 / D at most each.
 template <int D, bool INTER, int W>
@@ -317,14 +375,44 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
   const int e = max((int)(bits >> 23) - 126 - 9 + ((bits & 0x7fffffu) > 0x600000u), kKvMinExp);
   const int byte = older ? max(e + 127, was) : e + 127;
   const float down = byte == 255 ? __uint_as_float(0x7fc00000u) : e8m0_value(254 - byte);
+  const bool inexact = side == 0 && (p.r.w_k || p.r.cos_sin);
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int pos = begin + i * PER;
+    Values g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g.x[j] = mul2(f[i].x[j], pair2(down, down));
+    if (inexact) {
+      uint32_t which = 0;               // of the eight
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = split2(g.x[j]), y = split2(partner<INTER>(g, j));
+        which |= (near_middle(x.x, y.x) ? 1u : 0u) << 2 * j | (near_middle(x.y, y.y) ? 2u : 0u) << 2 * j;
+      }
+      if (__any_sync(0xffffffffu, which && pos < end)) {
+        int64_t row = pos;
+        uint2 a = make_uint2(0, 0), b = a;
+        if (pos < end) {
+          const int64_t t = row0 + pos - first;
+          a = *reinterpret_cast<const uint2*>(src + t * ld + at.a);
+          b = *reinterpret_cast<const uint2*>(src + t * ld + at.b);
+          if (p.r.positions) row = __ldg(p.r.positions + t);
+        }
+        const bool turned = p.r.cos_sin && pos < end && at.pair >= 0 && row >= 0 &&
+                            row < p.r.table_rows;
+        const Values again = keys_again<D, INTER>(p.r, at, a, b, turned, row, byte - 127);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = split2(g.x[j]), y = split2(again.x[j]);
+          g.x[j] = pair2(which >> 2 * j & 1 ? y.x : x.x, which >> 2 * j & 2 ? y.y : x.y);
+        }
+      }
+    }
     if (pos >= end) continue;
     uint32_t q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 x = split2(mul2(f[i].x[j], pair2(down, down)));
+      const float2 x = split2(g.x[j]);
       q[j] = f32x2_to_e4m3x2(x.x, x.y);
     }
     *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.a) = q[0] | q[1] << 16;
@@ -365,7 +453,7 @@ __device__ __forceinline__ int sequence_at(const int32_t* cu, int batch, int64_t
 
 // The blocks of k and v, behind them q: kv_blocks thread blocks and the others.
 template <int D, bool INTER, int PASSES, int W>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p,
+__global__ void __launch_bounds__(32 * kWarps, 9) append_kernel(const AppendParams p,
                                                              unsigned kv_blocks) {
   constexpr int PER = PASSES * 256 / D;
   __shared__ float tops[kWarps];
@@ -493,8 +581,9 @@ cudaError_t append_launch(const AppendParams& p, cudaStream_t st) {
 
 // One warp to a block of the cache where no sequence has more new tokens than it holds
 // at a time (single tokens: 256 sequences 4096 warps), else four, whose loads are on their
-// way together. Five prompts of up to 3001 tokens, 64 + 8 heads of 128: 79 us for 447 MB,
-// issue slots 70 %.
+// way together. Five prompts of up to 3001 tokens, 64 + 8 heads of 128: 83 us for 447 MB,
+// issue slots 72 %. Nine blocks to an SM: with the registers that FP64 would take (72 to
+// 80, six blocks) 103 us in place of 99, append and read-back.
 template <int D, bool INTER>
 cudaError_t append(const AppendParams& p, cudaStream_t st) {
   constexpr int PER = 256 / D;

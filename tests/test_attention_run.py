@@ -367,3 +367,45 @@ def test_norms_and_appends_do_not_depend_on_the_batch(D, inter):
     together = appended([(0, len(lengths))])
     alone = appended([(i, i + 1) for i in range(len(lengths))])
     assert all(torch.equal(a, c) for a, c in zip(together, alone))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rot,inter,placed", [(128, 128, False, False), (64, 32, True, True)])
+def test_keys_are_rounded_to_the_nearest_code(D, rot, inter, placed):
+    """Of 8 million normed and rotated keys, against FP64: FP32's last place (2^-24, a few
+    of them) next to middles 2^-4 apart gets about one of a million wrong, 8 here, and those
+    as near as 2^-20 are worked out in FP64. What is left are keys whose error is above
+    2^-20 of the larger value of their pair, 16 units: none to speak of, and keys under 2^-6
+    of the scale. At most one."""
+    need_gpu()
+    T, heads = 2 ** 23 // (8 * D), 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, 2 * heads, D, device="cuda", generator=g).to(B16)
+    w = (1 + 0.3 * torch.randn(D, device="cuda", generator=g)).to(B16)
+    turn = torch.arange(T)[:, None] * 10000.0 ** (-torch.arange(rot // 2) * 2.0 / rot)
+    cs = torch.cat([turn.cos(), turn.sin()], 1).float().cuda()
+    pos = torch.randperm(T, device="cuda", generator=g).to(I32) if placed else None
+    pages = -(-T // 64)
+    cache = torch.zeros(pages, 2, heads, 64, D, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(pages, 2, heads, 4, dtype=torch.uint8, device="cuda")
+    cu, kv = (torch.tensor(a, dtype=I32, device="cuda") for a in ([0, T], [T]))
+    table = torch.randperm(pages, device="cuda", generator=g).to(I32)[None]
+    ws = ig.mx4_workspace()
+    k, v = x[:, :heads], x[:, heads:]
+    ig.kv_append(k, v, cache, scales, cu, kv, table, ws, w_k=w, cos_sin=cs, positions=pos, eps=1e-6,
+                 flags=ig.ROPE_INTERLEAVED if inter else 0)
+    got, _ = torch.empty(2, T, heads, D, dtype=B16, device="cuda")
+    ig.kv_gather(cache, scales, cu, kv, table, got, torch.empty_like(got), ws)
+    assert ig.check_status(ws) == 0
+    y = k.double()
+    y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+    c, s = cs.double()[torch.arange(T) if pos is None else pos.long()][:, None].chunk(2, -1)
+    a, b = (y[..., :rot:2], y[..., 1:rot:2]) if inter else (y[..., :rot // 2], y[..., rot // 2:rot])
+    one, two = a * c - b * s, b * c + a * s
+    y[..., :rot] = torch.stack([one, two], -1).flatten(-2) if inter else torch.cat([one, two], -1)
+    scale = scales[table[0].long(), 0].permute(0, 2, 1).reshape(-1, heads)[:T // 16].double()
+    z = y.view(-1, 16, heads, D) / torch.exp2(scale - 127)[:, None, :, None]
+    step = torch.exp2(torch.floor(torch.log2(z.abs().clamp(min=2.0 ** -6))) - 3)
+    want = (z / step).round() * step * torch.exp2(scale - 127)[:, None, :, None]
+    assert z.abs().max() <= 448
+    assert (want.view(T, heads, D) != got.double()).sum() <= 1
