@@ -582,8 +582,8 @@ cudaError_t append_launch(const AppendParams& p, cudaStream_t st) {
 // One warp to a block of the cache where no sequence has more new tokens than it holds
 // at a time (single tokens: 256 sequences 4096 warps), else four, whose loads are on their
 // way together. Five prompts of up to 3001 tokens, 64 + 8 heads of 128: 83 us for 447 MB,
-// issue slots 72 %. Nine blocks to an SM: with the registers that FP64 would take (72 to
-// 80, six blocks) 103 us in place of 99, append and read-back.
+// issue slots 72 %. (Nine blocks to an SM; with eight 103 us in place of 99, append and
+// read-back.)
 template <int D, bool INTER>
 cudaError_t append(const AppendParams& p, cudaStream_t st) {
   constexpr int PER = 256 / D;
