@@ -79,7 +79,7 @@ struct Smem {
   int partly[kInfo];                    // some block of the step is not there
   float less[kInfo];                    // 2^(E before - E) of the step
   int top[2];                           // E in the end, of the even and the odd steps
-  int nan_at[D], nans;                  // first NaN token of each value; whether there is one
+  int nan_at[D], nans;                  // first token that makes each value NaN; whether one does
   float most[2][2][2 * kTile];          // [step % 2][half][row]: largest logit, sum
   float base[2 * kTile];                // m in the end
   uint32_t tmem;
@@ -953,6 +953,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         kb = __ldg(sc);
         vb = __ldg(sc + p.c.heads * blocks);
       }
+      // a NaN scale of keys: rows that see the block are NaN, others are to know nothing of
+      // it, so it stays out of the softmax and comes with the results
+      for (uint32_t bad = __ballot_sync(0xffffffffu, there && kb == 255); bad; bad &= bad - 1) {
+        const int first = tok0 + j0 * kTile + (__ffs(bad) - 1) * kKvBlock;
+        for (int d = lane; d < D; d += 32) atomicMin(&s.nan_at[d], first);
+        s.nans = 1;
+      }
+      if (kb == 255) kb = 127;
       const uint32_t have = __ballot_sync(0xffffffffu, there);
       for (int i = 0; i < 4 && j0 + i < steps; ++i) {
         const int in = (j0 + i) % kInfo;
