@@ -46,6 +46,7 @@ constexpr float kHeadroom = 7.0f;
 constexpr float kBias = 8.0f;
 constexpr int kMinShift = -40;
 constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
+constexpr int kNoExp = -1000;           // of no block yet
 constexpr int kNoBlock = 2000;          // tokens that no row sees, or an absent page
 constexpr int kInfo = 8;                // steps whose pages and scales are held
 
@@ -560,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     s.dead = 0;
     s.nans = 0;
+    s.top[0] = s.top[1] = kNoExp;       // (a block without steps reads it all the same)
   }
   if (tid == 64) {
     for (int i = 0; i < 2; ++i) {
@@ -934,9 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* table = p.c.table + (int64_t)s.it.b * p.c.ld_table;
     const int blocks = 1 << (p.c.page_shift - 4);
     bool ok = true;
-    int expo = -1000;                   // E, the largest value scale so far
+    int expo = kNoExp;                  // E, the largest value scale so far
     int old[2] = {expo, expo};          // E of the step before and of the one before that
-    if (lane == 0) s.top[0] = s.top[1] = expo;
     for (int j0 = 0; ok && j0 < steps; j0 += 4) {
       const int tok = tok0 + j0 * kTile + lane * kKvBlock;
       bool there = tok <= high;

@@ -1,8 +1,9 @@
-"""Attention at the ends of its ranges: NaN scales of tokens that some rows do not see."""
+"""Attention at the ends of its ranges: NaN scales of tokens that some rows do not see, sequences
+with no tokens."""
 import numpy as np
 import pytest
 
-from attention_helpers import Batch
+from attention_helpers import Batch, f64
 from helpers import need_gpu
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,19 @@ def test_nan_scale_of_keys_stays_with_the_rows_that_see_it(length, hq, D):
     assert 0 < sees.sum() < n
     assert np.isnan(out[:n][sees]).all() and not np.isnan(out[:n][~sees]).any()
     assert not np.isnan(out[n:]).any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_and_no_tokens(D):
+    """Sequences of more than 64 rows that have no tokens at all: rows of 0, whatever the
+    blocks before left in shared memory."""
+    need_gpu()
+    b = Batch([(100, 0), (70, 0), (300, 0), (129, 0), (128, 0), (200, 100)], 2, 1, D, 16, seed=45).fill()
+    q = b.rows(2, 3.0)
+    big = Batch([(300, 700)] * 12, 2, 1, D, 16, seed=46).fill(size=1e6)
+    bq = big.rows(2, 1e4)
+    for _ in range(3):
+        big.attend(bq)
+        got = f64(b.attend(q))
+        assert (got[:-100] == 0).all() and (got[-100:] != 0).any()
+    b.check(q, b.attend(q))
