@@ -278,12 +278,16 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
   // more new tokens than the sequence has in all: those before its first are
   // not in it
   const int first = kv - n;
-  const int start = (max(first, 0) / kKvBlock + blk) * kKvBlock;
-  if (n == 0 || start >= kv) return;
+  blk += max(first, 0) / kKvBlock;
+  if (n == 0 || kv == 0 || blk > (kv - 1) / kKvBlock) return;
+  // (kv may be close to 2^31, so what is behind the block's last token is not counted up to:
+  // places from here on are the block's, 0 to 15)
+  const int start = blk * kKvBlock;
   const int32_t page = __ldg(c.table + (int64_t)b * c.ld_table + (start >> c.page_shift));
   // the new tokens of this warp: begin + PER i, of those before end
-  const int begin = max(start, first) + warp * PASSES * PER + lane / L;
-  const int end = min(start + kKvBlock, kv);
+  const int begin = max(first - start, 0) + warp * PASSES * PER + lane / L;
+  const int end = min(kKvBlock, kv - start);
+  const int row_at = row0 + (start - first);        // row of place 0
   const Place at = place_of<INTER>(p.r, l);
   const __nv_bfloat16* src = (side ? p.v : p.r.k) + (int64_t)h * D;
   const int64_t ld = side ? p.ld_v : p.r.ld_k;
@@ -293,7 +297,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
     const int pos = begin + i * PER;
     raw[i][0] = raw[i][1] = make_uint2(0, 0);
     if (pos < end) {
-      const int64_t t = row0 + pos - first;
+      const int64_t t = row_at + pos;
       raw[i][0] = *reinterpret_cast<const uint2*>(src + t * ld + at.a);
       raw[i][1] = *reinterpret_cast<const uint2*>(src + t * ld + at.b);
     }
@@ -313,9 +317,9 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
     for (int i = 0; i < PASSES; ++i) {
       const int pos = begin + i * PER;
       bool bad = false;
-      int64_t row = pos;
+      int64_t row = (int64_t)start + pos;
       if (p.r.cos_sin && pos < end) {
-        if (p.r.positions) row = __ldg(p.r.positions + row0 + pos - first);
+        if (p.r.positions) row = __ldg(p.r.positions + row_at + pos);
         bad = !in_table(p.r, row);
       }
       const bool turned = p.r.cos_sin && pos < end && !bad && at.pair >= 0;
@@ -390,10 +394,10 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
         which |= (near_middle(x.x, y.x) ? 1u : 0u) << 2 * j | (near_middle(x.y, y.y) ? 2u : 0u) << 2 * j;
       }
       if (__any_sync(0xffffffffu, which && pos < end)) {
-        int64_t row = pos;
+        int64_t row = (int64_t)start + pos;
         uint2 a = make_uint2(0, 0), b = a;
         if (pos < end) {
-          const int64_t t = row0 + pos - first;
+          const int64_t t = row_at + pos;
           a = *reinterpret_cast<const uint2*>(src + t * ld + at.a);
           b = *reinterpret_cast<const uint2*>(src + t * ld + at.b);
           if (p.r.positions) row = __ldg(p.r.positions + t);
@@ -415,8 +419,8 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int b, int b
       const float2 x = split2(g.x[j]);
       q[j] = f32x2_to_e4m3x2(x.x, x.y);
     }
-    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.a) = q[0] | q[1] << 16;
-    *reinterpret_cast<uint32_t*>(rows + (pos - start) * D + at.b) = q[2] | q[3] << 16;
+    *reinterpret_cast<uint32_t*>(rows + pos * D + at.a) = q[0] | q[1] << 16;
+    *reinterpret_cast<uint32_t*>(rows + pos * D + at.b) = q[2] | q[3] << 16;
   }
   if (warp != 0) return;
   __syncwarp();                         // every lane has read the scale that was

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import invariant_gemm_gb300 as ig
-from attention_helpers import B16, Batch, f64
+from attention_helpers import B16, I32, Batch, f64
 from helpers import need_gpu
 from oracle import attention as ref
 
@@ -279,3 +279,37 @@ def test_pools_of_more_than_4_gb_and_strides():
     assert (pool[far:].cpu().numpy() == a.codes).all()
     assert (spool[far:].cpu().numpy() == a.scales).all()
     assert not pool[:far].any() and not spool[:far].any()
+
+
+@pytest.mark.parametrize("D,n", [(128, 1), (128, 2), (64, 20)])
+def test_append_and_gather_at_the_last_positions(D, n):
+    """A sequence of 2^31 - 1 tokens, the most that a length can say, with blocks of another
+    sequence's count behind its last one: only its own block is written, and reads back."""
+    need_gpu()
+    kv, page, cols = 2 ** 31 - 1, 256, 1 << 23
+    b = Batch([(n, n), (150, 150)], 2, 2, D, page, seed=50)
+    k, v = b.rows(2), b.rows(2)
+    tables = [{cols - 1: int(b.table[0, 0])}, {0: int(b.table[1, 0])}]
+    table = torch.zeros(2, cols, dtype=I32, device="cuda")
+    table[0, -1], table[1, 0] = tables[0][cols - 1], tables[1][0]
+    codes, scales, cu, _, _ = b.device_args()
+    lengths = torch.tensor([kv, 150], dtype=I32, device="cuda")
+    ws = ig.mx4_workspace()
+    for max_q in ((150, None) if n > 1 else (150,)):
+        codes.copy_(torch.from_numpy(b.codes))
+        scales.copy_(torch.from_numpy(b.scales))
+        ig.kv_append(k.cuda(), v.cuda(), codes, scales, cu, lengths, table, ws, max_q=max_q)
+        assert ig.check_status(ws) == 0
+        want_c, want_s = b.codes.copy(), b.scales.copy()
+        for s, first in ((0, kv - n), (1, 0)):
+            for side, x in ((0, k), (1, v)):
+                ref.append(want_c, want_s, f64(x)[b.cu[s]:b.cu[s + 1]], tables[s], first, side)
+        assert (codes.cpu().numpy() == want_c).all() and (scales.cpu().numpy() == want_s).all()
+    ko, vo = (torch.zeros(b.T, 2, D, dtype=B16, device="cuda") for _ in range(2))
+    ig.kv_gather(codes, scales, cu, lengths, table, ko, vo, ws)
+    assert ig.check_status(ws) == 0
+    for side, got in ((0, ko), (1, vo)):
+        page_of, at = tables[0][cols - 1], np.arange(page - 1 - n, page - 1)
+        unit = 2.0 ** (want_s[page_of, side][:, at // 16].astype(int) - 127.0)
+        want = ref.decode(want_c[page_of, side][:, at]) * unit[..., None]
+        np.testing.assert_array_equal(f64(got)[:n], want.transpose(1, 0, 2))
