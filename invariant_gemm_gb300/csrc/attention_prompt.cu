@@ -44,6 +44,7 @@ constexpr int kThreads = 768;
 constexpr int kHalf = kTile / 2;        // columns of a thread
 constexpr float kHeadroom = 7.0f;
 constexpr float kBias = 8.0f;
+constexpr float kFar = 1048576.0f;      // logits past this are rounded before they are used
 constexpr int kMinShift = -40;
 constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
 constexpr int kNoExp = -1000;           // of no block yet
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4 ks = *reinterpret_cast<const float4*>(&s.ks[in][4 * half]);
       const float4 bias = *reinterpret_cast<const float4*>(&s.bias[in][4 * half]);
       const float4 back = *reinterpret_cast<const float4*>(&s.back[in][4 * half]);
-      const float k[4] = {factor(f, ks.x), factor(f, ks.y), factor(f, ks.z), factor(f, ks.w)};
+      float k[4] = {factor(f, ks.x), factor(f, ks.y), factor(f, ks.z), factor(f, ks.w)};
       const bool partly = s.partly[in];
       float down = s.less[in];
       // one warp of the tile looks for the products, the others wait for it: looks
@@ -740,20 +741,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) y[q] = max3(y[q], v[16 * q + i], v[16 * q + i + 1]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) y[q] = fmaxf(y[q], v[16 * q + 15]) * k[q];
+      for (int q = 0; q < 4; ++q) y[q] = __fmul_rn(fmaxf(y[q], v[16 * q + 15]), k[q]);
       float x = fmaxf(max3(y[0], y[1], y[2]), y[3]);
       // the other half's; both have their products in registers from here on, so
       // P may take the place of S
       s.most[n & 1][half][slot] = x;
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       x = fmaxf(x, s.most[n & 1][half ^ 1][slot]);
-      if (x > m + kHeadroom) {
+      if (x > __fadd_rd(m, kHeadroom)) {
         const float up = ceilf(x), d = m == neg_inf() ? 0.0f : pow2_down(m - up);
         m = up;
         l *= d;
         down *= d;
       }
-      const float base = m == neg_inf() ? 0.0f : m;
+      float base = m == neg_inf() ? 0.0f : m;
+      if (__builtin_expect(fabsf(base) > kFar, 0)) {
+        // m is a rounded logit, and what the product below has beyond it is no longer small
+        // against p's range: logits as they were rounded for m
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // (two roundings: with mul2 and add2 they came out as one)
+#pragma unroll
+          for (int i = 16 * q; i < 16 * q + 16; ++i)
+            v[i] = __fsub_rn(__fmul_rn(v[i], k[q]), base);
+          k[q] = 1.0f;
+        }
+        base = 0.0f;
+      }
       const float off[4] = {bias.x - base, bias.y - base, bias.z - base, bias.w - base};
       float sums[4];
 #pragma unroll

@@ -55,6 +55,7 @@ constexpr int kRows = 16;               // of a tile
 constexpr int kUnit = 32;               // steps looked up at a time
 constexpr float kHeadroom = 7.0f;       // a row's m is raised past m + this
 constexpr float kBias = 8.0f;           // p is 2^kBias at m
+constexpr float kFar = 1048576.0f;      // past this m takes its own difference from a logit
 constexpr int kMinShift = -40;          // value scales below 2^-40 of the largest: as 2^-40
 constexpr uint32_t kAbsent = 1u << 16;  // step's word: its page does not exist
 constexpr int kSeqs = 128;              // sequences that a block keeps beside their items
@@ -538,8 +539,8 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float a0 = f[nt][0] * ks, a1 = f[nt][1] * ks;
-        sc[nt][0] *= a0; sc[nt][1] *= a1;
-        sc[nt][2] *= a0; sc[nt][3] *= a1;
+        sc[nt][0] = __fmul_rn(sc[nt][0], a0); sc[nt][1] = __fmul_rn(sc[nt][1], a1);
+        sc[nt][2] = __fmul_rn(sc[nt][2], a0); sc[nt][3] = __fmul_rn(sc[nt][3], a1);
       }
       const uint32_t vbyte = (info >> 8) & 0xffu;
       if (vbyte == 255) {               // the block's values are NaN
@@ -583,7 +584,7 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          raise |= fmaxf(sc[nt][r], sc[nt][2 + r]) > m[nt][r] + kHeadroom;
+          raise |= fmaxf(sc[nt][r], sc[nt][2 + r]) > __fadd_rd(m[nt][r], kHeadroom);
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -594,7 +595,7 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
             float d = 1.0f;
-            if (x > m[nt][r] + kHeadroom) {
+            if (x > __fadd_rd(m[nt][r], kHeadroom)) {
               const float to = ceilf(x);
               d = m[nt][r] == neg_inf() ? 0.0f : pow2_down(m[nt][r] - to);
               m[nt][r] = to;
@@ -629,8 +630,18 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = (m[nt][0] == neg_inf() ? 0.0f : m[nt][0]) - (kBias + (float)shift);
-        const float b1 = (m[nt][1] == neg_inf() ? 0.0f : m[nt][1]) - (kBias + (float)shift);
+        float b[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float base = m[nt][r] == neg_inf() ? 0.0f : m[nt][r];
+          if (fabsf(base) > kFar) {     // (m - kBias may be rounded up or down by more than kBias)
+            sc[nt][r] -= base;
+            sc[nt][2 + r] -= base;
+            base = 0.0f;
+          }
+          b[r] = base - (kBias + (float)shift);
+        }
+        const float b0 = b[0], b1 = b[1];
         const float p0 = ex2(sc[nt][0] - b0), p1 = ex2(sc[nt][1] - b1);
         const float p2 = ex2(sc[nt][2] - b0), p3 = ex2(sc[nt][3] - b1);
         l[nt][0] = fmaf(p0 + p2, back, l[nt][0]);
