@@ -556,11 +556,13 @@ size_t ig_attention_workspace_bytes(const ig_attn_shape* shape, const ig_kv_cach
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j),
  * over the tokens j <= kv_len - rows + i for row i of a sequence's `rows`. Rows
  * that see no token (rows > kv_len) are 0. Products of the held values in
- * the tensor cores with FP32 sums, softmax in FP32; p is rounded to 11 bits for
- * the product with v. A sequence of at most 64 rows a kv head (rows times heads_q
- * / heads) is one kernel's, of more another's, which takes the values of a query
- * under 2^-9 of its largest to within 2^-17 of it. out may not be q, nor overlap
- * what the call reads. */
+ * the tensor cores with FP32 sums, softmax in FP32; for the product with the codes of
+ * v, p times v's scale is rounded to 11 bits or to 2^-32 of the row's largest such product,
+ * whichever is more (scales under 2^-120 of the largest up to the row's step of 128 tokens
+ * count as that). A sequence of at most 64 rows a kv head (rows times heads_q / heads) is
+ * one kernel's, which takes the values of a query under 2^-31 of its largest to within
+ * 2^-39 of it, of more another's: under 2^-9, 2^-17. out may not be q, nor
+ * overlap what the call reads. */
 int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
                        const ig_batch* batch, const void* q, void* out, void* ws,
                        size_t ws_bytes, void* stream);

@@ -123,7 +123,7 @@ constexpr int kFewRows = 64;
 // (so that a row's bits do not depend on the batch): 256 up to 4096 tokens, then
 // whole 512s, at most 64 of them.
 constexpr int kMaxSplits = 64;
-constexpr int kPartWords = 4;           // of a row of a part: maximum, sum, exponent, unused
+constexpr int kPartWords = 4;           // of a row of a part: m, l, c (below), unused
 __host__ __device__ inline int split_tokens(int kv) {
   return kv <= 4096 ? 256 : 512 * ((kv + 512 * kMaxSplits - 1) / (512 * kMaxSplits));
 }
@@ -163,6 +163,20 @@ __host__ __device__ inline int prompt_seen(int high, int len) {
   return high < 0 || len < 1 ? 1 : high / kPromptStep / len + 1;
 }
 
+// --- a row's sums -------------------------------------------------------------
+// Of a token, t is the logit in base 2 and e the exponent of its value's scale. Its weight
+// in the product with the values' codes is p = 2^(t + e - m + 8), m a whole number that the
+// row's largest t + e passes by 7 at most: FP16 has 11 bits of it down to 2^-14, so that
+// tokens lose bits against the row's own largest weight times scale, and against nothing
+// that the row does not see. The products sum to 2^(8 - m) sum 2^t v, and
+// l = sum p 2^(c - e) = 2^(8 - m + c) sum 2^t, so the result is their quotient times 2^c.
+// Powers of two round nothing, and c is a matter of FP32's range alone: with -40 up to
+// scales of 2^63, then 40, l is between 2^-95 and 2^102 times the number of tokens where
+// scales are less than 2^kSpread apart (a smaller one counts as 2^-kSpread of the largest
+// so far, or p could be 0 of a token that has its part in l).
+constexpr int kSpread = 120;
+__host__ __device__ constexpr int c_of(int largest_e) { return largest_e < 64 ? -40 : 40; }
+
 // For divide(): (2^32 - 1) / d.
 inline uint32_t magic_of(int d) { return 0xffffffffu / (uint32_t)d; }
 
@@ -196,6 +210,9 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
 }
 // 2^e for e from -126 to 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// 2^(c - e) for a value scale's exponent e, E the largest so far
+__device__ __forceinline__ float back_of(int e, int E) { return pow2(c_of(E) - e); }
 
 // Two e4m3 codes (the low one in bits 0-7) -> two FP16 values, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {

@@ -15,7 +15,8 @@
 //               their own into the MMA's order (tokens along K, so V as it lies:
 //               the MN-major operand).
 // Softmax as in the split kernel: base 2, whole exponents, a row's maximum raised
-// only past m + 7, value scales folded into P, key scales into the logits.
+// only past m + 7, value scales folded into P ("a row's sums" in attention.cuh), key
+// scales into the logits.
 //
 // Warps: 0-7 and 8-15 the softmax of a tile each, half a row to a thread; 16-19
 // the values; 20 the copies; 21 the MMAs; 22 the pages and scales. The two tiles
@@ -45,7 +46,6 @@ constexpr int kHalf = kTile / 2;        // columns of a thread
 constexpr float kHeadroom = 7.0f;
 constexpr float kBias = 8.0f;
 constexpr float kFar = 1048576.0f;      // logits past this are rounded before they are used
-constexpr int kMinShift = -40;
 constexpr int kNaNExp = 1000;           // of a block whose value scale is NaN
 constexpr int kNoExp = -1000;           // of no block yet
 constexpr int kNoBlock = 2000;          // tokens that no row sees, or an absent page
@@ -74,13 +74,13 @@ struct Smem {
   uint64_t k_full[2], k_empty[2], v8_full[2], v8_empty[2], v16_full[2], v16_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t info_full[kInfo], info_empty[kInfo], q_full, drain;
-  // of a step's 8 blocks: scale of the keys; kBias + e - E and 2^(E - e) for p; e
-  alignas(16) float ks[kInfo][8], bias[kInfo][8], back[kInfo][8];
+  // of a step's 8 blocks: scale of the keys; e and 2^(c - e) for p; e or what is wrong with it
+  alignas(16) float ks[kInfo][8], expo[kInfo][8], back[kInfo][8];
   int ve[kInfo][8];
   int page[kInfo][8];
   int partly[kInfo];                    // some block of the step is not there
-  float less[kInfo];                    // 2^(E before - E) of the step
-  int top[2];                           // E in the end, of the even and the odd steps
+  float more[kInfo];                    // 2^(c - c of the tile's step before)
+  int c[2];                             // c in the end, of the even and the odd steps
   int nan_at[D], nans;                  // first token that makes each value NaN; whether one does
   float most[2][2][2 * kTile];          // [step % 2][half][row]: largest logit, sum
   float base[2 * kTile];                // m in the end
@@ -370,31 +370,28 @@ __device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, uint
   const bool twin = it.twin;
   const int t = warp >> 3, local = (warp & 3) * 32 + lane, my_row = twin ? local : t * kTile + local;
   const int first = twin ? (2 * t + half) * (D / 4) : half * (D / 2), count = twin ? D / 4 : D / 2;
-  int expo = s.top[1];
+  int c = s.c[1];
   float w0 = 1.0f, w1 = 0.0f;
   uint32_t from = tmem + 2 * kTile + ((uint32_t)((warp & 3) * 32) << 16) + first;
   if (!twin) {
     from += t * D;
-    if (it.steps & 1) expo = s.top[0];
+    if (it.steps & 1) c = s.c[0];
   } else {
     const float m0 = s.base[local], m1 = s.base[kTile + local];
     const float l0 = s.most[1][0][local] + s.most[1][1][local];
     const float l1 = s.most[1][0][kTile + local] + s.most[1][1][kTile + local];
-    const int e0 = s.top[0], e1 = s.top[1];
+    c = max(s.c[0], s.c[1]);
     m = fmaxf(m0, m1);
-    expo = max(e0, e1);
-    const float y0 = m0 == neg_inf() ? 1.0f : pow2_down(m0 - m);
-    const float y1 = m1 == neg_inf() ? 1.0f : pow2_down(m1 - m);
-    l = l0 * y0 + l1 * y1;
-    w0 = y0 * pow2(max(e0 - expo, -126));
-    w1 = y1 * pow2(max(e1 - expo, -126));
+    w0 = m0 == neg_inf() ? 1.0f : pow2_down(m0 - m);
+    w1 = m1 == neg_inf() ? 1.0f : pow2_down(m1 - m);
+    l = l0 * pow2(c - s.c[0]) * w0 + l1 * pow2(c - s.c[1]) * w1;
   }
   const bool whole = it.parts == 1;
   const int lim = it.low + token_of(p, it.rem + my_row);
   const bool nans = s.nans;
   // (where l is 0 so are the sums)
-  const float inv =
-      !whole ? 1.0f : l == 0.0f || expo <= -1000 ? 0.0f : __fdividef(e8m0_value(expo + 127), l);
+  // (one after the other: 2^c / l may be below FP32's range where the result is not)
+  const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l), unit = pow2(c);
   // the warp's 32 rows of `chunks` 16-byte chunks, in shared memory that nothing else
   // uses any more: a lane has a row there, and takes whole lines of the rows from there
   const int shift = (whole ? 3 : 4) - (twin ? 1 : 0) - (D == 64 ? 1 : 0);
@@ -433,7 +430,7 @@ __device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, uint
         uint32_t u[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          u[k] = f32x2_to_bf16x2_bits(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+          u[k] = f32x2_to_bf16x2_bits(v[8 * i + 2 * k] * inv * unit, v[8 * i + 2 * k + 1] * inv * unit);
         mine[place(lane, c / 8 + i)] = make_uint4(u[0], u[1], u[2], u[3]);
       }
     } else {
@@ -445,7 +442,7 @@ __device__ __noinline__ void store_results(const AttnParams& p, Smem<D>& s, uint
   }
   if (my_row < it.rows && !whole && first == 0)
     *reinterpret_cast<float4*>(p.big_ml + (it.part + my_row) * kPartWords) =
-        make_float4(m, l, __int_as_float(expo), 0.0f);
+        make_float4(m, l, __int_as_float(c), 0.0f);
   __syncwarp();
   const int ch = lane & (chunks - 1), row0 = my_row - lane;
 #pragma unroll 1
@@ -508,27 +505,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const Attn
         x[q] = make_uint4(0, 0, 0, 0);
         if (in && q < parts) x[q] = ldg_cg_v4(p.parts + (at + q * pitch) * D + d);
       }
-      float w = 0.0f, scale = 0.0f;       // of part `lane % L` of this lane's row
+      float w = 0.0f, inv = 0.0f, unit = 0.0f;      // of part `lane % L` of this lane's row
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int64_t from = __shfl_sync(0xffffffffu, at, k * L);
         const int count = __shfl_sync(0xffffffffu, in ? parts : 0, k * L);
-        float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+        float4 u = make_float4(neg_inf(), 0.0f, __int_as_float(c_of(kNoExp)), 0.0f);
         if (lane < count)
           u = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (from + lane * pitch) * kPartWords));
         float top = u.x;
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
+        const int c = __reduce_max_sync(0xffffffffu, __float_as_int(u.z));
         const float y = u.x == neg_inf() ? 1.0f : pow2_down(u.x - top);
-        float sum = u.y * y;
+        float sum = u.y * pow2(c - __float_as_int(u.z)) * y;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float mine = __shfl_sync(0xffffffffu, y * pow2(max(__float_as_int(u.z) - e, -126)),
-                                       lane % L);
+        const float mine = __shfl_sync(0xffffffffu, y, lane % L);
         if (k == sub) {
           w = mine;
-          scale = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
+          inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          unit = pow2(c);
         }
       }
       float4 v = make_float4(0, 0, 0, 0);
@@ -544,8 +541,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const Attn
       }
       if (in)
         *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_out + (int64_t)h * D + d) =
-            make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
-                       f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
+            make_uint2(f32x2_to_bf16x2_bits(v.x * inv * unit, v.y * inv * unit),
+                       f32x2_to_bf16x2_bits(v.z * inv * unit, v.w * inv * unit));
     }
   }
 }
@@ -562,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     s.dead = 0;
     s.nans = 0;
-    s.top[0] = s.top[1] = kNoExp;       // (a block without steps reads it all the same)
+    s.c[0] = s.c[1] = c_of(kNoExp);     // (a block without steps reads it all the same)
   }
   if (tid == 64) {
     for (int i = 0; i < 2; ++i) {
@@ -702,11 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(s, &s.info_full[in], (j / kInfo) & 1, p.c.status);
       // what the scales have to say is here before the products are
       const float4 ks = *reinterpret_cast<const float4*>(&s.ks[in][4 * half]);
-      const float4 bias = *reinterpret_cast<const float4*>(&s.bias[in][4 * half]);
+      const float4 expo = *reinterpret_cast<const float4*>(&s.expo[in][4 * half]);
       const float4 back = *reinterpret_cast<const float4*>(&s.back[in][4 * half]);
       float k[4] = {factor(f, ks.x), factor(f, ks.y), factor(f, ks.z), factor(f, ks.w)};
       const bool partly = s.partly[in];
-      float down = s.less[in];
+      l *= s.more[in];
       // one warp of the tile looks for the products, the others wait for it: looks
       // share a queue with the exponentials
       if ((warp & 7) == 0) ok = ok && wait(s, &s.s_full[t], n & 1, p.c.status);
@@ -733,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (s.ve[in][4 * half + i / 16] == kNoBlock) v[i] = neg_inf();
         }
       }
-      float y[4];
+      float e[4] = {expo.x, expo.y, expo.z, expo.w}, y[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) y[q] = max3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
 #pragma unroll
@@ -741,18 +738,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) y[q] = max3(y[q], v[16 * q + i], v[16 * q + i + 1]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) y[q] = __fmul_rn(fmaxf(y[q], v[16 * q + 15]), k[q]);
+      for (int q = 0; q < 4; ++q) y[q] = __fmaf_rn(fmaxf(y[q], v[16 * q + 15]), k[q], e[q]);
       float x = fmaxf(max3(y[0], y[1], y[2]), y[3]);
       // the other half's; both have their products in registers from here on, so
       // P may take the place of S
       s.most[n & 1][half][slot] = x;
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       x = fmaxf(x, s.most[n & 1][half ^ 1][slot]);
+      float down = 1.0f;
       if (x > __fadd_rd(m, kHeadroom)) {
-        const float up = ceilf(x), d = m == neg_inf() ? 0.0f : pow2_down(m - up);
+        const float up = ceilf(x);
+        down = m == neg_inf() ? 0.0f : pow2_down(m - up);
         m = up;
-        l *= d;
-        down *= d;
+        l *= down;
       }
       float base = m == neg_inf() ? 0.0f : m;
       if (__builtin_expect(fabsf(base) > kFar, 0)) {
@@ -760,15 +758,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // against p's range: logits as they were rounded for m
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          // (two roundings: with mul2 and add2 they came out as one)
 #pragma unroll
           for (int i = 16 * q; i < 16 * q + 16; ++i)
-            v[i] = __fsub_rn(__fmul_rn(v[i], k[q]), base);
+            v[i] = __fsub_rn(__fmaf_rn(v[i], k[q], e[q]), base);
           k[q] = 1.0f;
+          e[q] = 0.0f;
         }
         base = 0.0f;
       }
-      const float off[4] = {bias.x - base, bias.y - base, bias.z - base, bias.w - base};
+      base -= kBias;
+      const float off[4] = {e[0] - base, e[1] - base, e[2] - base, e[3] - base};
       float sums[4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -795,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       l = fmaf(sums[1], back.y, l);
       l = fmaf(sums[2], back.z, l);
       l = fmaf(sums[3], back.w, l);
-      // the sums so far by the new maximum and exponent
+      // the sums so far by the new maximum
       if (n > 0 && __any_sync(0xffffffffu, down != 1.0f)) {
         constexpr int N = D / 2 < 32 ? D / 2 : 32;
 #pragma unroll
@@ -950,8 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* table = p.c.table + (int64_t)s.it.b * p.c.ld_table;
     const int blocks = 1 << (p.c.page_shift - 4);
     bool ok = true;
-    int expo = kNoExp;                  // E, the largest value scale so far
-    int old[2] = {expo, expo};          // E of the step before and of the one before that
+    int expo = kNoExp;                  // the largest exponent of a value scale so far
+    int old[2] = {c_of(expo), c_of(expo)};        // c of the step before and of the one before that
     for (int j0 = 0; ok && j0 < steps; j0 += 4) {
       const int tok = tok0 + j0 * kTile + lane * kKvBlock;
       bool there = tok <= high;
@@ -984,23 +983,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const bool mine = lane >> 3 == i, scaled = there && vb != 255;
         const int e = (int)vb - 127;
-        const int to = max(expo, __reduce_max_sync(0xffffffffu, mine && scaled ? e : -1000));
+        expo = max(expo, __reduce_max_sync(0xffffffffu, mine && scaled ? e : kNoExp));
+        const int c = c_of(expo);
         if (mine) {
-          const int shift = scaled ? max(e - to, kMinShift) : 0;
+          const int with = scaled ? max(e, expo - kSpread) : 0;
           s.ks[in][lane & 7] = e8m0_value(kb);
-          s.bias[in][lane & 7] = kBias + (float)shift;
-          s.back[in][lane & 7] = pow2(-shift);
+          s.expo[in][lane & 7] = (float)with;
+          s.back[in][lane & 7] = back_of(with, expo);
           s.ve[in][lane & 7] = !there ? kNoBlock : vb == 255 ? kNaNExp : e;
           s.page[in][lane & 7] = page;
         }
         if (lane == 0) {
           s.partly[in] = (have >> (8 * i) & 0xffu) != 0xffu;
-          const int then = twin ? old[1] : old[0];      // of the tile's step before
-          s.less[in] = then > -1000 ? pow2(max(then - to, -126)) : 1.0f;
-          s.top[(j0 + i) & 1] = to;
+          s.more[in] = pow2(c - (twin ? old[1] : old[0]));
+          s.c[(j0 + i) & 1] = c;
         }
         old[1] = old[0];
-        old[0] = expo = to;
+        old[0] = c;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.info_full[in]);
       }

@@ -18,15 +18,15 @@
 // FP16 tensor-core products with the tokens as rows (M) and the query rows as
 // columns (N, 8 at a time): S^T = K Q^T and O^T = V^T P^T, so that 8 rows a kv
 // head leave no part of an MMA unused. A code is exact in FP16, a query row too
-// once it is scaled by a power of two to a maximum below 2^15. Scales, being
-// powers of two, are applied outside the products: the keys' to the logits, the
-// values' to p.
+// once it is scaled by a power of two to a maximum below 2^15 (but for values under
+// 2^-31 of its largest, which are off by 2^-39 of that). Scales, being powers of two,
+// are applied outside the products: the keys' to the logits, the values' to p.
 //
 // Online softmax in base 2 with whole exponents: a row's m is raised only when a
 // logit passes m + 7, to the next whole number, so that every rescaling is by
-// an exact power of two and most steps have none. p = 2^(t - m + 8 + e - E), E
-// the largest exponent of the value scales so far and e this step's, stays below
-// 2^15; as FP16 it has 11 bits down to 2^-14. The sum of p is FP32.
+// an exact power of two and most steps have none. A value's scale is part of its logit
+// there ("a row's sums" in attention.cuh). p stays below 2^15; as FP16 it has 11 bits down
+// to 2^-14. The sum of p is FP32.
 //
 // The K order of both products is free, and so is the M order of the second, so
 // the fragments are what lies together: a lane's keys are 32 consecutive bytes of
@@ -55,8 +55,8 @@ constexpr int kRows = 16;               // of a tile
 constexpr int kUnit = 32;               // steps looked up at a time
 constexpr float kHeadroom = 7.0f;       // a row's m is raised past m + this
 constexpr float kBias = 8.0f;           // p is 2^kBias at m
-constexpr float kFar = 1048576.0f;      // past this m takes its own difference from a logit
-constexpr int kMinShift = -40;          // value scales below 2^-40 of the largest: as 2^-40
+constexpr float kFar = 1048576.0f;      // past this a logit's difference from m is taken first
+constexpr int kNoExp = -1000;           // of no value scale yet
 constexpr uint32_t kAbsent = 1u << 16;  // step's word: its page does not exist
 constexpr int kSeqs = 128;              // sequences that a block keeps beside their items
 
@@ -81,7 +81,7 @@ struct Smem {
   float o[kTeam][8 * NT][kPitch];
   alignas(16) __nv_bfloat16 q[2][8 * NT][D];
   float ml[kTeam][8 * NT][2];
-  int expo[kTeam];
+  int c[kTeam];
   alignas(16) int nan_at[2][D];
   Item item[2];
   uint64_t full[kStages], empty[kStages], item_full[2], item_empty[2], sums_full, sums_empty;
@@ -344,13 +344,12 @@ __device__ __forceinline__ void join_sums(const AttnParams& p, const Smem<D, NT>
   constexpr int PER = 128 / D;          // rows of a pass, 4 values to a lane
   const int d = lane * 4 % D, sub = lane * 4 / D;
   const Item& it = s.item[buf];
-  int top_e = s.expo[0];
+  int c = s.c[0];
 #pragma unroll
-  for (int w = 1; w < kTeam; ++w) top_e = max(top_e, s.expo[w]);
-  float less[kTeam];
+  for (int w = 1; w < kTeam; ++w) c = max(c, s.c[w]);
+  float more[kTeam];
 #pragma unroll
-  for (int w = 0; w < kTeam; ++w) less[w] = pow2(max(s.expo[w] - top_e, -126));
-  const float out_e = top_e > -1000 ? e8m0_value(top_e + 127) : 0.0f;
+  for (int w = 0; w < kTeam; ++w) more[w] = pow2(c - s.c[w]);
   const int4 nan_at = *reinterpret_cast<const int4*>(&s.nan_at[buf][d]);
   const bool parts = it.parts > 1;
   const int64_t part =
@@ -371,8 +370,8 @@ __device__ __forceinline__ void join_sums(const AttnParams& p, const Smem<D, NT>
 #pragma unroll
     for (int w = 0; w < kTeam; ++w) {
       // a warp that saw nothing has sums of 0, or of NaN
-      const float x = m[w] == neg_inf() ? 1.0f : pow2_down(m[w] - top), y = x * less[w];
-      l = fmaf(s.ml[w][r][1], x, l);
+      const float y = m[w] == neg_inf() ? 1.0f : pow2_down(m[w] - top);
+      l = fmaf(s.ml[w][r][1] * more[w], y, l);
       v.x = fmaf(u[w].x, y, v.x); v.y = fmaf(u[w].y, y, v.y);
       v.z = fmaf(u[w].z, y, v.z); v.w = fmaf(u[w].w, y, v.w);
     }
@@ -386,13 +385,15 @@ __device__ __forceinline__ void join_sums(const AttnParams& p, const Smem<D, NT>
       *reinterpret_cast<float4*>(p.parts + at * D + d) = v;
       if (d == 0)
         *reinterpret_cast<float4*>(p.part_ml + at * kPartWords) =
-            make_float4(top, l, __int_as_float(top_e), 0.0f);
+            make_float4(top, l, __int_as_float(c), 0.0f);
     } else {
-      const float scale = l == 0.0f ? 0.0f : out_e / l;
+      // (one after the other: 2^c / l may be below FP32's range where the result is not)
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, unit = pow2(c);
+      v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
       *reinterpret_cast<uint2*>(p.out + (int64_t)(it.row0 + tok) * p.ld_out +
                                 (it.h * p.group + gr - tok * p.group) * D + d) =
-          make_uint2(f32x2_to_bf16x2_bits(v.x * scale, v.y * scale),
-                     f32x2_to_bf16x2_bits(v.z * scale, v.w * scale));
+          make_uint2(f32x2_to_bf16x2_bits(v.x * unit, v.y * unit),
+                     f32x2_to_bf16x2_bits(v.z * unit, v.w * unit));
     }
   }
 }
@@ -465,7 +466,8 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
         m[nt][i] = neg_inf();
         l[nt][i] = 0.0f;
       }
-    int expo = -1000;                   // E; none yet
+    int expo = kNoExp;                  // largest exponent of a value scale so far
+    bool odd = true;                    // some row's m is -inf or far from 0
 
     for (int i = 0; i < steps; i += kTeam) {
       const uint32_t st = taken % S::kStages;
@@ -578,14 +580,29 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
         }
       }
 
-      // maxima: raised where a logit passes m + 7
+      // exponent of the value scale
+      int e = 0;
+      if (vbyte != 255) {
+        e = (int)vbyte - 127;
+        if (c_of(max(e, expo)) != c_of(expo)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) l[nt][r] *= pow2(c_of(64) - c_of(0));
+        }
+        expo = max(expo, e);
+        e = max(e, expo - kSpread);
+      }
+      const float ef = (float)e, back = back_of(e, expo);
+      // maxima: raised where a logit and e pass m + 7
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          raise |= fmaxf(sc[nt][r], sc[nt][2 + r]) > __fadd_rd(m[nt][r], kHeadroom);
+          raise |= __fadd_rn(fmaxf(sc[nt][r], sc[nt][2 + r]), ef) > __fadd_rd(m[nt][r], kHeadroom);
       if (__any_sync(0xffffffffu, raise)) {
+        odd = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -594,12 +611,14 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = __fadd_rn(x, ef);
             float d = 1.0f;
             if (x > __fadd_rd(m[nt][r], kHeadroom)) {
               const float to = ceilf(x);
               d = m[nt][r] == neg_inf() ? 0.0f : pow2_down(m[nt][r] - to);
               m[nt][r] = to;
             }
+            odd |= !(fabsf(m[nt][r]) <= kFar);
             l[nt][r] *= d;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
@@ -607,41 +626,25 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
               o[j][nt][2 + r] *= d;
             }
           }
+        odd = __any_sync(0xffffffffu, odd);
       }
-      // exponents of the value scales
-      int shift = 0;
-      if (vbyte != 255) {
-        const int e = (int)vbyte - 127;
-        if (e > expo) {
-          if (expo > -1000) {
-            const float d = pow2(max(expo - e, -126));
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[j][nt][k] *= d;
-          }
-          expo = e;
-        }
-        shift = max(e - expo, kMinShift);
-      }
-      const float back = pow2(-shift);
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float b[2];
+        float b0 = m[nt][0] - (kBias + ef), b1 = m[nt][1] - (kBias + ef);
+        if (odd) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float base = m[nt][r] == neg_inf() ? 0.0f : m[nt][r];
-          if (fabsf(base) > kFar) {     // (m - kBias may be rounded up or down by more than kBias)
-            sc[nt][r] -= base;
-            sc[nt][2 + r] -= base;
-            base = 0.0f;
+          for (int r = 0; r < 2; ++r) {
+            float& b = r ? b1 : b0;
+            if (m[nt][r] == neg_inf()) b = -(kBias + ef);
+            if (!(fabsf(m[nt][r]) <= kFar) && m[nt][r] != neg_inf()) {
+              // (m - kBias may be rounded up or down by more than kBias)
+              sc[nt][r] = __fadd_rn(sc[nt][r], ef) - m[nt][r];
+              sc[nt][2 + r] = __fadd_rn(sc[nt][2 + r], ef) - m[nt][r];
+              b = -kBias;
+            }
           }
-          b[r] = base - (kBias + (float)shift);
         }
-        const float b0 = b[0], b1 = b[1];
         const float p0 = ex2(sc[nt][0] - b0), p1 = ex2(sc[nt][1] - b1);
         const float p2 = ex2(sc[nt][2] - b0), p3 = ex2(sc[nt][3] - b1);
         l[nt][0] = fmaf(p0 + p2, back, l[nt][0]);
@@ -685,7 +688,7 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
           *reinterpret_cast<float4*>(at + 2 * j) =
               make_float4(o[j][nt][r], o[j][nt][2 + r], o[j + 1][nt][r], o[j + 1][nt][2 + r]);
       }
-    if (lane == 0) s.expo[warp] = expo;
+    if (lane == 0) s.c[warp] = c_of(expo);
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sums_full);
     if (!wait(s, &s.sums_full, turn & 1, p.c.status)) return;
@@ -713,7 +716,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   constexpr int C = kJoinSums / W;      // sums of a warp: w = warp, warp + W, ...
   constexpr int B = 8 / C;              // parts of each asked for at a time
   __shared__ float4 sums[kJoinSums][32];
-  __shared__ float weight[PER][kMaxSplits], inverse[PER];
+  __shared__ float weight[PER][kMaxSplits], inverse[PER], unit[PER];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L, d = lane % L * 4;
   const int heads = p.c.heads * p.group;
   uint32_t b = blockIdx.x * PER + sub;          // [sequence][token][head], below 2^30
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
       }
   };
   ask(0);
-  // maxima, sums and exponents, by the first warps, a row each: parts `lane` and
+  // m, l and c, by the first warps, a row each: parts `lane` and
   // `lane` + 32
   for (int k = warp; k < PER; k += W) {
     const float* from = reinterpret_cast<const float*>(
@@ -757,10 +760,10 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
     const int count = __shfl_sync(0xffffffffu, parts, k * L);
     float4 u[SL];
     float top = neg_inf();
-    int e = -1000;
+    int c = c_of(kNoExp);
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
-      u[i] = make_float4(neg_inf(), 0.0f, __int_as_float(-1000), 0.0f);
+      u[i] = make_float4(neg_inf(), 0.0f, __int_as_float(c), 0.0f);
       if (lane + 32 * i < count && count > 1)
         u[i] = __ldcg(reinterpret_cast<const float4*>(
             from + (int64_t)(lane + 32 * i) * p.part_rows * kPartWords));
@@ -768,22 +771,24 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       top = fmaxf(top, u[i].x);
-      e = max(e, __float_as_int(u[i].z));
+      c = max(c, __float_as_int(u[i].z));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    e = __reduce_max_sync(0xffffffffu, e);
+    c = __reduce_max_sync(0xffffffffu, c);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       const float y = u[i].x == neg_inf() ? 1.0f : pow2_down(u[i].x - top);
-      weight[k][lane + 32 * i] = y * pow2(max(__float_as_int(u[i].z) - e, -126));
-      sum = fmaf(u[i].y, y, sum);
+      weight[k][lane + 32 * i] = y;
+      sum = fmaf(u[i].y * pow2(c - __float_as_int(u[i].z)), y, sum);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-      inverse[k] = sum == 0.0f ? 0.0f : (e > -1000 ? e8m0_value(e + 127) : 0.0f) / sum;
+    if (lane == 0) {
+      inverse[k] = sum == 0.0f ? 0.0f : 1.0f / sum;
+      unit[k] = pow2(c);
+    }
   }
   __syncthreads();
   float4 v[C];
@@ -816,10 +821,11 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
     const float4 u = sums[i][lane];
     o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
   }
-  const float inv = inverse[sub];
+  const float inv = inverse[sub], by = unit[sub];
+  o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
   *reinterpret_cast<uint2*>(p.out + (int64_t)(row0 + tok) * p.ld_out + (int64_t)head * D + d) =
-      make_uint2(f32x2_to_bf16x2_bits(o.x * inv, o.y * inv),
-                 f32x2_to_bf16x2_bits(o.z * inv, o.w * inv));
+      make_uint2(f32x2_to_bf16x2_bits(o.x * by, o.y * by),
+                 f32x2_to_bf16x2_bits(o.z * by, o.w * by));
 }
 
 template <int D, int NT>

@@ -1,5 +1,6 @@
 """Attention at the ends of its ranges: NaN scales of tokens that some rows do not see, sequences
-with no tokens, logits far beyond what FP32 tells apart."""
+with no tokens, logits far beyond what FP32 tells apart, values whose scales lie far apart or
+are as small as they get."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +86,94 @@ def test_logits_that_fp32_holds_in_steps(length, hq, size):
         top = x[see] == x[see].max()
         want, mag = v[see][top].mean(0), np.abs(v[see][top]).mean(0)
         assert (np.abs(got[i] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mag).all(), i
+
+
+def exact(b, s, q, scale):
+    """(out, tolerance) of sequence s from what its rows see: half a step of bf16; twice, as
+    in the sum of the weights too, 2^-11 of FP16 weights and 2^-16 of a logit's magnitudes
+    (and 2^-17 of the row's largest query value times the keys' magnitudes where a query is
+    two e4m3 numbers); of weights under 2^-14 half a step of 2^-24, times 448 of their block's
+    scale, where the largest of weight times scale is 2^7 at least: 2^-32 times 448."""
+    n, kv = b.lengths[s]
+    k, v = ref.held(b.codes, b.scales, b.table[s], kv)
+    j = np.arange(kv)
+    page, block = b.table[s, j // b.page], j % b.page // 16
+    x = f64(q)[b.cu[s]:b.cu[s + 1]]
+    out, tol = np.zeros(x.shape), np.zeros(x.shape)
+    group = b.hq // b.hkv
+    for h in range(b.hq):
+        kk, vv = k[:, h // group], v[:, h // group]
+        unit = 2.0 ** (b.scales[page, 1, h // group, block] - 127.0)
+        for i in range(n):
+            see = slice(0, kv - n + i + 1)
+            t = kk[see] @ x[i, h] * scale
+            p = np.exp(t - t.max())
+            p /= p.sum()
+            logit = 2.0 ** -16 * abs(scale) * (np.abs(kk[see]) @ np.abs(x[i, h])).max()
+            if n * group > 64:
+                logit += 2.0 ** -17 * abs(scale) * np.abs(kk[see]).sum(-1).max() * np.abs(x[i, h]).max()
+            out[i, h] = p @ vv[see]
+            tol[i, h] = (2.0 ** -8 * np.abs(out[i, h]) + 2 * (2.0 ** -11 + logit) * (p @ np.abs(vv[see])) +
+                         kv * 2.0 ** -32 * 448 * (p * unit[see]).max())
+    return out, tol
+
+
+def close(b, q, got, scale=None):
+    got = f64(got)
+    for s in range(len(b.lengths)):
+        out, tol = exact(b, s, q, b.D ** -0.5 if scale is None else scale)
+        err = np.abs(got[b.cu[s]:b.cu[s + 1]] - out)
+        bad = ~(err <= tol)
+        assert not bad.any(), (s, bad.sum(), np.argwhere(bad)[0], got[b.cu[s]:b.cu[s + 1]][bad][0],
+                               out[bad][0], tol[bad][0])
+
+
+@pytest.mark.parametrize("apart", [12, 24, 34, 45, 80])
+@pytest.mark.parametrize("length,hq", ROWS)
+def test_values_of_tokens_that_a_row_does_not_see(length, hq, apart):
+    """The last tokens' values are 2^`apart` times the others': rows before them keep all
+    their bits."""
+    need_gpu()
+    n, kv = length
+    b = Batch([length], hq, 1, 128, 32, seed=42).fill()
+    for j in range((kv - 20) // 16 * 16, kv, 16):
+        page, block = at(b, 0, j)
+        b.scales[page, 1, 0, block] += apart
+    q = b.rows(hq, 0.5)
+    close(b, q, b.attend(q))
+
+
+@pytest.mark.parametrize("apart", [12, 24, 34, 45, 80, -34, -80])
+@pytest.mark.parametrize("length,hq", ROWS)
+def test_values_of_the_tokens_that_carry_the_weight(length, hq, apart):
+    """Two tokens in three have nearly no weight (exp(-280)) and values 2^`apart` times those
+    of the third, which make up the result."""
+    need_gpu()
+    n, kv = length
+    b = Batch([length], hq, 1, 128, 32, seed=43).fill()
+    for j in range(kv):
+        page, block = at(b, 0, j)
+        b.scales[page, 0, 0, block] = 127 - 4
+        if j // 16 % 3 != 0:
+            b.codes[page, 0, 0, j % 32, 5] = 0xf0           # -128
+            if j % 16 == 0:
+                b.scales[page, 1, 0, block] = int(b.scales[page, 1, 0, block]) + apart
+        else:
+            b.codes[page, 0, 0, j % 32, 5] = 0x70           # 128
+    q = b.rows(hq, 2.0 ** -6).float()
+    q[:, :, 5] = 17.5
+    q = q.bfloat16()
+    close(b, q, b.attend(q, scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("byte", [2, 7, 9, 30, 190, 191, 246])
+def test_the_smallest_and_largest_scales_over_long_contexts(byte):
+    """Positive values of around 2^-118 and less, or 2^119, a sum of weights of 2^22 and
+    more."""
+    need_gpu()
+    for length, hq in (((1, 40000), 2), ((1, 5000), 2), ((20, 2000), 4), ((2, 300), 1), ((150, 150), 1)):
+        b = Batch([length], hq, 1, 64, 64, seed=44).fill()
+        b.scales[:, 1] = byte
+        b.codes[:, 1] &= 0x7f
+        q = b.rows(hq, 0.3)
+        close(b, q, b.attend(q))
