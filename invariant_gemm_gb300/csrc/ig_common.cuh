@@ -262,7 +262,14 @@ __device__ __forceinline__ float bf16_round_f32(float f) {
 // previous kernel on the stream has finished; griddep_wait() blocks until that
 // kernel has completed and its memory is visible. Every kernel here reads
 // activations, z, y and workspace state, and writes anything, only after
-// griddep_wait(). griddep_launch() lets the next kernel start launching:
+// griddep_wait(), but for two of the attention: the split kernel behind a prompt
+// kernel, which does all its work before its wait, and the split kernel's join, which
+// reads the batch's lengths before it. Both rest on the first kernel of the call (the
+// prompt kernel, or the split kernel where there is none) calling griddep_launch() only
+// after its own wait: those behind it start later, so all that was before the call is
+// there. They read nothing before their wait that the kernels between write, and
+// the prompt's and the split kernel's rows, parts and counters are apart.
+// griddep_launch() lets the next kernel start launching:
 // the warp-level tensor-core kernels (and the pairwise-tree combine) call it
 // first thing, so that the next layer's blocks are resident and through
 // their prologue (tile entry, weight copies) by the time this grid

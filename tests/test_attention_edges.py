@@ -1,11 +1,12 @@
 """Attention at the ends of its ranges: NaN scales of tokens that some rows do not see, sequences
 with no tokens, logits far beyond what FP32 tells apart, values whose scales lie far apart or
-are as small as they get."""
+are as small as they get, lengths that change between replays."""
 import numpy as np
 import pytest
 import torch
 
-from attention_helpers import Batch, f64
+import invariant_gemm_gb300 as ig
+from attention_helpers import B16, I32, Batch, f64
 from helpers import need_gpu
 from oracle import attention as ref
 
@@ -177,3 +178,66 @@ def test_the_smallest_and_largest_scales_over_long_contexts(byte):
         b.codes[:, 1] &= 0x7f
         q = b.rows(hq, 0.3)
         close(b, q, b.attend(q))
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (64, 4, 4)])
+def test_lengths_that_change_between_replays(D, hq, hkv):
+    """One captured call of an append and the attention behind it: single tokens, prompts cut
+    into parts and not, sequences of both kernels and empty ones, as the lengths on the device
+    say at the time. Bit for bit what an eager run in a workspace of its own gives."""
+    need_gpu()
+    T, most, longest = 310, 300, 3000
+    b = Batch([(0, longest)] * 4, hq, hkv, D, 64, seed=47).fill(spread=1)
+    codes, scales, _, _, table = b.device_args()
+    start = codes.clone(), scales.clone()
+    x = torch.randn(T, hq + 2 * hkv, D, device="cuda").bfloat16()
+    q, k, v = x.split([hq, hkv, hkv], 1)
+    cu, kv = (torch.zeros(n, dtype=I32, device="cuda") for n in (5, 4))
+    q_out, out = (torch.zeros(T, hq, D, dtype=B16, device="cuda") for _ in range(2))
+    w = torch.ones(D, device="cuda").bfloat16()
+
+    def run(ws):
+        ig.kv_append(k, v, codes, scales, cu, kv, table, ws, w_k=w, q=q, q_out=q_out, w_q=w, max_q=most)
+        ig.paged_attention(q_out, codes, scales, cu, kv, table, out, ws, max_q=most)
+
+    def put(lengths):
+        cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum([n for n, _ in lengths])]), dtype=I32))
+        kv.copy_(torch.tensor([m for _, m in lengths], dtype=I32))
+        for t, s in zip((codes, scales), start):
+            t.copy_(s)
+        out.fill_(7.0)
+        q_out.fill_(7.0)
+
+    ws, other = (ig.attention_workspace(q, codes, table, most) for _ in range(2))
+    put([(1, 5)] * 4)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        run(ws)
+    for lengths in ([(1, 900), (200, 2900), (40, 40), (1, 1)], [(1, 5)] * 4,
+                    [(300, 300), (1, 3000), (0, 0), (2, 70)], [(0, 0), (0, 17), (129, 3000), (90, 90)],
+                    [(70, 3000)] * 4, [(16, 1024), (17, 17), (20, 2000), (100, 100)],
+                    [(0, 0)] * 4, [(100, 60), (80, 2999), (65, 65), (64, 64)]):
+        put(lengths)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (out, q_out, codes, scales)]
+        put(lengths)
+        run(other)
+        assert all(torch.equal(g, t) for g, t in zip(got, (out, q_out, codes, scales))), lengths
+        used = sum(n for n, _ in lengths)
+        assert (out[used:] == 7).all() and not (out[:used] == 7).all(-1).any()
+        one = Batch(lengths, hq, hkv, D, 64)
+        one.table, one.pages = b.table, b.pages
+        one.codes, one.scales = codes.cpu().numpy(), scales.cpu().numpy()
+        one.check(q_out[:used], out[:used])
+    assert ig.check_status(ws) == 0 and ig.check_status(other) == 0
+
+
+@pytest.mark.parametrize("kv", [32767, 32768, 32769, 65537])
+def test_where_parts_grow(kv):
+    """64 parts of 512 tokens are the most; behind them parts of 1024, then 1536."""
+    need_gpu()
+    b = Batch([(1, kv), (2, kv - 5)], 4, 1, 64, 128, seed=kv).fill()
+    q = b.rows(4, 2.0)
+    b.check(q, b.attend(q))
