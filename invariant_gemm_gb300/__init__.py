@@ -706,7 +706,8 @@ def kv_gather(cache, scales, cu, kv_len, page_table, k_out, v_out, ws, *, stream
 def attention_workspace(q, cache, page_table, max_q=None):
     """Allocate (with torch) a workspace for paged_attention over up to the rows
     of q, the sequences and pages of page_table and max_q new tokens of one
-    sequence (None: as many as q has). It serves the other calls as well."""
+    sequence (None: as many as q has, three times the bytes of max_q=1 for 256
+    sequences of a token each). It serves the other calls as well."""
     import torch
     T, hq, D = q.shape
     _, _, heads, page, Dc = cache.shape

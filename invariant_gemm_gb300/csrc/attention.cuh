@@ -64,13 +64,13 @@ struct AttnParams {
   __nv_bfloat16* out;
   uint32_t* next;       // [0] items of the split kernel taken beyond each block's first,
                         // [1] whether the prompt kernel cut a sequence; 0 between calls
-  float* parts;         // results of parts [sequence][tile][kv head][part][row][D]
-  float* part_ml;       // [sequence][tile][kv head][part][row][kPartWords]
-  float* big;           // the prompt kernel's parts [sequence][item][row][D]
-  float* big_ml;        // [sequence][item][row][kPartWords]
+  float* parts;         // results of parts [first_tile + tile][kv head][part][row][D]
+  float* part_ml;       // [first_tile + tile][kv head][part][row][kPartWords]
+  float* big;           // the prompt kernel's parts [first_big + row of an item][D]
+  float* big_ml;        // [first_big + row of an item][kPartWords]
   int64_t ld_q, ld_out;
-  int32_t big_rows;     // rows that an item has room for
-  int32_t big_by_row;   // see big_place
+  int32_t big_rows;     // rows of an item of the prompt kernel's parts at most; 0: no parts
+  int32_t big_by_row, tiles_by_row;     // see first_big, first_tile
   int32_t heads_q, group;   // query heads, and of one kv head
   uint32_t group_inv;   // 65536 / group, rounded up: row / group for few rows
   uint32_t group_magic, heads_magic;    // see divide
@@ -90,7 +90,7 @@ struct AttnJoinParams {
   const float* parts;
   const float* part_ml;
   int64_t ld_out;
-  int32_t group, few_rows, tokens, max_tiles, max_parts, part_rows, big_by_row;
+  int32_t group, few_rows, tokens, max_tiles, max_parts, part_rows, by_row;
 };
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, cudaStream_t st);
@@ -148,12 +148,19 @@ __host__ __device__ inline int prompt_parts(int64_t rows, int kv, int heads) {
   if (parts > kPromptParts) parts = kPromptParts;
   return parts < 1 ? 1 : parts;
 }
-// Place of a sequence that the prompt kernel cuts in the workspace: its number or, where
-// there are more sequences than can have over kFewRows rows, by where its rows begin
-// (two such sequences' rows begin kFewRows + 1 apart at least).
-__host__ __device__ inline int64_t big_place(bool by_row, int b, int64_t row0, int group) {
-  return by_row ? row0 * group / (kFewRows + 1) : b;
+// Where a sequence's parts are in the workspace: its first tile of the split kernel's,
+// and its first row of the prompt kernel's (kPromptItems items at most, of item_rows rows
+// each). By its number, or by where its rows begin where the rows of all sequences are too
+// few for every one to have the most.
+__host__ __device__ inline int64_t first_tile(bool by_row, int b, int64_t row0, int group,
+                                              int max_tiles) {
+  return by_row ? b + row0 * group / 16 : (int64_t)b * max_tiles;
 }
+__host__ __device__ inline int64_t first_big(bool by_row, int b, int64_t row0, int group,
+                                             int big_rows) {
+  return (by_row ? row0 * group : (int64_t)b * big_rows) * kPromptItems;
+}
+__host__ __device__ inline int item_rows(int rows) { return rows < kPromptRows ? rows : kPromptRows; }
 // Steps to a part.
 __host__ __device__ inline int prompt_len(int kv, int parts) {
   return ((kv + kPromptStep - 1) / kPromptStep + parts - 1) / parts;

@@ -143,7 +143,7 @@ int rope_params(const ig_rope_shape* s, const void* q, const void* k, const void
 // counters (of which it uses two).
 struct AttnPlan {
   int group, max_tiles, max_parts, part_rows;
-  int big_rows, big_by_row;
+  int big_rows, big_by_row, tiles_by_row;
   size_t ml_at, big_at, big_ml_at, total;    // behind the counters
 };
 
@@ -167,7 +167,11 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
   pl->part_rows = (int)(rows < 16 ? rows : 16);
   const int64_t cap = b->ld_table * c->page;
   pl->max_parts = cap < 256 * kMaxSplits ? (int)((cap + 255) / 256) : kMaxSplits;
-  const int64_t items = (int64_t)b->batch * pl->max_tiles * c->heads * pl->max_parts;
+  const int64_t many = s->T * pl->group;        // rows of all sequences
+  int64_t tiles = (int64_t)b->batch * pl->max_tiles;
+  pl->tiles_by_row = b->batch + many / 16 < tiles;
+  if (pl->tiles_by_row) tiles = b->batch + many / 16;
+  const int64_t items = tiles * c->heads * pl->max_parts;
   if (items > (1ll << 30)) return IG_ERR_UNSUPPORTED;
   pl->ml_at = align_up((size_t)items * pl->part_rows * c->head_dim * 4, 256);
   pl->big_at = align_up(pl->ml_at + (size_t)items * pl->part_rows * kPartWords * 4, 256);
@@ -175,15 +179,13 @@ int attn_plan(const ig_attn_shape* s, const ig_kv_cache* c, const ig_batch* b, A
   // few enough tiles, long enough
   pl->big_rows = pl->big_by_row = 0;
   int64_t big = 0;
-  if (rows > kFewRows && s->T * pl->group > kFewRows &&
-      prompt_parts(kFewRows + 1, (int)cap, c->heads) > 1) {
-    const int64_t places = s->T * pl->group / (kFewRows + 1) + 1;
-    pl->big_by_row = places < b->batch;
-    pl->big_rows = (int)(rows < kPromptRows ? rows : kPromptRows);
-    big = (pl->big_by_row ? places : b->batch) * kPromptItems * pl->big_rows;
+  if (rows > kFewRows && many > kFewRows && prompt_parts(kFewRows + 1, (int)cap, c->heads) > 1) {
+    pl->big_rows = item_rows((int)rows);
+    const int64_t most = (int64_t)b->batch * pl->big_rows;
+    pl->big_by_row = many < most;
+    big = (many < most ? many : most) * kPromptItems;
   }
   // (blocks of the prompt kernel: as its launch counts them)
-  const int64_t many = s->T * pl->group;
   if ((many / kPromptRows + b->batch) * c->heads + (int64_t)b->batch * kPromptItems >= 1ll << 31)
     return IG_ERR_UNSUPPORTED;
   pl->big_ml_at = align_up(pl->big_at + (size_t)big * c->head_dim * 4, 256);
@@ -311,6 +313,7 @@ int ig_paged_attention(const ig_attn_shape* shape, const ig_kv_cache* cache,
   p.big_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMapOffset + pl.big_ml_at);
   p.big_rows = pl.big_rows;
   p.big_by_row = pl.big_by_row;
+  p.tiles_by_row = pl.tiles_by_row;
   p.ld_q = shape->ld_q;
   p.ld_out = shape->ld_out;
   p.heads_q = shape->heads_q;

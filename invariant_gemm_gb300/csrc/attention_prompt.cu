@@ -495,10 +495,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const Attn
       const int parts = prompt_seen(kv - n + last / p.group, len);
       const bool in = h0 + sub < heads && parts > 1;
       // item (tiles - 1 - tile, part, kv head) of the sequence
-      const int64_t first = big_place(p.big_by_row, b, row0, p.group) * kPromptItems +
-                            (tiles - 1 - tile) * cut * p.c.heads + h / p.group;
-      const int64_t pitch = (int64_t)p.c.heads * p.part_rows;
-      const int64_t at = first * p.part_rows + r % kPromptRows;
+      const int room = item_rows(n * p.group);
+      const int64_t pitch = (int64_t)p.c.heads * room;
+      const int64_t at = first_big(p.by_row, b, row0, p.group, p.part_rows) +
+                         (int64_t)((tiles - 1 - tile) * cut * p.c.heads + h / p.group) * room +
+                         r % kPromptRows;
       uint4 x[kPromptParts];
 #pragma unroll
       for (int q = 0; q < kPromptParts; ++q) {
@@ -633,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.parts = prompt_seen(it.high, len);
             it.step0 = part * len;
             it.steps = max(0, min(it.steps, it.step0 + len) - it.step0);
-            it.part = (big_place(p.big_by_row, first, row0, p.group) * kPromptItems + item) *
-                      p.big_rows;
+            it.part = first_big(p.big_by_row, first, row0, p.group, p.big_rows) +
+                      (int64_t)item * item_rows(n * p.group);
           }
           it.b = part < it.parts ? first : -1;
           s.it = it;
@@ -1133,7 +1134,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t st) {
   j.group = p.group;
   j.few_rows = p.few_rows;
   j.part_rows = p.big_rows;
-  j.big_by_row = p.big_by_row;
+  j.by_row = p.big_by_row;
   constexpr int PER = kJoinWarps * 128 / D;             // heads to a block at a time
   const int64_t items = p.c.T * ((p.heads_q + PER - 1) / PER), most = 4 * sm_count();
   return launch_pdl(prompt_join_kernel<D>, dim3((unsigned)(items < most ? items : most)),

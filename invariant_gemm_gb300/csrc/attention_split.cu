@@ -353,8 +353,8 @@ __device__ __forceinline__ void join_sums(const AttnParams& p, const Smem<D, NT>
   const int4 nan_at = *reinterpret_cast<const int4*>(&s.nan_at[buf][d]);
   const bool parts = it.parts > 1;
   const int64_t part =
-      ((((int64_t)it.b * p.max_tiles + it.tile) * p.c.heads + it.h) * p.max_parts + it.split) *
-      p.part_rows;
+      (((first_tile(p.tiles_by_row, it.b, it.row0, p.group, p.max_tiles) + it.tile) * p.c.heads +
+        it.h) * p.max_parts + it.split) * p.part_rows;
 #pragma unroll
   for (int i = 0; i < 2 * NT; i += PER) {
     const int r = i / PER * kTeam * PER + warp * PER + sub;
@@ -737,7 +737,9 @@ __global__ void __launch_bounds__(32 * W) join_kernel(const AttnJoinParams p) {
   if (!__any_sync(0xffffffffu, in)) return;         // the same in all warps
   if (!in) parts = 1;
   const int64_t first =
-      in ? (((int64_t)b * p.max_tiles + tile) * p.c.heads + head / p.group) * p.max_parts : 0;
+      in ? ((first_tile(p.by_row, (int)b, row0, p.group, p.max_tiles) + tile) * p.c.heads +
+            head / p.group) * p.max_parts
+         : 0;
   const float* ml = p.part_ml + (first * p.part_rows + r % kRows) * kPartWords;
   const float* at = p.parts + (first * p.part_rows + r % kRows) * D + d;
   uint4 x[B][C];
@@ -922,6 +924,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t st) {
   j.group = p.group;
   j.few_rows = p.few_rows;
   j.max_tiles = p.max_tiles;
+  j.by_row = p.tiles_by_row;
   j.max_parts = p.max_parts;
   j.part_rows = p.part_rows;
   const int most = p.few_rows / p.group;              // tokens of a sequence of this kernel

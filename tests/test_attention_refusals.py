@@ -248,3 +248,25 @@ def test_structs_match_the_header():
     """Sizes as a C compiler lays them out (8-byte alignment, no tail padding lost)."""
     assert len(rope()) == 72 and len(cache()) == 56 and len(batch()) == 40 and len(attn()) == 40
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_workspace_follows_the_rows():
+    """Not every sequence can have the most new tokens: 256 sequences, 64 query and 8 kv heads
+    of 128, tables of 65536 tokens."""
+    def size(T, max_q, B=256):
+        return ig.lib().ig_attention_workspace_bytes(
+            attn(T=T, hq=64, ld_q=8192, ld_o=8192),
+            cache(codes=0, scales=0, pages=0, ps=0, ss=0, page=64, heads=8), batch(
+                0, 0, 0, cols=1024, B=B, max_q=max_q))
+
+    row = 4 * (128 + 4)                         # of a part: sums, maximum, sum of weights
+
+    def close(got, rows):
+        assert rows * row <= got <= rows * row + (1 << 20)
+
+    close(size(256, 1), 256 * 8 * 64 * 8)       # single tokens: 8 rows in 64 parts of 8 heads
+    # no bound on new tokens given: tiles of 16 rows as 256 sequences of 2048 rows can fill them,
+    # 152 items for the prompts' rows
+    close(size(256, 256), (256 + 128) * 8 * 64 * 16 + 2048 * 152)
+    close(size(2304, 2048), 256 * 4 * 8 * 64 * 16 + 2304 * 8 * 152)
+    close(size(2304, 2048, 16), 16 * 4 * 8 * 64 * 16 + 16 * 256 * 152)
