@@ -55,7 +55,7 @@ constexpr int kRows = 16;               // of a tile
 constexpr int kUnit = 32;               // steps looked up at a time
 constexpr float kHeadroom = 7.0f;       // a row's m is raised past m + this
 constexpr float kBias = 8.0f;           // p is 2^kBias at m
-constexpr float kFar = 1048576.0f;      // past this a logit's difference from m is taken first
+constexpr float kMost = 15.0f;          // of p's exponent: kHeadroom + kBias
 constexpr int kNoExp = -1000;           // of no value scale yet
 constexpr uint32_t kAbsent = 1u << 16;  // step's word: its page does not exist
 constexpr int kSeqs = 128;              // sequences that a block keeps beside their items
@@ -103,6 +103,14 @@ __device__ __forceinline__ float pow2_down(float d) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// An exponent of p: logits past 2^22 come in steps by which it could pass what FP16 has (at
+// the largest logit it is off by one of them at most, and not below 0 from steps of 16 on).
+// NaN stays.
+__device__ __forceinline__ float at_most(float x) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(kMost));
   return r;
 }
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
@@ -467,7 +475,6 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
         l[nt][i] = 0.0f;
       }
     int expo = kNoExp;                  // largest exponent of a value scale so far
-    bool odd = true;                    // some row's m is -inf or far from 0
 
     for (int i = 0; i < steps; i += kTeam) {
       const uint32_t st = taken % S::kStages;
@@ -600,9 +607,8 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          raise |= __fadd_rn(fmaxf(sc[nt][r], sc[nt][2 + r]), ef) > __fadd_rd(m[nt][r], kHeadroom);
+          raise |= fmaxf(sc[nt][r], sc[nt][2 + r]) > m[nt][r] + (kHeadroom - ef);
       if (__any_sync(0xffffffffu, raise)) {
-        odd = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -611,14 +617,13 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = __fadd_rn(x, ef);
+            x += ef;
             float d = 1.0f;
-            if (x > __fadd_rd(m[nt][r], kHeadroom)) {
+            if (x > m[nt][r] + kHeadroom) {
               const float to = ceilf(x);
               d = m[nt][r] == neg_inf() ? 0.0f : pow2_down(m[nt][r] - to);
               m[nt][r] = to;
             }
-            odd |= !(fabsf(m[nt][r]) <= kFar);
             l[nt][r] *= d;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
@@ -626,27 +631,14 @@ __device__ void compute_warp(const AttnParams& p, Smem<D, NT>& s, const uint8_t*
               o[j][nt][2 + r] *= d;
             }
           }
-        odd = __any_sync(0xffffffffu, odd);
       }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float b0 = m[nt][0] - (kBias + ef), b1 = m[nt][1] - (kBias + ef);
-        if (odd) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float& b = r ? b1 : b0;
-            if (m[nt][r] == neg_inf()) b = -(kBias + ef);
-            if (!(fabsf(m[nt][r]) <= kFar) && m[nt][r] != neg_inf()) {
-              // (m - kBias may be rounded up or down by more than kBias)
-              sc[nt][r] = __fadd_rn(sc[nt][r], ef) - m[nt][r];
-              sc[nt][2 + r] = __fadd_rn(sc[nt][2 + r], ef) - m[nt][r];
-              b = -kBias;
-            }
-          }
-        }
-        const float p0 = ex2(sc[nt][0] - b0), p1 = ex2(sc[nt][1] - b1);
-        const float p2 = ex2(sc[nt][2] - b0), p3 = ex2(sc[nt][3] - b1);
+        const float b0 = (m[nt][0] == neg_inf() ? 0.0f : m[nt][0]) - (kBias + ef);
+        const float b1 = (m[nt][1] == neg_inf() ? 0.0f : m[nt][1]) - (kBias + ef);
+        const float p0 = ex2(at_most(sc[nt][0] - b0)), p1 = ex2(at_most(sc[nt][1] - b1));
+        const float p2 = ex2(at_most(sc[nt][2] - b0)), p3 = ex2(at_most(sc[nt][3] - b1));
         l[nt][0] = fmaf(p0 + p2, back, l[nt][0]);
         l[nt][1] = fmaf(p1 + p3, back, l[nt][1]);
         pb[nt][0] = transpose8(f16x2_of(p0, p1));
