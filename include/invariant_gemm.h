@@ -478,7 +478,8 @@ typedef struct ig_kv_cache {
 } ig_kv_cache;
 
 typedef struct ig_batch {
-  const int32_t* cu;         /* [batch + 1], not falling */
+  const int32_t* cu;         /* [batch + 1], not falling (where it falls, rows of the
+                                sequences around are unspecified) */
   const int32_t* kv_len;     /* [batch] tokens in all, the new ones among them */
   const int32_t* page_table; /* [batch][ld_table] */
   int64_t ld_table;          /* pages that a row of page_table can name */
@@ -506,8 +507,9 @@ int ig_qk_norm_rope(const ig_rope_shape* shape, const void* q, const void* k, co
  * smallest 2^e, e >= -120, with max|value| <= 448 2^e over the finite values of
  * its new tokens; where older tokens of the sequence are in the block it is at
  * least their scale, and where it grew they are divided by as much. Values are
- * rounded to nearest, ties to even (keys that FP32 cannot tell from the middle
- * between two codes by their FP64 values); what is not finite is held as NaN.
+ * rounded to nearest, ties to even (keys of 2^-6 scale or more that FP32 cannot
+ * tell from the middle between two codes by their FP64 values; smaller keys, and the
+ * largest one for the scale, as FP32 has them); what is not finite is held as NaN.
  * Rows of the block behind the last token keep their bytes.
  * A block that is written must be one token range of one sequence: not shared
  * by two sequences, nor on a page that the page table names twice (its bytes are

@@ -115,7 +115,8 @@ int encode_map_codes(CUtensorMap* map, const void* base, int head_dim, uint64_t 
 // of 128: 32 rows 306 us by the one, 399 by the other, 64 rows 575 and 468; 64 rows of
 // one sequence of 40000 89 and 44, of four of up to 1000 with 32 query heads 22 and 24, of
 // one of 60000 with 8 query and 2 kv heads of 64 32 and 47. Fewer rows stay with the split
-// kernel all the more: 20 over 500 tokens 13 and 21.)
+// kernel all the more: 20 over 500 tokens 13 and 21. The number of rows alone is not the
+// best rule at the border: with 8 kv heads and long contexts 64 rows are slower by it.)
 constexpr int kFewRows = 64;
 
 // --- splitting a sequence ---------------------------------------------------
@@ -178,9 +179,9 @@ __host__ __device__ inline int prompt_seen(int high, int len) {
 // that the row does not see. The products sum to 2^(8 - m) sum 2^t v, and
 // l = sum p 2^(c - e) = 2^(8 - m + c) sum 2^t, so the result is their quotient times 2^c.
 // Powers of two round nothing, and c is a matter of FP32's range alone: with -40 up to
-// scales of 2^63, then 40, l is between 2^-95 and 2^102 times the number of tokens where
-// scales are less than 2^kSpread apart (a smaller one counts as 2^-kSpread of the largest
-// so far, or p could be 0 of a token that has its part in l).
+// scales of 2^63, then 40, l is at least 2^-96 and at most 2^111 for each token where
+// scales are no more than 2^kSpread apart (a smaller one counts as 2^-kSpread of the
+// largest so far, or p could be 0 of a token that has its part in l).
 constexpr int kSpread = 120;
 __host__ __device__ constexpr int c_of(int largest_e) { return largest_e < 64 ? -40 : 40; }
 

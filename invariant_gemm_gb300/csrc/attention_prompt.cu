@@ -31,8 +31,8 @@
 // other tile's. Beside its steps a block costs 23000 clocks: 2400 to find its rows,
 // 9000 to load and convert 64 KB of queries, 1900 to the first products, 2300 from the
 // last P to the last sums, 5500 for the results, 2100 to the next block. 2048 tokens over
-// 32768 (32 query, 8 kv heads of 128): 871 us, 1220 TFLOP/s; three prompts of up to 4095
-// tokens 214 us.
+// 32768 (32 query, 8 kv heads of 128): 884 us, 1205 TFLOP/s; three prompts of up to 4095
+// tokens 217 us.
 #include "attention.cuh"
 #include "umma_mx4.cuh"
 
@@ -756,7 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float base = m == neg_inf() ? 0.0f : m;
       if (__builtin_expect(fabsf(base) > kFar, 0)) {
         // m is a rounded logit, and what the product below has beyond it is no longer small
-        // against p's range: logits as they were rounded for m
+        // against p's range: logits as they were rounded for m. (That such rows are asked
+        // for costs 1.1 %: 2048 tokens over 8192 222.4 us without, 224.9 with.)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
 #pragma unroll

@@ -5,7 +5,7 @@
 // tile. A work item is one tile, one kv head and one part of the sequence's
 // tokens (split_tokens). Items go to whichever block asks first (a counter in the
 // workspace), of blocks that stay: three to an SM where a tile has 8 rows at most,
-// else two. In a block four warps compute and one copies ahead:
+// else two (heads of 64: four and three). In a block four warps compute and one copies ahead:
 //   copies   pages and scales of the part, a step of 16 tokens (a block of the
 //            cache) to a lane, asked for while the part before is on its way;
 //            then one TMA box for a step's keys and one for its values, four
@@ -39,7 +39,7 @@
 // calls are the chain start - lengths (0.9 us) - pages, queries, copies (1.8) - products of
 // four steps to a warp (2.7) - join of the warps (0.6) - join of the parts (2): 777 tokens
 // 8.9 us. With more than 16 rows each tile reads and converts the tokens again, from L2:
-// 32 rows 305 us where 8 take 113. (Tiles of 32 rows, queries in shared memory, one block
+// 32 rows 302 us where 8 take 114. (Tiles of 32 rows, queries in shared memory, one block
 // of 254 registers to an SM: 434 us.)
 #include "attention.cuh"
 #include "warp_mma.cuh"
