@@ -15,7 +15,9 @@ M * layers / step time, deterministic Split-K = 8, inputs resident in HBM.
 Also reported: the atomic Split-K = 8 and unsplit variants, a sweep over
 M in {1, 8, 32, 128, 256}, HBM GB/s of the algorithmic bytes, the dominant
 kernel's roofline, the end-to-end number with host buffers, and the FP64
-oracle timed on the host cores.
+oracle timed on the host cores. `--details FILE` keeps the tables that are too long
+for the line: the sweep over M of every variant, the whole prefill grid, the same
+bytes through a plain kernel and the oracle by configuration.
 
 `--impl reference` times the FP64 CPU oracle on the same workload instead.
 """
@@ -886,6 +888,37 @@ def reference_main(args, rank, world):
 # size-dependent copy ceiling (context for the roofline fractions)
 # ---------------------------------------------------------------------------
 
+# tables that make the result's line longer than what keeps the end of an output may hold:
+# into the file that --details names
+DETAILS = ("sweep_M", "prefill", "same_bytes_ceiling")
+
+
+def six_digits(v):
+    if isinstance(v, float):
+        return float(f"{v:.6g}")
+    if isinstance(v, dict):
+        return {k: six_digits(x) for k, x in v.items()}
+    if isinstance(v, (list, tuple)):
+        return [six_digits(x) for x in v]
+    return v
+
+
+def result_lines(out):
+    """(the result's line, the details)."""
+    details = {k: out[k] for k in DETAILS if k in out}
+    line = {k: v for k, v in out.items() if k not in DETAILS}
+    if "per_config" in out.get("cpu_baseline", {}):
+        details["cpu_baseline"] = out["cpu_baseline"]
+        line["cpu_baseline"] = {k: v for k, v in out["cpu_baseline"].items()
+                                if not k.startswith("per_config")}
+    stacked = out.get("prefill", {}).get("stacked", {})
+    if stacked:
+        line["prefill_us"] = {name: {k: v["us"] for k, v in points.items()
+                                     if isinstance(v, dict) and "us" in v}
+                              for name, points in stacked.items() if isinstance(points, dict)}
+    return six_digits(line), six_digits(details)
+
+
 def ceiling_main():
     print(json.dumps(ceiling_points(torch.device("cuda", 0))))
     return 0
@@ -983,6 +1016,8 @@ def main():
                     help="identical-input replays per variant for the mismatch statistics")
     ap.add_argument("--profile-case", choices=["decode"] + sorted(PROFILE_CASES),
                     help="run a few calls of one kernel on a fixed workload (for ncu) and exit")
+    ap.add_argument("--details", metavar="FILE",
+                    help="write the tables that are too long for the line there")
     ap.add_argument("--ceiling", action="store_true",
                     help="time a plain device copy of each workload's byte count and exit")
     args = ap.parse_args()
@@ -1254,7 +1289,11 @@ def main():
                    "on distinct buffers back to back in one CUDA graph"}
         out["same_bytes_ceiling"] = ceil
         out["cpu_baseline"] = cpu_baseline_obj(args.cpu_seconds, args.cpu_config_seconds)
-        print(json.dumps(out))
+        line, details = result_lines(out)
+        if args.details:
+            with open(args.details, "w") as f:
+                json.dump(details, f, indent=1)
+        print(json.dumps(line))
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
