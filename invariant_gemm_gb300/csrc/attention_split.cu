@@ -25,7 +25,7 @@
 // Online softmax in base 2 with whole exponents: a row's m is raised only when a
 // logit passes m + 7, to the next whole number, so that every rescaling is by
 // an exact power of two and most steps have none. A value's scale is part of its logit
-// there ("a row's sums" in attention.cuh). p stays below 2^15; as FP16 it has 11 bits down
+// there ("a row's sums" in attention.cuh). p is 2^15 at most; as FP16 it has 11 bits down
 // to 2^-14. The sum of p is FP32.
 //
 // The K order of both products is free, and so is the M order of the second, so
