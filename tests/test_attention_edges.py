@@ -241,3 +241,21 @@ def test_where_parts_grow(kv):
     b = Batch([(1, kv), (2, kv - 5)], 4, 1, 64, 128, seed=kv).fill()
     q = b.rows(4, 2.0)
     b.check(q, b.attend(q))
+
+
+@pytest.mark.parametrize("lengths", [[(1, 3000)] * 20 + [(0, 40)] + [(5, 2000)] * 7,
+                                     [(1, 900)] * 15 + [(100, 2500), (0, 0), (300, 900), (70, 3000)],
+                                     [(66, 2000)] * 9 + [(1, 1500)] * 9])
+def test_parts_placed_by_rows(lengths):
+    """With no bound on new tokens a sequence's parts are where its rows begin, not where its
+    number says: the same bits, and nothing written behind the workspace."""
+    need_gpu()
+    b = Batch(lengths, 8, 2, 64, 32, seed=48).fill()
+    q = b.rows(8, 2.0).cuda()
+    args = b.device_args()
+    b.check(q, b.attend(q, args=args))
+    size = ig.attention_workspace(q, args[0], args[4], b.T).numel()
+    buf = torch.full((size + (1 << 20),), 0xab, dtype=torch.uint8, device="cuda")
+    buf[:size] = 0
+    got = b.attend(q, args=args, max_q=b.T, ws=buf[:size])
+    assert torch.equal(got, b.attend(q, args=args)) and (buf[size:] == 0xab).all()
